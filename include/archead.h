@@ -20,7 +20,7 @@
  *    _host variants.
  *  - Return value: ARCHEAD_OK (0) or a negative ARCHEAD_ERR_* code.  Argument errors are
  *    detected on the host before anything is enqueued.  Errors detected by a kernel
- *    (ARCHEAD_ERR_RANGE_H, ARCHEAD_ERR_TARGET) set a per-device error word; the affected
+ *    (ARCHEAD_ERR_RANGE_H, ARCHEAD_ERR_TARGET, ARCHEAD_ERR_SEGMENT) set a per-device error word; the affected
  *    outputs are non-finite; archead_check() reports and clears the word.
  *  - Temporary device memory (the N x (r_c + r_r) prologue product t, the FP16 image of H,
  *    the split-tile partials and counters, the NLL partials) is taken with
@@ -62,7 +62,8 @@ enum archead_status {
   ARCHEAD_ERR_TIMEOUT = -6,     /* a bounded device wait gave up                      */
   ARCHEAD_ERR_CUDA = -7,        /* a CUDA runtime call or launch failed               */
   ARCHEAD_ERR_UNSUPPORTED = -8, /* no kernel for this device / configuration          */
-  ARCHEAD_ERR_NOMEM = -9        /* stream-ordered allocation failed                   */
+  ARCHEAD_ERR_NOMEM = -9,       /* stream-ordered allocation failed                   */
+  ARCHEAD_ERR_SEGMENT = -10     /* sequence offsets or pair indices out of range      */
 };
 
 /* Storage formats of a head (archead_head.format). */
@@ -142,6 +143,109 @@ int archead_logits(const uint16_t* H, const archead_head* head, float* Y, int64_
 int archead_nll(const uint16_t* H, const archead_head* head, const int32_t* targets,
                 float* nll_out, int64_t N, int64_t V, int64_t D, int r_c, int r_r, int g,
                 void* stream);
+
+/*
+ * archead_nll_lse -- archead_nll that also writes every token's log-sum-exp:
+ *   lse_out[n] = logsumexp_v Y[n, v] (float N, device).  nll_out is what archead_nll gives,
+ *   bit for bit.  The pair is what archead_nll_grad takes.
+ */
+int archead_nll_lse(const uint16_t* H, const archead_head* head, const int32_t* targets,
+                    float* nll_out, float* lse_out, int64_t N, int64_t V, int64_t D, int r_c,
+                    int r_r, int g, void* stream);
+
+/*
+ * archead_nll_grad -- the gradient of a loss on the per-token NLLs with respect to the hidden
+ *   states, through the packed head (which stays frozen):
+ *     dH[n, :] = dnll[n] sum_v (exp(Y[n, v] - lse[n]) - [v = targets[n]]) W[v, :],
+ *   W = W_d + A_w B_w and Y = H W^T, evaluated again from the packed head.
+ *   nll, lse float N (device): what archead_nll_lse gave for the same H, head and targets.
+ *   dnll float N (device): the loss's derivative by each token's NLL.  dH bf16 N x D (device,
+ *   16-byte aligned, fully overwritten).
+ *   A token with dnll[n] = 0 (a masked one) gets a row of zeros whatever its other inputs
+ *   hold, and its target may be any value; H must be finite in every row
+ *   (ARCHEAD_ERR_RANGE_H).  A target outside [0, V) of another token sets
+ *   ARCHEAD_ERR_TARGET and makes its row NaN.
+ *   The tokens are taken in chunks that bound the scratch memory (about 2 GB).  Equal calls
+ *   give equal bits.  Asynchronous on `stream`.
+ */
+int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t* targets,
+                     const float* nll, const float* lse, const float* dnll, uint16_t* dH,
+                     int64_t N, int64_t V, int64_t D, int r_c, int r_r, int g, void* stream);
+
+/*
+ * archead_logits_grad -- dH = dY W: the gradient with respect to the hidden states of a loss
+ *   whose gradient by the logits is dY (float N x V, device, 4-byte aligned), W as above.
+ *   dH bf16 N x D (device, 16-byte aligned, fully overwritten).  A non-finite entry of dY
+ *   makes its own token's row non-finite and no other.  Asynchronous on `stream`.
+ */
+int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH, int64_t N,
+                        int64_t V, int64_t D, int r_c, int r_r, int g, void* stream);
+
+/* How archead_policy_loss takes the mean of its per-token losses l under the weights w. */
+enum archead_reduction {
+  ARCHEAD_REDUCE_TOKEN = 0,    /* sum w l / sum w                                          */
+  ARCHEAD_REDUCE_SEQUENCE = 1, /* mean, over the sequences with sum w > 0, of their own    */
+                               /* sum w l / sum w                                          */
+  ARCHEAD_REDUCE_SUM = 2       /* sum w l                                                  */
+};
+
+/*
+ * archead_policy_loss -- clipped policy loss with a KL term on per-token NLLs, and its
+ *   gradient.  With the log-probabilities -nll (of the tokens under the policy), -nll_old
+ *   (under the policy that sampled them) and -nll_ref (under a fixed reference policy):
+ *     r = exp(nll_old - nll),  z = nll - nll_ref,
+ *     l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(z) - z - 1).
+ *   nll, nll_old float N; nll_ref float N or NULL (no KL term); weights float N or NULL (all
+ *   1), not negative; cu_seqlens int32 B + 1 or NULL: sequence i is the tokens
+ *   [cu_seqlens[i], cu_seqlens[i + 1]); advantages A float N, or float B with adv_per_seq
+ *   (which needs cu_seqlens, as ARCHEAD_REDUCE_SEQUENCE does).  All on the device.
+ *   dnll float N (device): the loss's derivative by each token's NLL; where the clipped side
+ *   is the smaller one the surrogate's derivative is 0 (at the border itself it is not).
+ *   stats float 4 (device): the loss, the surrogate's and the KL term's (before kl_coef)
+ *   shares of it, and the share of the weight whose surrogate is clipped, all reduced alike.
+ *   A token with weight 0, or outside every sequence, is masked: nothing else of it is used
+ *   (it may hold NaN) and its dnll is 0.  Where no token counts, loss and gradient are 0.
+ *   Offsets that fall or leave [0, N] set ARCHEAD_ERR_SEGMENT (each is then taken at the
+ *   nearest allowed value).  0 <= clip_low < 1, clip_high >= 0, kl_coef finite; B < 2^31 - 1.
+ *   Sums are held in FP64 and in a fixed order: equal calls give equal bits.  N = 0 writes
+ *   stats alone.  Asynchronous on `stream`.
+ */
+int archead_policy_loss(const float* nll, const float* nll_old, const float* nll_ref,
+                        const float* advantages, const float* weights,
+                        const int32_t* cu_seqlens, float* dnll, float* stats, int64_t N,
+                        int64_t B, int adv_per_seq, double clip_low, double clip_high,
+                        double kl_coef, int reduction, void* stream);
+
+/* The loss of archead_preference_loss on a pair's margin. */
+enum archead_preference {
+  ARCHEAD_PREF_SIGMOID = 0, /* -(1 - s) log sigma(m) - s log sigma(-m), s = label_smoothing */
+  ARCHEAD_PREF_HINGE = 1,   /* max(0, 1 - m)                                               */
+  ARCHEAD_PREF_IPO = 2      /* (f_a - f_b - margin - 1 / (2 beta))^2                       */
+};
+
+/*
+ * archead_preference_loss -- loss of preference pairs on per-token NLLs, and its gradient.
+ *   Sequence i (tokens [cu_seqlens[i], cu_seqlens[i + 1]), int32 B + 1) scores
+ *     f_i = sum_t w_t (nll_ref[t] - nll[t]), its log-probability ratio to the reference,
+ *   divided by sum_t w_t with `average` (0 where that sum is 0).  A pair (a, b) = pairs[p]
+ *   (int32 P x 2: a preferred to b) has the margin m = beta (f_a - f_b) - margin and the loss
+ *   its kind gives; the result is the mean over the pairs (0 for P = 0).
+ *   nll float N; nll_ref float N or NULL (taken as 0: no reference); weights float N or NULL.
+ *   A sequence may be in any number of pairs, also on both sides of one.
+ *   dnll float N: the loss's derivative by each token's NLL (0 for weight 0 and outside every
+ *   sequence, whatever else such a token holds); loss float 1; pair_loss float P; rewards
+ *   float P x 2: beta f_a, beta f_b.  All pointers on the device.
+ *   A pair index outside [0, B) sets ARCHEAD_ERR_SEGMENT; that pair's loss and rewards and
+ *   the mean loss are NaN and it adds nothing to dnll.  Offsets as in archead_policy_loss.
+ *   label_smoothing in [0, 1) (0 unless the kind is sigmoid), beta > 0, margin finite.
+ *   Sums are held in FP64 and in a fixed order: equal calls give equal bits.
+ *   Asynchronous on `stream`.
+ */
+int archead_preference_loss(const float* nll, const float* nll_ref, const float* weights,
+                            const int32_t* cu_seqlens, const int32_t* pairs, float* dnll,
+                            float* loss, float* pair_loss, float* rewards, int64_t N, int64_t B,
+                            int64_t P, int kind, int average, double beta,
+                            double label_smoothing, double margin, void* stream);
 
 /*
  * archead_agreement -- how closely the packed head's next-token distribution follows a
@@ -247,8 +351,8 @@ int archead_dequant(const archead_head* head, int64_t row0, int64_t nrows, float
 
 /*
  * archead_check -- synchronises `stream`, then reads and clears this device's error
- * word.  Returns ARCHEAD_OK, ARCHEAD_ERR_RANGE_H, ARCHEAD_ERR_TARGET, ARCHEAD_ERR_TIMEOUT
- * or ARCHEAD_ERR_CUDA (a pending CUDA error).
+ * word.  Returns ARCHEAD_OK, ARCHEAD_ERR_RANGE_H, ARCHEAD_ERR_TARGET, ARCHEAD_ERR_SEGMENT,
+ * ARCHEAD_ERR_TIMEOUT or ARCHEAD_ERR_CUDA (a pending CUDA error).
  */
 int archead_check(void* stream);
 

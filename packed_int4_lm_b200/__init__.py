@@ -9,6 +9,12 @@ point without the built library raises.
     dh    = DeviceHead.from_canonical(head, "cuda")             # upload + repack
     Y     = logits(H_bf16, dh)                                  # N x V float32
     nlls  = nll(H_bf16, dh, targets)                            # N float32, no logits
+
+and, to train what feeds the (frozen) head:
+
+    nlls, lse = nll_lse(H_bf16, dh, targets)                    # forward
+    out = policy_loss(nlls, nlls_old, advantages)               # or preference_loss(...)
+    dH  = nll_grad(H_bf16, dh, targets, nlls, lse, out["dnll"]) # N x D bf16: H.backward(dH)
 """
 from __future__ import annotations
 
@@ -21,7 +27,8 @@ import torch
 from . import _lib, pack
 from ._lib import ArcheadError, ArcheadHead
 
-__all__ = ["DeviceHead", "logits", "nll", "agreement", "logits_host", "nll_host", "dequant", "check",
+__all__ = ["DeviceHead", "logits", "nll", "nll_lse", "nll_grad", "logits_grad", "policy_loss",
+           "preference_loss", "agreement", "logits_host", "nll_host", "dequant", "check",
            "last_launches", "profile", "profile_read", "ArcheadError", "pack"]
 
 _KEYS = ("r_nib", "r_code", "r_super", "Ac", "sAc", "Bc", "sBc", "Aw", "sAw", "Bw", "sBw")
@@ -208,6 +215,193 @@ def agreement(H: torch.Tensor, dh: DeviceHead, Y_dense: torch.Tensor, k: int = 1
         *[out[x].data_ptr() if N else None for x in ("topk", "top1_dense", "kl", "lse")],
         N, *dh.shape_args, _stream_handle(stream)), "archead_agreement")
     return out
+
+
+def _float_arrays(N: int, dev, **arrays):
+    """Checks that each given array is a contiguous float32 CUDA tensor of shape (N,) on dev."""
+    for name, t in arrays.items():
+        if t is not None and (t.dtype != torch.float32 or t.shape != (N,) or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({N},) on {dev}")
+
+
+def _int_array(name: str, t: torch.Tensor, shape, dev):
+    if (t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != dev
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
+
+
+def _optional(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+class _Call:
+    """The device and stream of one call: the tensors' device is made current around the C call
+    (the library works on the current device), the stream is the given one or that device's
+    current one, and tensors used on a stream other than that one are recorded on it."""
+
+    __slots__ = ("dev", "stream", "handle", "prev")
+
+    def __init__(self, dev: torch.device, stream):
+        self.dev, self.stream = dev, stream
+        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def run(self, name: str, *args, tensors=()):
+        prev = torch.cuda.current_device()
+        if prev != self.dev.index:
+            torch.cuda.set_device(self.dev)
+        try:
+            status = getattr(_lib.lib(), name)(*args, self.handle)
+        finally:
+            if prev != self.dev.index:
+                torch.cuda.set_device(prev)
+        _lib.check(status, name)
+        if self.stream is not None and self.handle != torch.cuda.current_stream(self.dev).cuda_stream:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _head_on(dh: DeviceHead, dev: torch.device):
+    if dh.tensors["r_nib"].device != dev:
+        raise ValueError(f"the head is on {dh.tensors['r_nib'].device}, the inputs are on {dev}")
+
+
+def _grad_out(out: Optional[torch.Tensor], N: int, dh: DeviceHead, dev) -> torch.Tensor:
+    if out is None:
+        return torch.empty(N, dh.D, device=dev, dtype=torch.bfloat16)
+    if (out.dtype != torch.bfloat16 or tuple(out.shape) != (N, dh.D) or out.device != dev
+            or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous bf16 tensor of shape ({N}, {dh.D}) on {dev}")
+    return out
+
+
+def nll_lse(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, stream=None):
+    """The per-token NLL, as nll gives it, and log-sum-exp of the logits (N float32 each):
+    what nll_grad takes."""
+    _check_H(H, dh)
+    N, dev = H.shape[0], H.device
+    _head_on(dh, dev)
+    _int_array("targets", targets, (N,), dev)
+    out = torch.empty(N, device=dev, dtype=torch.float32)
+    lse = torch.empty(N, device=dev, dtype=torch.float32)
+    _Call(dev, stream).run("archead_nll_lse", H.data_ptr(), ctypes.byref(dh.struct),
+                           targets.data_ptr(), out.data_ptr(), lse.data_ptr(), N, *dh.shape_args,
+                           tensors=(H, targets, out, lse))
+    return out, lse
+
+
+def nll_grad(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, nll: torch.Tensor,
+             lse: torch.Tensor, dnll: torch.Tensor, out: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """dH (N x D bf16): the gradient by the hidden states of a loss whose gradient by the
+    per-token NLLs is dnll (N float32), through the packed head.  nll, lse: from nll_lse on the
+    same H, head and targets.  Tokens with dnll = 0 are masked: their rows are zero, whatever
+    their target."""
+    _check_H(H, dh)
+    N, dev = H.shape[0], H.device
+    _head_on(dh, dev)
+    _int_array("targets", targets, (N,), dev)
+    _float_arrays(N, dev, nll=nll, lse=lse, dnll=dnll)
+    out = _grad_out(out, N, dh, dev)
+    _Call(dev, stream).run("archead_nll_grad", H.data_ptr(), ctypes.byref(dh.struct),
+                           targets.data_ptr(), nll.data_ptr(), lse.data_ptr(), dnll.data_ptr(),
+                           out.data_ptr(), N, *dh.shape_args,
+                           tensors=(H, targets, nll, lse, dnll, out))
+    return out
+
+
+def logits_grad(dY: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """dH = dY W (N x D bf16): the gradient by the hidden states of a loss whose gradient by the
+    logits is dY (N x V float32), through the packed head."""
+    if (dY.dtype != torch.float32 or dY.dim() != 2 or dY.shape[1] != dh.V or not dY.is_cuda
+            or not dY.is_contiguous()):
+        raise ValueError(f"dY must be a contiguous float32 CUDA tensor of shape (N, {dh.V})")
+    N, dev = dY.shape[0], dY.device
+    _head_on(dh, dev)
+    out = _grad_out(out, N, dh, dev)
+    _Call(dev, stream).run("archead_logits_grad", dY.data_ptr(), ctypes.byref(dh.struct),
+                           out.data_ptr(), N, *dh.shape_args, tensors=(dY, out))
+    return out
+
+
+REDUCTIONS = {"token": 0, "sequence": 1, "sum": 2}        # archead_reduction
+PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}        # archead_preference
+
+
+def _loss_inputs(nll: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):
+    if nll.dim() != 1 or not nll.is_cuda:
+        raise ValueError("nll must be a float32 CUDA tensor of shape (N,)")
+    N, dev = nll.shape[0], nll.device
+    B = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must hold B + 1 offsets")
+        B = cu_seqlens.shape[0] - 1
+        _int_array("cu_seqlens", cu_seqlens, (B + 1,), dev)
+    return N, B, dev
+
+
+def policy_loss(nll: torch.Tensor, nll_old: torch.Tensor, advantages: torch.Tensor, *,
+                nll_ref: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None, per_sequence: bool = False,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                reduction: str = "token", stream=None) -> dict:
+    """archead_policy_loss: the clipped policy loss with a KL term on per-token NLLs (N float32
+    each) and its gradient.  advantages: one per token, or with per_sequence one per sequence
+    of cu_seqlens (B + 1 int32 offsets).  weights: 0 masks a token.  reduction: "token",
+    "sequence" (needs cu_seqlens) or "sum".  Returns "stats" (4 float32: loss, surrogate, KL
+    term, clipped share) and "dnll" (N float32, for nll_grad)."""
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
+    N, B, dev = _loss_inputs(nll, cu_seqlens)
+    if cu_seqlens is None and (per_sequence or reduction == "sequence"):
+        raise ValueError("per_sequence advantages and the sequence reduction need cu_seqlens")
+    _float_arrays(N, dev, nll=nll, nll_old=nll_old, nll_ref=nll_ref, weights=weights)
+    _float_arrays(B if per_sequence else N, dev, advantages=advantages)
+    dnll = torch.empty(N, device=dev, dtype=torch.float32)
+    stats = torch.empty(4, device=dev, dtype=torch.float32)
+    _Call(dev, stream).run(
+        "archead_policy_loss", nll.data_ptr(), nll_old.data_ptr(), _optional(nll_ref),
+        advantages.data_ptr(), _optional(weights), _optional(cu_seqlens), dnll.data_ptr(),
+        stats.data_ptr(), N, B, int(per_sequence), clip_low, clip_high, kl_coef,
+        REDUCTIONS[reduction],
+        tensors=(nll, nll_old, nll_ref, advantages, weights, cu_seqlens, dnll, stats))
+    return {"stats": stats, "dnll": dnll}
+
+
+def preference_loss(nll: torch.Tensor, cu_seqlens: torch.Tensor, pairs: torch.Tensor, *,
+                    nll_ref: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, beta: float = 0.1,
+                    kind: str = "sigmoid", label_smoothing: float = 0.0, margin: float = 0.0,
+                    average: bool = False, stream=None) -> dict:
+    """archead_preference_loss: the loss of preference pairs (P x 2 int32 sequence indices, the
+    preferred one first) on per-token NLLs (N float32) of the sequences of cu_seqlens, and its
+    gradient.  kind: "sigmoid", "hinge" or "ipo"; average: scores per weighted token.  Returns
+    "loss" (1 float32, the mean), "pair_loss" (P), "rewards" (P x 2) and "dnll" (N, for
+    nll_grad)."""
+    if kind not in PREFERENCES:
+        raise ValueError(f"kind must be one of {sorted(PREFERENCES)}, got {kind!r}")
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens must hold B + 1 offsets")
+    N, B, dev = _loss_inputs(nll, cu_seqlens)
+    _float_arrays(N, dev, nll=nll, nll_ref=nll_ref, weights=weights)
+    if pairs.dim() != 2:
+        raise ValueError("pairs must be an int32 tensor of shape (P, 2)")
+    P = pairs.shape[0]
+    _int_array("pairs", pairs, (P, 2), dev)
+    dnll = torch.empty(N, device=dev, dtype=torch.float32)
+    loss = torch.empty(1, device=dev, dtype=torch.float32)
+    pair_loss = torch.empty(P, device=dev, dtype=torch.float32)
+    rewards = torch.empty(P, 2, device=dev, dtype=torch.float32)
+    _Call(dev, stream).run(
+        "archead_preference_loss", nll.data_ptr(), _optional(nll_ref), _optional(weights),
+        cu_seqlens.data_ptr(), pairs.data_ptr(), dnll.data_ptr(), loss.data_ptr(),
+        pair_loss.data_ptr(), rewards.data_ptr(), N, B, P, PREFERENCES[kind], int(average), beta,
+        label_smoothing, margin,
+        tensors=(nll, nll_ref, weights, cu_seqlens, pairs, dnll, loss, pair_loss, rewards))
+    return {"loss": loss, "pair_loss": pair_loss, "rewards": rewards, "dnll": dnll}
 
 
 def logits_host(H: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = None,

@@ -11,13 +11,14 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "archead.h")
 
 c_i64 = ctypes.c_int64
 c_int = ctypes.c_int
+c_double = ctypes.c_double
 c_vp = ctypes.c_void_p
 
 STATUS = {
     0: "ARCHEAD_OK", -1: "ARCHEAD_ERR_NULLPTR", -2: "ARCHEAD_ERR_ALIGN",
     -3: "ARCHEAD_ERR_SHAPE", -4: "ARCHEAD_ERR_RANGE_H", -5: "ARCHEAD_ERR_TARGET",
     -6: "ARCHEAD_ERR_TIMEOUT", -7: "ARCHEAD_ERR_CUDA", -8: "ARCHEAD_ERR_UNSUPPORTED",
-    -9: "ARCHEAD_ERR_NOMEM",
+    -9: "ARCHEAD_ERR_NOMEM", -10: "ARCHEAD_ERR_SEGMENT",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -57,6 +58,16 @@ _SIGS = {
     "archead_nll_merge": (c_int, [c_vp, c_int, c_i64, c_vp, c_vp]),
     "archead_agreement": (c_int, [c_vp, ctypes.POINTER(ArcheadHead), c_vp, c_int, c_vp, c_vp,
                                   c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_vp]),
+    "archead_nll_lse": (c_int, [c_vp, ctypes.POINTER(ArcheadHead), c_vp, c_vp, c_vp, c_i64,
+                                c_i64, c_i64, c_int, c_int, c_int, c_vp]),
+    "archead_nll_grad": (c_int, [c_vp, ctypes.POINTER(ArcheadHead), c_vp, c_vp, c_vp, c_vp, c_vp,
+                                 c_i64, c_i64, c_i64, c_int, c_int, c_int, c_vp]),
+    "archead_logits_grad": (c_int, [c_vp, ctypes.POINTER(ArcheadHead), c_vp, c_i64, c_i64, c_i64,
+                                    c_int, c_int, c_int, c_vp]),
+    "archead_policy_loss": (c_int, [c_vp] * 8 + [c_i64, c_i64, c_int, c_double, c_double,
+                                                 c_double, c_int, c_vp]),
+    "archead_preference_loss": (c_int, [c_vp] * 9 + [c_i64, c_i64, c_i64, c_int, c_int, c_double,
+                                                     c_double, c_double, c_vp]),
     "archead_profile": (c_int, [c_int]),
     "archead_test_hooks": (c_int, [ctypes.c_longlong, c_int]),
     "archead_profile_read": (c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)]),

@@ -179,7 +179,7 @@ struct NllShard {
 
 int run_dec(const uint16_t* H, const archead_head* head, float* Y, const int32_t* targets,
             float* nll, const Shapes& s, const DecPlan& pl, DeviceState* ds, cudaStream_t st,
-            const NllShard* shard) {
+            const NllShard* shard, float* lse) {
   int launches = 0;
   const int RR = s.r_c + s.r_r;
   const bool nll_mode = nll != nullptr || shard != nullptr;
@@ -219,7 +219,7 @@ int run_dec(const uint16_t* H, const archead_head* head, float* Y, const int32_t
     prof_mark(1, st);
     if (e == cudaSuccess && nll_mode)
       e = shard ? launch_nll_partials(part, tl, s, shard->partials, st, &launches)
-                : launch_nll_combine(part, tl, targets, s, nll, ds->err, st, &launches);
+                : launch_nll_combine(part, tl, targets, s, nll, lse, ds->err, st, &launches);
   }
   cudaFreeAsync(base, st);
   if (e != cudaSuccess) return ARCHEAD_ERR_CUDA;
@@ -228,7 +228,8 @@ int run_dec(const uint16_t* H, const archead_head* head, float* Y, const int32_t
 }
 
 int run(const uint16_t* H, const archead_head* head, float* Y, const int32_t* targets,
-        float* nll, const Shapes& s, cudaStream_t st, const NllShard* shard = nullptr) {
+        float* nll, const Shapes& s, cudaStream_t st, const NllShard* shard = nullptr,
+        float* lse = nullptr) {
   DeviceState* ds;
   int rc = current_state(&ds);
   if (rc) return rc;
@@ -242,7 +243,7 @@ int run(const uint16_t* H, const archead_head* head, float* Y, const int32_t* ta
   // Row INT8 heads run on the token-block warp-MMA kernel only
   const bool row8 = head->format == ARCHEAD_FMT_ROW8;
   const DecPlan dplan = row8 ? DecPlan{0, 0, 0} : dec_plan(s, nll_mode);
-  if (dplan.nt8 > 0) return run_dec(H, head, Y, targets, nll, s, dplan, ds, st, shard);
+  if (dplan.nt8 > 0) return run_dec(H, head, Y, targets, nll, s, dplan, ds, st, shard, lse);
   const TcPlan plan = s.N > 8 && !row8 ? tc_plan(s, nll_mode) : TcPlan{0, 0, 0, 0};
   const bool use_tc = plan.nt > 0;
   const int64_t tb = use_tc ? plan.nt : residual_token_block(s.N);
@@ -291,7 +292,7 @@ int run(const uint16_t* H, const archead_head* head, float* Y, const int32_t* ta
       prof_mark(1, st);
       if (e == cudaSuccess && nll_mode)
         e = shard ? launch_nll_partials(part, tl, s, shard->partials, st, &launches)
-                  : launch_nll_combine(part, tl, targets, s, nll, ds->err, st, &launches);
+                  : launch_nll_combine(part, tl, targets, s, nll, lse, ds->err, st, &launches);
     } else if (!nll_mode) {
       prof_mark(0, st);
       e = launch_residual_gemm(Hh, t, tsc, head, s, Y, nullptr, nullptr, nullptr, st, &launches, 0);
@@ -304,7 +305,7 @@ int run(const uint16_t* H, const archead_head* head, float* Y, const int32_t* ta
       prof_mark(1, st);
       if (e == cudaSuccess)
         e = shard ? launch_nll_partials(part, tl, s, shard->partials, st, &launches)
-                  : launch_nll_combine(part, tl, targets, s, nll, ds->err, st, &launches);
+                  : launch_nll_combine(part, tl, targets, s, nll, lse, ds->err, st, &launches);
     }
   }
   cudaFreeAsync(base, st);
@@ -320,6 +321,21 @@ int validate_head_args(const archead_head* head, int64_t N, int64_t V, int64_t D
                        int r_r, int g) {
   return check_head(head, N, V, D, r_c, r_r, g);
 }
+
+int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err) {
+  DeviceState* ds;
+  const int rc = current_state(&ds);
+  if (rc) return rc;
+  *err = ds->err;
+  *base = nullptr;
+  if (bytes && cudaMallocFromPoolAsync(base, bytes, ds->pool, st) != cudaSuccess) {
+    cudaGetLastError();
+    return ARCHEAD_ERR_NOMEM;
+  }
+  return ARCHEAD_OK;
+}
+
+void set_last_launches(int n) { t_last_launches = n; }
 
 // Device address of this device's error word (the device must be current).
 unsigned* error_word_address() {
@@ -350,6 +366,7 @@ const char* archead_strerror(int status) {
     case ARCHEAD_ERR_TIMEOUT: return "a bounded device wait gave up";
     case ARCHEAD_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";
     case ARCHEAD_ERR_UNSUPPORTED: return "unsupported device or configuration";
+    case ARCHEAD_ERR_SEGMENT: return "sequence offsets or pair indices are out of range";
     case ARCHEAD_ERR_NOMEM: return "stream-ordered device allocation failed";
     default: return "unknown status";
   }
@@ -382,6 +399,22 @@ int archead_nll(const uint16_t* H, const archead_head* head, const int32_t* targ
   if (!aligned(H, 16) || !aligned(targets, 4) || !aligned(nll_out, 4)) return ARCHEAD_ERR_ALIGN;
   return run(H, head, nullptr, targets, nll_out, make_shapes(N, V, D, r_c, r_r, g),
              static_cast<cudaStream_t>(stream));
+}
+
+int archead_nll_lse(const uint16_t* H, const archead_head* head, const int32_t* targets,
+                    float* nll_out, float* lse_out, int64_t N, int64_t V, int64_t D, int r_c,
+                    int r_r, int g, void* stream) {
+  int rc = check_head(head, N, V, D, r_c, r_r, g);
+  if (rc) return rc;
+  if (N == 0) {
+    t_last_launches = 0;
+    return ARCHEAD_OK;
+  }
+  if (!H || !targets || !nll_out || !lse_out) return ARCHEAD_ERR_NULLPTR;
+  if (!aligned(H, 16) || !aligned(targets, 4) || !aligned(nll_out, 4) || !aligned(lse_out, 4))
+    return ARCHEAD_ERR_ALIGN;
+  return run(H, head, nullptr, targets, nll_out, make_shapes(N, V, D, r_c, r_r, g),
+             static_cast<cudaStream_t>(stream), nullptr, lse_out);
 }
 
 int archead_nll_partials(const uint16_t* H, const archead_head* head, const int32_t* targets,
@@ -654,6 +687,7 @@ int archead_check(void* stream) {
   if (cudaGetLastError() != cudaSuccess) return ARCHEAD_ERR_CUDA;
   if (w & kErrRangeH) return ARCHEAD_ERR_RANGE_H;
   if (w & kErrTarget) return ARCHEAD_ERR_TARGET;
+  if (w & kErrSegment) return ARCHEAD_ERR_SEGMENT;
   if (w & kErrTimeout) return ARCHEAD_ERR_TIMEOUT;
   return ARCHEAD_OK;
 }

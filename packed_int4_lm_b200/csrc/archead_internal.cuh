@@ -15,6 +15,7 @@ enum : unsigned {
   kErrRangeH = 1u,
   kErrTarget = 2u,
   kErrTimeout = 4u,
+  kErrSegment = 8u,
 };
 
 // ---------------------------------------------------------------------------------
@@ -255,9 +256,10 @@ cudaError_t launch_agreement(const __half* Hh, const float* t, const float* tsc,
                              float* kl_out, float* lse_out, cudaStream_t st, int* launches);
 int64_t residual_token_block(int64_t N);  // rows of the zero-padded FP16 copy of H
 
-// nll[n] from the partials; a target outside [0, V) gives NaN and sets kErrTarget.
+// nll[n] (and, unless lse is nullptr, the log-sum-exp) from the partials; a target outside
+// [0, V) gives NaN and sets kErrTarget.
 cudaError_t launch_nll_combine(const float2* part, const float* tlogit,
-                               const int32_t* targets, const Shapes& s, float* nll,
+                               const int32_t* targets, const Shapes& s, float* nll, float* lse,
                                unsigned* err, cudaStream_t st, int* launches);
 
 // Vocabulary-parallel NLL (csrc/nll_shard.cu).  A shard holds rows [v_begin, v_begin + V)
@@ -276,7 +278,48 @@ cudaError_t launch_nll_merge(const float* partials, int G, int64_t N, float* nll
 cudaError_t launch_repack(const uint8_t* canon, uint8_t* dev, int64_t V, int64_t D,
                           cudaStream_t st);
 
+// Gradient product dH = dY W through the packed head (csrc/head_grad.cu): dY float n x V,
+// dH bf16 n x D, each row multiplied by rowscale[n] (nullptr: 1; a row whose scale is 0 is
+// written as zeros).  scratch: head_grad_scratch_bytes.
+size_t head_grad_scratch_bytes(const archead_head* head, int64_t n);
+cudaError_t launch_head_grad(const float* dY, const archead_head* head, int64_t n,
+                             const float* rowscale, uint16_t* dH, void* scratch,
+                             cudaStream_t st, int* launches);
+// In place: Y[n, v] -> exp(Y[n, v] - lse[n]) - [v = targets[n]], with the target's entry
+// taken from its NLL (exp(-nll) - 1).
+cudaError_t launch_softmax_grad(float* Y, const int32_t* targets, const float* nll,
+                                const float* lse, const float* dnll, int64_t n, int64_t V,
+                                unsigned* err, cudaStream_t st, int* launches);
+
+// Losses on per-token NLLs (csrc/losses.cu).
+struct PolicyArgs {
+  const float *nll, *nll_old, *nll_ref, *adv, *w;
+  const int32_t* cu;
+  float *dnll, *stats;
+  int64_t N, B;
+  int adv_per_seq, reduction;
+  double clip_low, clip_high, kl_coef;
+};
+size_t policy_scratch_bytes(const PolicyArgs& a);
+cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err,
+                               cudaStream_t st, int* launches);
+struct PreferenceArgs {
+  const float *nll, *nll_ref, *w;
+  const int32_t *cu, *pairs;
+  float *dnll, *loss, *pair_loss, *rewards;
+  int64_t N, B, P;
+  int kind, average;
+  double beta, smoothing, margin;
+};
+size_t preference_scratch_bytes(const PreferenceArgs& a);
+cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsigned* err,
+                                   cudaStream_t st, int* launches);
+
 // Host helpers defined in archead_api.cu.
+// The current device's error word and `bytes` of stream-ordered scratch from the library's
+// pool (none for 0 bytes); freed with cudaFreeAsync on the same stream.
+int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err);
+void set_last_launches(int n);
 int validate_head_args(const archead_head* head, int64_t N, int64_t V, int64_t D, int r_c,
                        int r_r, int g);
 unsigned* error_word_address();

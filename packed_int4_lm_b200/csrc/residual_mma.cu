@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(256) nll_combine_kernel(const float2* __restri
                                                           const int32_t* __restrict__ targets,
                                                           int64_t N, int64_t V, int nvblk,
                                                           float* __restrict__ nll,
+                                                          float* __restrict__ lse,
                                                           unsigned* err) {
   const int lane = threadIdx.x & 31;
   const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(256) nll_combine_kernel(const float2* __restri
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) {
+    if (lse) lse[n] = m + logf(s);
     const int32_t tg = targets[n];
     if (tg < 0 || (int64_t)tg >= V) {
       nll[n] = __int_as_float(0x7fc00000);
@@ -788,11 +790,11 @@ cudaError_t launch_agreement(const __half* Hh, const float* t, const float* tsc,
 }
 
 cudaError_t launch_nll_combine(const float2* part, const float* tlogit,
-                               const int32_t* targets, const Shapes& s, float* nll,
+                               const int32_t* targets, const Shapes& s, float* nll, float* lse,
                                unsigned* err, cudaStream_t st, int* launches) {
   const int nvblk = residual_gemm_vblocks(s);
   nll_combine_kernel<<<(unsigned)((s.N + 7) / 8), 256, 0, st>>>(part, tlogit, targets, s.N,
-                                                                 s.V, nvblk, nll, err);
+                                                                 s.V, nvblk, nll, lse, err);
   ++*launches;
   return cudaGetLastError();
 }

@@ -1,0 +1,154 @@
+// C ABI of the training operators (archead.h): the gradient of the per-token NLL and of the
+// logits through the packed head, and the losses on per-token NLLs.  Argument checks,
+// scratch and dispatch.
+#include <math.h>
+
+#include <algorithm>
+
+#include "archead_internal.cuh"
+
+using namespace archead;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Scratch of one chunk of archead_nll_grad: its logits, about 2 GB at most.
+constexpr int64_t kChunkBytes = 2ll << 30;
+
+int64_t grad_chunk(int64_t N, int64_t V) {
+  const int64_t c = std::max<int64_t>(kChunkBytes / (V * 4), 1);
+  return std::min(N, c >= 256 ? c / 256 * 256 : c);
+}
+
+// Runs `launch` with scratch of the given size; the common end of every entry point here.
+template <typename F>
+int with_scratch(size_t bytes, cudaStream_t st, F launch) {
+  void* base;
+  unsigned* err;
+  const int rc = take_scratch(bytes, st, &base, &err);
+  if (rc) return rc;
+  int launches = 0;
+  const cudaError_t e = launch(static_cast<char*>(base), err, &launches);
+  if (base) cudaFreeAsync(base, st);
+  if (e != cudaSuccess) return ARCHEAD_ERR_CUDA;
+  set_last_launches(launches);
+  return ARCHEAD_OK;
+}
+
+int check_tokens(const int32_t* cu, const float* const* f, int nf, int64_t N, int64_t B) {
+  if (N < 0 || N > 0x7fffffffLL || B < 0 || B >= 0x7fffffffLL) return ARCHEAD_ERR_SHAPE;
+  if (cu && !aligned(cu, 4)) return ARCHEAD_ERR_ALIGN;
+  for (int i = 0; i < nf; ++i)
+    if (f[i] && !aligned(f[i], 4)) return ARCHEAD_ERR_ALIGN;
+  return ARCHEAD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t* targets,
+                     const float* nll, const float* lse, const float* dnll, uint16_t* dH,
+                     int64_t N, int64_t V, int64_t D, int r_c, int r_r, int g, void* stream) {
+  int rc = validate_head_args(head, N, V, D, r_c, r_r, g);
+  if (rc) return rc;
+  if (N == 0) {
+    set_last_launches(0);
+    return ARCHEAD_OK;
+  }
+  if (!H || !targets || !nll || !lse || !dnll || !dH) return ARCHEAD_ERR_NULLPTR;
+  if (!aligned(H, 16) || !aligned(dH, 16) || !aligned(targets, 4) || !aligned(nll, 4) ||
+      !aligned(lse, 4) || !aligned(dnll, 4))
+    return ARCHEAD_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t chunk = grad_chunk(N, V);
+  const size_t yb = (size_t)chunk * V * 4, yoff = (yb + 255) / 256 * 256;
+  return with_scratch(yoff + head_grad_scratch_bytes(head, chunk), st,
+                      [&](char* b, unsigned* err, int* launches) {
+    float* Y = reinterpret_cast<float*>(b);
+    cudaError_t e = cudaSuccess;
+    for (int64_t n0 = 0; n0 < N && e == cudaSuccess; n0 += chunk) {
+      const int64_t n = std::min(chunk, N - n0);
+      if (archead_logits(H + n0 * D, head, Y, n, V, D, r_c, r_r, g, stream) != ARCHEAD_OK)
+        return cudaErrorUnknown;
+      *launches += archead_last_launches();
+      e = launch_softmax_grad(Y, targets + n0, nll + n0, lse + n0, dnll + n0, n, V, err, st,
+                              launches);
+      if (e == cudaSuccess)
+        e = launch_head_grad(Y, head, n, dnll + n0, dH + n0 * D, b + yoff, st, launches);
+    }
+    return e;
+  });
+}
+
+int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH, int64_t N,
+                        int64_t V, int64_t D, int r_c, int r_r, int g, void* stream) {
+  int rc = validate_head_args(head, N, V, D, r_c, r_r, g);
+  if (rc) return rc;
+  if (N == 0) {
+    set_last_launches(0);
+    return ARCHEAD_OK;
+  }
+  if (!dY || !dH) return ARCHEAD_ERR_NULLPTR;
+  if (!aligned(dY, 4) || !aligned(dH, 16)) return ARCHEAD_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_scratch(head_grad_scratch_bytes(head, N), st,
+                      [&](char* b, unsigned* err, int* launches) {
+    return launch_head_grad(dY, head, N, nullptr, dH, b, st, launches);
+  });
+}
+
+int archead_policy_loss(const float* nll, const float* nll_old, const float* nll_ref,
+                        const float* advantages, const float* weights,
+                        const int32_t* cu_seqlens, float* dnll, float* stats, int64_t N,
+                        int64_t B, int adv_per_seq, double clip_low, double clip_high,
+                        double kl_coef, int reduction, void* stream) {
+  const float* f[] = {nll, nll_old, nll_ref, advantages, weights, dnll, stats};
+  const int rc = check_tokens(cu_seqlens, f, 7, N, B);
+  if (rc) return rc;
+  if (reduction < ARCHEAD_REDUCE_TOKEN || reduction > ARCHEAD_REDUCE_SUM) return ARCHEAD_ERR_SHAPE;
+  if (!(clip_low >= 0.0 && clip_low < 1.0) || !(clip_high >= 0.0) || !isfinite(clip_high) ||
+      !isfinite(kl_coef))
+    return ARCHEAD_ERR_SHAPE;
+  if (!stats || ((adv_per_seq || reduction == ARCHEAD_REDUCE_SEQUENCE) && !cu_seqlens))
+    return ARCHEAD_ERR_NULLPTR;
+  if (N > 0 && (!nll || !nll_old || (!advantages && !(adv_per_seq && B == 0)) || !dnll))
+    return ARCHEAD_ERR_NULLPTR;
+  const PolicyArgs a = {nll, nll_old, nll_ref, advantages, weights, cu_seqlens, dnll, stats,
+                        N, B, adv_per_seq != 0, reduction, clip_low, clip_high,
+                        nll_ref ? kl_coef : 0.0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_scratch(policy_scratch_bytes(a), st, [&](char* b, unsigned* err, int* launches) {
+    return launch_policy_loss(a, b, err, st, launches);
+  });
+}
+
+int archead_preference_loss(const float* nll, const float* nll_ref, const float* weights,
+                            const int32_t* cu_seqlens, const int32_t* pairs, float* dnll,
+                            float* loss, float* pair_loss, float* rewards, int64_t N, int64_t B,
+                            int64_t P, int kind, int average, double beta,
+                            double label_smoothing, double margin, void* stream) {
+  const float* f[] = {nll, nll_ref, weights, dnll, loss, pair_loss, rewards};
+  const int rc = check_tokens(cu_seqlens, f, 7, N, B);
+  if (rc) return rc;
+  if (P < 0 || P > 0x7fffffffLL || kind < ARCHEAD_PREF_SIGMOID || kind > ARCHEAD_PREF_IPO)
+    return ARCHEAD_ERR_SHAPE;
+  if (!(beta > 0.0) || !isfinite(beta) || !isfinite(1.0 / beta) || !isfinite(margin) ||
+      !(label_smoothing >= 0.0 && label_smoothing < 1.0) ||
+      (kind != ARCHEAD_PREF_SIGMOID && label_smoothing != 0.0))
+    return ARCHEAD_ERR_SHAPE;
+  if (!cu_seqlens || !loss) return ARCHEAD_ERR_NULLPTR;
+  if (N > 0 && (!nll || !dnll)) return ARCHEAD_ERR_NULLPTR;
+  if (P > 0 && (!pairs || !pair_loss || !rewards)) return ARCHEAD_ERR_NULLPTR;
+  if (pairs && !aligned(pairs, 4)) return ARCHEAD_ERR_ALIGN;
+  const PreferenceArgs a = {nll, nll_ref, weights, cu_seqlens, pairs, dnll, loss, pair_loss,
+                            rewards, N, B, P, kind, average != 0, beta, label_smoothing, margin};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_scratch(preference_scratch_bytes(a), st,
+                      [&](char* b, unsigned* err, int* launches) {
+    return launch_preference_loss(a, b, err, st, launches);
+  });
+}
+
+}  // extern "C"
