@@ -278,18 +278,19 @@ cudaError_t launch_nll_merge(const float* partials, int G, int64_t N, float* nll
 cudaError_t launch_repack(const uint8_t* canon, uint8_t* dev, int64_t V, int64_t D,
                           cudaStream_t st);
 
-// Gradient product dH = dY W through the packed head (csrc/head_grad.cu): dY float n x V,
-// dH bf16 n x D, each row multiplied by rowscale[n] (nullptr: 1; a row whose scale is 0 is
-// written as zeros).  scratch: head_grad_scratch_bytes.
+// Gradient product dH = dY W through the packed head for n tokens (csrc/grad_tc.cu).  dY comes
+// as it is, or from logits as dY[n, v] = exp(Y[n, v] - lse[n]) - [v = targets[n]] with the
+// target's entry taken from its NLL (exp(-nll) - 1); row n of the product is multiplied by
+// dnll[n] (nullptr: 1) and is zero where that is.  scratch: head_grad_scratch_bytes.
+struct HeadGrad {
+  const float* dY;      // n x V, or nullptr:
+  const float* logits;  // n x V
+  const int32_t* targets;
+  const float *nll, *lse, *dnll;
+};
 size_t head_grad_scratch_bytes(const archead_head* head, int64_t n);
-cudaError_t launch_head_grad(const float* dY, const archead_head* head, int64_t n,
-                             const float* rowscale, uint16_t* dH, void* scratch,
-                             cudaStream_t st, int* launches);
-// In place: Y[n, v] -> exp(Y[n, v] - lse[n]) - [v = targets[n]], with the target's entry
-// taken from its NLL (exp(-nll) - 1).
-cudaError_t launch_softmax_grad(float* Y, const int32_t* targets, const float* nll,
-                                const float* lse, const float* dnll, int64_t n, int64_t V,
-                                unsigned* err, cudaStream_t st, int* launches);
+cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_t n, uint16_t* dH,
+                             void* scratch, unsigned* err, cudaStream_t st, int* launches);
 
 // Losses on per-token NLLs (csrc/losses.cu).
 struct PolicyArgs {

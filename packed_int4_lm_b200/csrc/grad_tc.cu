@@ -1,0 +1,881 @@
+// Gradient product through the packed head on the 5th-generation tensor cores:
+//
+//   dH[n, d] = s_n ( sum_v dY[n, v] S_v c[v, d / g] q[v, d]  +  sum_j u[n, j] b[j, d] ),
+//   u[n, j]  = sum_v dY[n, v] a[v, j],
+//
+// a = [Q8(A_c) | Q8(A_w)], b = [Q8(B_c) ; Q8(B_w)].  The long axis is the vocabulary, so the
+// packed head is the transposed operand: D[d, n] = sum_v A[v, d] B[n, v] with A the dequantised
+// head (vocabulary rows are K, its columns the 128 lanes of the accumulator) and B the FP16 image
+// of dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh).  u is one more tile of columns, A then
+// being a / S'.
+//
+//  * grad_rows_kernel: S'_v per row and their maximum; clears the per-token maxima.
+//  * dy_amax_kernel, dy_image_kernel: the image, from dY or from logits (softmax gradient).
+//  * grad_tc_kernel: the product.  A work item is 256 columns (two accumulators of 128 lanes) x
+//    NT tokens x a slab of the vocabulary; its FP32 sums go to scratch.
+//  * grad_finish_kernel: adds the slabs in order, adds u b, scales and rounds to BF16.
+// Nothing is accumulated in memory, so equal calls give equal bits.
+#include "grad_common.cuh"
+#include "tc_common.cuh"
+
+namespace archead {
+namespace {
+
+constexpr int kDequantWarps = 8;
+constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 2 producers, 1 MMA
+constexpr int kUnit = 128;                              // vocabulary rows per unit of K
+constexpr int kAStage = 64 * 256 * 2;                   // 64 rows x 256 columns FP16
+constexpr int kPkStage = 16384;                         // 128 rows x 256 columns of nibbles
+constexpr int kRowBlocks = 148;                         // blocks of grad_rows_kernel
+
+// ---- the image ---------------------------------------------------------------------------
+struct RowsParams {
+  archead_head h;
+  int64_t vpad;
+  float* sp;         // S'_v, vpad (0 past V)
+  float* spmax;      // kRowBlocks
+  unsigned* amax;    // per token, cleared here (n), or nullptr
+  int64_t n;
+};
+
+__global__ void __launch_bounds__(256) grad_rows_kernel(const RowsParams p) {
+  allow_dependent_launch();
+  __shared__ float red[8];
+  const int64_t t0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+  float m = 0.f;
+  for (int64_t v = t0; v < p.vpad; v += step) {
+    float s = 0.f;
+    if (v < p.h.V) {
+      if (p.h.format == ARCHEAD_FMT_ROW8)
+        s = p.h.row_scale[v];
+      else
+        s = grad_row(bf16_bits_to_float(p.h.r_super[v]), p.h.r_c ? p.h.sAc[v] : 0.f,
+                     p.h.r_r ? p.h.sAw[v] : 0.f).sp;
+    }
+    p.sp[v] = s;
+    m = fmaxf(m, fabsf(s));
+  }
+  if (p.amax)
+    for (int64_t i = t0; i < p.n; i += step) p.amax[i] = 0u;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+    p.spmax[blockIdx.x] = m;
+  }
+}
+
+// Exponent of the largest S' (0 for a head of zeros), by one warp.
+__device__ __forceinline__ int spmax_exp(const float* spmax) {
+  float m = 0.f;
+  for (int i = threadIdx.x & 31; i < kRowBlocks; i += 32) m = fmaxf(m, spmax[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = m > 0.f && m <= 3.402823466e38f ? ilogbf(m) : 0;
+  return e < -100 ? -100 : (e > 100 ? 100 : e);  // so that pow2_pair can take every sum of two
+}
+
+// Per token the largest |dY| (as bits: a NaN is the largest), one warp per 2048 entries.
+__global__ void __launch_bounds__(256) dy_amax_kernel(const float* __restrict__ dY, int64_t n,
+                                                      int64_t V, unsigned* amax) {
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t per = (V + 2047) / 2048, total = per * n;
+  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < total; i += gridDim.x * 8ll) {
+    const int64_t t = i / per, v0 = (i - t * per) * 2048;
+    const int64_t v1 = v0 + 2048 < V ? v0 + 2048 : V;
+    unsigned m = 0;
+    for (int64_t v = v0 + lane; v < v1; v += 32)
+      m = max(m, __float_as_uint(dY[t * V + v]) & 0x7fffffffu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) atomicMax(amax + t, m);
+  }
+}
+
+struct ImageParams {
+  const float* src;  // dY, or logits
+  int64_t n, npad, V;
+  int nt;
+  const float* sp;
+  const float* spmax;
+  const unsigned* amax;  // dY: per-token maxima
+  // logits: dY = exp(Y - lse) - [v = target], the target's entry from its NLL
+  const int32_t* targets;
+  const float* nll;
+  const float* lse;
+  const float* dnll;
+  char* img;
+  int* texp;  // per token: dH = 2^texp times the product
+  unsigned* err;
+};
+
+// Token factor 2^f of the image (before S' 2^-es): dY 2^f S' 2^-es stays below 2^15.
+__device__ __forceinline__ int dy_exp(unsigned amax) {
+  const int e = (int)(amax >> 23) - 127;  // floor(log2 amax) (subnormal: -127)
+  return amax == 0u || amax >= 0x7f800000u ? 0 : 12 - e;
+}
+// The softmax gradient's entries are below b = 1 - p_target.  p_target comes from the NLL; as
+// its FP32 error (a few half steps of the log-sum-exp) may be all of it, b is taken larger.
+__device__ __forceinline__ int softmax_exp(float nll, float lse) {
+  const float b = fmaxf(fmaxf(-expm1f(-nll), 0x1p-18f), fabsf(lse) * 0x1p-21f);
+  return b <= 3.402823466e38f ? 12 - ilogbf(b) : 0;
+}
+
+// One warp per 64 vocabulary rows and group of 32 tokens: each lane two rows, one 128-byte
+// image row per token.
+template <bool kSoftmax>
+__global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t nhb = (p.V + kUnit - 1) / kUnit * 2;
+  const int64_t hb = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int64_t n0 = blockIdx.y * 32ll;
+  const int es = spmax_exp(p.spmax);
+  // this lane's token of the group: its factor
+  const int64_t mine = n0 + lane;
+  int f = 0;
+  bool bad = false;
+  if (mine < p.n) {
+    if (kSoftmax) {
+      const int32_t t = p.targets[mine];
+      f = softmax_exp(p.nll[mine], p.lse[mine]);
+      bad = (t < 0 || t >= p.V) && p.dnll[mine] != 0.f;
+    } else {
+      f = dy_exp(p.amax[mine]);
+    }
+    if (hb == 0) p.texp[mine] = es - f;  // within +-240
+  }
+  if (hb == 0 && bad) atomicOr(p.err, kErrTarget);
+  if (hb >= nhb) return;
+  const int64_t v = 64 * hb + 2 * lane;
+  float s0 = p.sp[v], s1 = p.sp[v + 1], e0, e1;
+  pow2_pair(-es, &e0, &e1);
+  s0 = s0 * e0 * e1;
+  s1 = s1 * e0 * e1;
+  for (int k = 0; k < 32 && n0 + k < p.npad; ++k) {
+    const int64_t n = n0 + k;
+    float y0 = 0.f, y1 = 0.f;
+    const int fk = __shfl_sync(0xffffffffu, f, k);
+    const bool bk = __shfl_sync(0xffffffffu, (int)bad, k);
+    if (n < p.n) {
+      const float* row = p.src + n * p.V;
+      if (v < p.V) y0 = row[v];
+      if (v + 1 < p.V) y1 = row[v + 1];
+      if (kSoftmax) {
+        const float l = bk ? __int_as_float(0x7fc00000) : p.lse[n];
+        const int64_t t = p.targets[n];
+        y0 = v < p.V ? (v == t ? expm1f(-p.nll[n]) : expf(y0 - l)) : 0.f;
+        y1 = v + 1 < p.V ? (v + 1 == t ? expm1f(-p.nll[n]) : expf(y1 - l)) : 0.f;
+      }
+      float a, b;
+      pow2_pair(fk, &a, &b);
+      y0 = y0 * a * b * s0;
+      y1 = y1 * a * b * s1;
+    }
+    const int64_t tt = n / p.nt;
+    *reinterpret_cast<__half2*>(p.img + grad_image_offset(tt, hb, nhb, p.nt, (int)(n - tt * p.nt),
+                                                          2 * lane)) = __floats2half2_rn(y0, y1);
+  }
+}
+
+// ---- the product -------------------------------------------------------------------------
+struct GradParams {
+  archead_head h;
+  const char* img;
+  float* part;  // [slab][n][dp]
+  int64_t n, dp;
+  int64_t nunits;  // units of 128 vocabulary rows
+  int ntt;         // token tiles
+  int ntiles;      // column tiles: ceil(D / 256), one more for the ranks
+  int slabs;
+  int g_shift;
+  int a_words;  // factor rows readable as aligned 32-bit words
+  unsigned* err;
+};
+
+template <int NT>
+struct GradCfg {
+  // Shared memory (227 KB): rings of A stages (32 KB: 64 rows x 256 columns), packed stages
+  // (16 KB: 128 rows x 256 columns) and B stages (64 rows x NT tokens).
+  static constexpr int SA = NT >= 128 ? 3 : 4;
+  static constexpr int SP = NT == 256 ? 2 : (NT == 128 ? 3 : 4);
+  static constexpr int SB = NT == 256 ? 3 : 4;
+  static constexpr int BSTAGE = NT * 128;
+  static constexpr int SETS = NT == 256 ? 1 : 2;  // accumulator pairs
+  static constexpr int TMEM_COLS = 2 * NT * SETS < 32 ? 32 : 2 * NT * SETS;
+  static constexpr size_t SMEM = (size_t)SA * kAStage + SP * kPkStage + SB * BSTAGE + 1024 + 512;
+  static_assert(SMEM <= 227 * 1024 && TMEM_COLS <= 512, "does not fit an SM");
+};
+
+struct GradItem {
+  int64_t u0, u1;
+  int slab, tt, dt;
+  int nacc;   // accumulators of 128 columns: 1 or 2
+  bool rank;  // the tile of the rank sums
+};
+
+__device__ __forceinline__ bool grad_item(const GradParams& p, int64_t k, GradItem& it) {
+  const int64_t i = blockIdx.x + k * gridDim.x;
+  const int64_t per = (int64_t)p.ntt * p.ntiles;
+  if (i >= per * p.slabs) return false;
+  it.slab = (int)(i / per);
+  const int64_t r = i - it.slab * per;
+  it.tt = (int)(r / p.ntiles);
+  it.dt = (int)(r - (int64_t)it.tt * p.ntiles);
+  it.u0 = p.nunits * it.slab / p.slabs;
+  it.u1 = p.nunits * (it.slab + 1) / p.slabs;
+  const int64_t nd = (p.h.D + 255) >> 8;
+  it.rank = it.dt >= nd;
+  const int64_t cols = it.rank ? p.h.r_c + p.h.r_r : p.h.D - 256ll * it.dt;
+  it.nacc = cols > 128 ? 2 : 1;
+  return true;
+}
+
+// Shared-memory matrix descriptor, MN-major with the 128-byte swizzle: atoms of 64 columns x 8
+// rows of K, each K row 128 bytes; lead = byte distance of atoms adjacent in M / N, stride =
+// that of atoms adjacent in K.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead, uint32_t stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((stride >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, one M=128 x N x K=16 step, issued by one thread.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two signed bytes (the low two of w's bytes sel, sel + 1) as exact FP16: 1024 + 128 + b is a
+// half whose low mantissa byte is b ^ 0x80.
+__device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w_flipped), "r"(0x64646464u), "r"(sel));
+  return __hsub2(*reinterpret_cast<__half2*>(&r), __float2half2_rn(1152.f));
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// Four factor entries j .. j+3 of row v in [A_c | A_w], zeros past r_c + r_r.
+__device__ __forceinline__ uint32_t grad_factor_word(const GradParams& p, int64_t v, int j) {
+  const int rc = p.h.r_c, rr = p.h.r_r;
+  if (p.a_words) {
+    if (j < rc) return __ldg(reinterpret_cast<const uint32_t*>(p.h.Ac + v * rc + j));
+    if (j < rc + rr) return __ldg(reinterpret_cast<const uint32_t*>(p.h.Aw + v * rr + (j - rc)));
+    return 0u;
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int jj = j + u;
+    int8_t b = 0;
+    if (jj < rc) b = __ldg(p.h.Ac + v * rc + jj);
+    else if (jj < rc + rr) b = __ldg(p.h.Aw + v * rr + (jj - rc));
+    w |= (uint32_t)(uint8_t)b << (8 * u);
+  }
+  return w;
+}
+
+// Scales and codes of one vocabulary row for one block of 128 columns (CPC codes).
+struct RowLoad {
+  uint32_t code;
+  float S, sac, saw;
+};
+template <int CPC>
+__device__ __forceinline__ RowLoad load_grad_row(const GradParams& p, int64_t v, int64_t col, bool codes) {
+  RowLoad r = {0u, 0.f, 0.f, 0.f};
+  if (CPC == 0) return r;
+  if (v < p.h.V) {
+    r.S = bf16_bits_to_float(__ldg(p.h.r_super + v));
+    if (p.h.r_c) r.sac = __ldg(p.h.sAc + v);
+    if (p.h.r_r) r.saw = __ldg(p.h.sAw + v);
+  }
+  if (codes) {  // rows past V are padded
+    const uint8_t* c = p.h.r_code + v * (p.h.D >> p.g_shift) + (col >> p.g_shift);
+    if (CPC == 1) r.code = __ldg(c);
+    else if (CPC == 2) r.code = __ldg(reinterpret_cast<const uint16_t*>(c));
+    else r.code = __ldg(reinterpret_cast<const uint32_t*>(c));
+  }
+  return r;
+}
+
+template <int NT, int CPC>
+__global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradParams p) {
+  using C = GradCfg<NT>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* As = smem;
+  unsigned char* Bs = As + C::SA * kAStage;
+  unsigned char* Ps = Bs + C::SB * C::BSTAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(Ps + C::SP * kPkStage);
+  uint64_t* a_full = bars;
+  uint64_t* a_empty = a_full + C::SA;
+  uint64_t* b_full = a_empty + C::SA;
+  uint64_t* b_empty = b_full + C::SB;
+  uint64_t* p_full = b_empty + C::SB;
+  uint64_t* p_empty = p_full + C::SP;
+  uint64_t* acc_full = p_empty + C::SP;
+  uint64_t* acc_empty = acc_full + C::SETS;
+  uint64_t* mma_done = acc_empty + C::SETS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::SA; ++i) {
+      tc::mbar_init(&a_full[i], 4);  // the four warps that fill a stage
+      tc::mbar_init(&a_empty[i], 1);
+    }
+    for (int i = 0; i < C::SB; ++i) {
+      tc::mbar_init(&b_full[i], 1);
+      tc::mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < C::SP; ++i) {
+      tc::mbar_init(&p_full[i], 1);
+      tc::mbar_init(&p_empty[i], kDequantWarps);
+    }
+    for (int i = 0; i < C::SETS; ++i) {
+      tc::mbar_init(&acc_full[i], 1);
+      tc::mbar_init(&acc_empty[i], 128);
+    }
+    tc::mbar_init(mma_done, 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == kDequantWarps + 6) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+  GradItem it;
+
+  if (warp < kDequantWarps) {
+    // ---- dequantisation: lane = vocabulary row of a 32-row group ----
+    // A warp owns rows 32 rg .. + 31 of each unit and one 128-column block b; the unit's two
+    // 64-row halves are two A stages, so four warps fill a stage.
+    const int rg = warp & 3, b = warp >> 2, h = rg >> 1;
+    const int s = 32 * rg + lane;       // row in the unit
+    const int k = 32 * (rg & 1) + lane;  // row in the stage
+    const uint32_t a_row = tc::smem_u32(As) + (uint32_t)(b * 2) * 8192 + (k >> 3) * 1024 + (k & 7) * 128;
+    const uint32_t x7 = k & 7;
+    int64_t seq = 0;  // units so far
+    int ps = 0;
+    uint32_t pp = 0;
+    bool ok = true;
+    for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+      const bool work = b < it.nacc;
+      const int64_t col = 256ll * it.dt + 128 * b;
+      RowLoad nx = load_grad_row<CPC>(p, it.u0 * kUnit + s, col, work && !it.rank);
+      for (int64_t u = it.u0; u < it.u1; ++u, ++seq) {
+        const RowLoad r = nx;
+        const int64_t v = u * kUnit + s;
+        if (u + 1 < it.u1) nx = load_grad_row<CPC>(p, v + kUnit, col, work && !it.rank);
+        uint32_t w[16];
+        uint4 raw[8];
+        if (CPC != 0 && !it.rank) {
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err))) {
+            ok = false;
+            break;
+          }
+          const unsigned char* src = Ps + ps * kPkStage + b * 8192 + s * 16;
+          if (work) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 q = *reinterpret_cast<const uint4*>(src + c * 2048);
+              w[4 * c] = q.x;
+              w[4 * c + 1] = q.y;
+              w[4 * c + 2] = q.z;
+              w[4 * c + 3] = q.w;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&p_empty[ps]);
+          if (++ps == C::SP) {
+            ps = 0;
+            pp ^= 1u;
+          }
+        }
+        if (CPC == 0 && work) {  // INT8 rows straight from global memory
+          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            raw[c] = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
+        }
+        const int64_t ks = 2 * seq + h;
+        const int slot = (int)(ks % C::SA);
+        const int64_t use = ks / C::SA;
+        if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&a_empty[slot], (uint32_t)(use - 1) & 1u, p.err))) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = a_row + slot * kAStage;
+        if (work) {
+          if (CPC == 0) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the block
+              const uint32_t q[4] = {raw[c].x ^ 0x80808080u, raw[c].y ^ 0x80808080u,
+                                     raw[c].z ^ 0x80808080u, raw[c].w ^ 0x80808080u};
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t at = dst + (c >> 2) * 8192 + ((((2 * c + e) & 7) ^ x7) << 4);
+                st_shared16(at, h2_bits(bytes_to_half2(q[2 * e], 0x4140)), h2_bits(bytes_to_half2(q[2 * e], 0x4342)),
+                            h2_bits(bytes_to_half2(q[2 * e + 1], 0x4140)), h2_bits(bytes_to_half2(q[2 * e + 1], 0x4342)));
+              }
+            }
+          } else if (it.rank) {
+            const GradRow gr = grad_row(r.S, r.sac, r.saw);
+            const float rcp = gr.sp != 0.f ? 1.f / gr.sp : 0.f;
+            const int rc = p.h.r_c, RR = p.h.r_c + p.h.r_r;
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+              const int j0 = 128 * b + 8 * c;
+              uint32_t o[4] = {0u, 0u, 0u, 0u};
+              if (j0 < RR && v < p.h.V) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const uint32_t fw = grad_factor_word(p, v, j0 + 4 * q);
+                  float x[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    x[e] = __fmul_rn((float)(int8_t)((fw >> (8 * e)) & 0xFFu), j0 + 4 * q + e < rc ? r.sac : r.saw) * rcp;
+                  o[2 * q] = h2_bits(__floats2half2_rn(x[0], x[1]));
+                  o[2 * q + 1] = h2_bits(__floats2half2_rn(x[2], x[3]));
+                }
+              }
+              st_shared16(dst + (c >> 3) * 8192 + (((c & 7) ^ x7) << 4), o[0], o[1], o[2], o[3]);
+            }
+          } else {
+            const float cs = grad_row(r.S, r.sac, r.saw).cs;
+#pragma unroll
+            for (int wn = 0; wn < 4; ++wn) {  // window of 32 columns
+              const uint32_t cw = CPC == 1 ? r.code : (CPC == 2 ? (r.code >> (8 * (wn >> 1))) & 0xFFu : (r.code >> (8 * wn)) & 0xFFu);
+              const __half2 c2 = __float2half2_rn((float)cw * cs);  // exact for k <= 24
+              const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {  // columns 32 wn + 8 c .. + 7: one 16-byte chunk
+                __half2 o[4];
+                dequant_word(w[4 * c + wn], c2, nc24, o);
+                st_shared16(dst + (wn >> 1) * 8192 + (((((wn & 1) << 2) + c) ^ x7) << 4), h2_bits(o[0]),
+                            h2_bits(o[1]), h2_bits(o[2]), h2_bits(o[3]));
+              }
+            }
+          }
+        }
+        tc::fence_proxy_async_smem();  // the MMA reads the stage through the async proxy
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&a_full[slot]);
+      }
+    }
+  } else if (warp < kDequantWarps + 4) {
+    // ---- epilogue: lane = column of the tile; raw sums to scratch ----
+    const int e = warp - kDequantWarps;
+    const uint32_t lane_off = (uint32_t)(32 * e) << 16;
+    for (int64_t i = 0; grad_item(p, i, it); ++i) {
+      const int set = (int)(i % C::SETS);
+      const int64_t use = i / C::SETS;
+      if (!tc::bar_and(1, 128, tc::mbar_wait(&acc_full[set], (uint32_t)use & 1u, p.err))) break;
+      tc::fence_after_sync();
+      const int64_t tok0 = (int64_t)it.tt * NT;
+      const int64_t ntok = p.n - tok0 < NT ? p.n - tok0 : NT;
+      const int RR = p.h.r_c + p.h.r_r;
+#pragma unroll 1
+      for (int a = 0; a < it.nacc; ++a) {
+        const int64_t c = 128 * a + 32 * e + lane;
+        const bool live = it.rank ? c < RR : true;
+        float* dst = p.part + ((int64_t)it.slab * p.n + tok0) * p.dp + (it.rank ? p.h.D : 256ll * it.dt) + c;
+#pragma unroll 1
+        for (int c0 = 0; c0 < NT; c0 += 16) {
+          float y[16];
+          tc::tmem_ld16(tbase + (set * 2 + a) * NT + lane_off + c0, y);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              if (c0 + q < ntok) __stcs(dst + (c0 + q) * p.dp, y[q]);
+          }
+        }
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(&acc_empty[set]);
+    }
+  } else if (warp == kDequantWarps + 4) {
+    // ---- packed producer (one thread) ----
+    if (lane == 0 && CPC != 0) {
+      const int64_t nkb = p.h.D >> 7;
+      int64_t np = 0;
+      int ps = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+        if (it.rank) continue;
+        const uint32_t bytes = (uint32_t)it.nacc * 8192u;
+        for (int64_t u = it.u0; u < it.u1; ++u) {
+          if (np >= C::SP && !tc::mbar_wait(&p_empty[ps], ph ^ 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          tc::fence_proxy_async_smem();  // the stage was read with generic loads
+          tc::mbar_arrive_expect_tx(&p_full[ps], bytes);
+          tc::bulk_g2s(Ps + ps * kPkStage, p.h.r_nib + ((u * nkb + 2 * it.dt) << 13), bytes, &p_full[ps]);
+          ++np;
+          if (++ps == C::SP) {
+            ps = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int64_t q = np < C::SP ? 0 : np - C::SP; q < np; ++q)
+          tc::mbar_wait(&p_full[q % C::SP], (uint32_t)(q / C::SP) & 1u, p.err);
+    }
+  } else if (warp == kDequantWarps + 5) {
+    // ---- B producer (one thread): the image, written by the kernel before this one ----
+    if (lane == 0) {
+      grid_dependency_wait();
+      int64_t nb = 0;
+      int bs = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+        const char* src = p.img + ((int64_t)it.tt * p.nunits * 2 + 2 * it.u0) * C::BSTAGE;
+        for (int64_t u = 2 * it.u0; u < 2 * it.u1; ++u) {
+          if (nb >= C::SB && !tc::mbar_wait(&b_empty[bs], ph ^ 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&b_full[bs], C::BSTAGE);
+          tc::bulk_g2s(Bs + bs * C::BSTAGE, src, C::BSTAGE, &b_full[bs]);
+          src += C::BSTAGE;
+          ++nb;
+          if (++bs == C::SB) {
+            bs = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int64_t q = nb < C::SB ? 0 : nb - C::SB; q < nb; ++q)
+          tc::mbar_wait(&b_full[q % C::SB], (uint32_t)(q / C::SB) & 1u, p.err);
+    }
+  } else {
+    // ---- MMA issuer: the whole warp, one elected lane issues ----
+    const uint32_t idesc = tc::idesc_f16_m128(NT) | (1u << 15);  // A is MN-major
+    const uint64_t adesc0 = desc_mn_sw128(tc::smem_u32(As), 8192, 1024);
+    const uint64_t bdesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Bs));
+    int sa = 0, sb = 0;
+    uint32_t pa = 0, pb = 0;
+    bool ok = true;
+    for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+      const int set = (int)(i % C::SETS);
+      const int64_t use = i / C::SETS;
+      if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[set], (uint32_t)(use - 1) & 1u, p.err)))
+        break;
+      tc::fence_after_sync();
+      const uint32_t d0 = tbase + set * 2 * NT;
+      const int64_t k1 = 2 * (it.u1 - it.u0);
+      for (int64_t kk = 0; kk < k1; ++kk) {
+        const bool ra = tc::mbar_try_wait(&a_full[sa], pa);
+        const bool rb = tc::mbar_try_wait(&b_full[sb], pb);
+        if (!__all_sync(0xffffffffu, (ra && rb) || (tc::mbar_wait(&a_full[sa], pa, p.err) &&
+                                                     tc::mbar_wait(&b_full[sb], pb, p.err)))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint64_t ad = adesc0 + (uint64_t)((sa * kAStage) >> 4);
+        const uint64_t bd = bdesc0 + (uint64_t)((sb * C::BSTAGE) >> 4);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // K steps of 16 rows: two 8-row atoms of A, 32 bytes of B
+            mma_f16_ss(d0, ad + ((j * 2048) >> 4), bd + ((j * 32) >> 4), idesc, (kk | j) != 0);
+            if (it.nacc == 2)
+              mma_f16_ss(d0 + NT, ad + ((16384 + j * 2048) >> 4), bd + ((j * 32) >> 4), idesc, (kk | j) != 0);
+          }
+          tc::mma_commit(&a_empty[sa]);
+          tc::mma_commit(&b_empty[sb]);
+        }
+        __syncwarp();
+        if (++sa == C::SA) {
+          sa = 0;
+          pa ^= 1u;
+        }
+        if (++sb == C::SB) {
+          sb = 0;
+          pb ^= 1u;
+        }
+      }
+      if (ok && tc::elect_one()) tc::mma_commit(&acc_full[set]);
+      __syncwarp();
+    }
+    if (tc::elect_one()) {
+      tc::mma_commit(mma_done);
+      tc::mbar_wait(mma_done, 0, p.err);  // every MMA issued here has retired
+    }
+    __syncwarp();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kDequantWarps + 6) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, C::TMEM_COLS);
+  }
+}
+
+// ---- finish ------------------------------------------------------------------------------
+struct FinishParams {
+  archead_head h;
+  const float* part;
+  int64_t n, dp;
+  int slabs;
+  const int* texp;
+  const float* rowscale;
+  __nv_bfloat16* dH;
+};
+
+// 16 tokens x 256 columns per block; a thread owns two adjacent columns.
+__global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) {
+  grid_dependency_wait();
+  extern __shared__ float us[];  // [RR][16]
+  const int RR = p.h.r_c + p.h.r_r;
+  const int64_t n0 = blockIdx.x * 16ll;
+  for (int i = threadIdx.x; i < RR * 16; i += 128) {
+    const int j = i >> 4;
+    const int64_t n = n0 + (i & 15);
+    float a = 0.f;
+    if (n < p.n)
+      for (int s = 0; s < p.slabs; ++s) a += p.part[(s * p.n + n) * p.dp + p.h.D + j];
+    us[i] = a;
+  }
+  __syncthreads();
+  const int64_t d = blockIdx.y * 256ll + 2 * threadIdx.x;
+  if (d >= p.h.D) return;
+  float a0[16], a1[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    a0[t] = a1[t] = 0.f;
+    if (n0 + t < p.n)
+      for (int s = 0; s < p.slabs; ++s) {
+        const float2 q = *reinterpret_cast<const float2*>(p.part + (s * p.n + n0 + t) * p.dp + d);
+        a0[t] += q.x;
+        a1[t] += q.y;
+      }
+  }
+  const int64_t G = p.h.D / p.h.g, grp = d / p.h.g;
+  for (int j = 0; j < RR; ++j) {
+    const bool core = j < p.h.r_c;
+    const int jj = core ? j : j - p.h.r_c;
+    const char2 q = *reinterpret_cast<const char2*>((core ? p.h.Bc : p.h.Bw) + jj * p.h.D + d);
+    const float sc = __ldg((core ? p.h.sBc : p.h.sBw) + jj * G + grp);
+    const float b0 = __fmul_rn((float)q.x, sc), b1 = __fmul_rn((float)q.y, sc);
+#pragma unroll
+    for (int t4 = 0; t4 < 4; ++t4) {
+      const float4 u = *reinterpret_cast<const float4*>(us + 16 * j + 4 * t4);
+      a0[4 * t4] = fmaf(u.x, b0, a0[4 * t4]);
+      a1[4 * t4] = fmaf(u.x, b1, a1[4 * t4]);
+      a0[4 * t4 + 1] = fmaf(u.y, b0, a0[4 * t4 + 1]);
+      a1[4 * t4 + 1] = fmaf(u.y, b1, a1[4 * t4 + 1]);
+      a0[4 * t4 + 2] = fmaf(u.z, b0, a0[4 * t4 + 2]);
+      a1[4 * t4 + 2] = fmaf(u.z, b1, a1[4 * t4 + 2]);
+      a0[4 * t4 + 3] = fmaf(u.w, b0, a0[4 * t4 + 3]);
+      a1[4 * t4 + 3] = fmaf(u.w, b1, a1[4 * t4 + 3]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const int64_t n = n0 + t;
+    if (n >= p.n) break;
+    const float sc = p.rowscale ? p.rowscale[n] : 1.f;
+    float e0, e1, y0 = 0.f, y1 = 0.f;
+    pow2_pair(p.texp[n], &e0, &e1);
+    if (sc != 0.f) {
+      y0 = a0[t] * e0 * e1 * sc;
+      y1 = a1[t] * e0 * e1 * sc;
+    }
+    *reinterpret_cast<__nv_bfloat162*>(p.dH + n * p.h.D + d) = __floats2bfloat162_rn(y0, y1);
+  }
+}
+
+// ---- host --------------------------------------------------------------------------------
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+struct GradPlan {
+  int nt, ntt, ntiles, slabs;
+  int64_t npad, nunits, dp;
+  size_t o_img, o_sp, o_spmax, o_amax, o_texp, o_part, bytes;
+};
+
+GradPlan grad_plan(const archead_head& h, int64_t n) {
+  GradPlan g;
+  const int RR = h.r_c + h.r_r;
+  g.nt = n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : 256)));
+  g.ntt = (int)((n + g.nt - 1) / g.nt);
+  g.npad = (int64_t)g.ntt * g.nt;
+  g.ntiles = (int)((h.D + 255) / 256) + (RR > 0);
+  g.nunits = (h.V + kUnit - 1) / kUnit;
+  g.dp = (h.D + RR + 3) / 4 * 4;
+  // Slabs of the vocabulary: CTAs run items of equal length side by side, so the time is that of
+  // ceil(items / CTAs) rounds of 1 / slabs each, plus the partial sums' way through memory (an
+  // element written and read costs about as long as 1.2e-6 of a full-length tile).
+  const int64_t tiles = (int64_t)g.ntt * g.ntiles;
+  const int64_t sms = sm_count();
+  double best = 1e300;
+  g.slabs = 1;
+  for (int s = 1; s <= 64 && s * 4 <= g.nunits + 3; ++s) {
+    const double rounds = (double)((tiles * s + sms - 1) / sms) / s;
+    const double tile_us = g.nunits * (g.nt == 256 ? 1.25 : (g.nt == 128 ? 0.8 : 0.55));
+    const double cost = rounds * tile_us + 8.0 * s * n * g.dp / 4e6;
+    if (cost < best * 0.995) {
+      best = cost;
+      g.slabs = s;
+    }
+  }
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t r = o;
+    o += up256(b);
+    return r;
+  };
+  g.o_img = take((size_t)g.npad * g.nunits * kUnit * 2);
+  g.o_sp = take((size_t)g.nunits * kUnit * 4);
+  g.o_spmax = take(kRowBlocks * 4);
+  g.o_amax = take((size_t)n * 4);
+  g.o_texp = take((size_t)n * 4);
+  g.o_part = take((size_t)g.slabs * n * g.dp * 4);
+  g.bytes = o;
+  return g;
+}
+
+template <typename Kern, typename Params>
+cudaError_t launch_pdl(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t st, const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int NT, int CPC>
+cudaError_t launch_grad_cfg(const GradParams& p, cudaStream_t st) {
+  auto kern = grad_tc_kernel<NT, CPC>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradCfg<NT>::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)p.ntt * p.ntiles * p.slabs, sms = sm_count();
+  return launch_pdl(kern, dim3((unsigned)(items < sms ? items : sms)), kGradThreads, GradCfg<NT>::SMEM, st, p);
+}
+
+template <int NT>
+cudaError_t launch_grad_nt(const GradParams& p, cudaStream_t st) {
+  if (p.h.format == ARCHEAD_FMT_ROW8) return launch_grad_cfg<NT, 0>(p, st);
+  if (p.h.g == 32) return launch_grad_cfg<NT, 4>(p, st);
+  if (p.h.g == 64) return launch_grad_cfg<NT, 2>(p, st);
+  return launch_grad_cfg<NT, 1>(p, st);
+}
+
+}  // namespace
+
+size_t head_grad_scratch_bytes(const archead_head* head, int64_t n) { return grad_plan(*head, n).bytes; }
+
+cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_t n, uint16_t* dH,
+                             void* scratch, unsigned* err, cudaStream_t st, int* launches) {
+  const GradPlan g = grad_plan(*head, n);
+  char* b = static_cast<char*>(scratch);
+  float* sp = reinterpret_cast<float*>(b + g.o_sp);
+  float* spmax = reinterpret_cast<float*>(b + g.o_spmax);
+  unsigned* amax = reinterpret_cast<unsigned*>(b + g.o_amax);
+  int* texp = reinterpret_cast<int*>(b + g.o_texp);
+  const RowsParams rp = {*head, g.nunits * kUnit, sp, spmax, a.dY ? amax : nullptr, n};
+  grad_rows_kernel<<<kRowBlocks, 256, 0, st>>>(rp);
+  ++*launches;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (a.dY) {
+    const int64_t blocks = ((head->V + 2047) / 2048 * n + 7) / 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, dy_amax_kernel, a.dY, n, head->V, amax)) != cudaSuccess) return e;
+    ++*launches;
+  }
+  ImageParams ip;
+  ip.src = a.dY ? a.dY : a.logits;
+  ip.n = n;
+  ip.npad = g.npad;
+  ip.V = head->V;
+  ip.nt = g.nt;
+  ip.sp = sp;
+  ip.spmax = spmax;
+  ip.amax = amax;
+  ip.targets = a.targets;
+  ip.nll = a.nll;
+  ip.lse = a.lse;
+  ip.dnll = a.dnll;
+  ip.img = b + g.o_img;
+  ip.texp = texp;
+  ip.err = err;
+  const dim3 ig((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + 31) / 32));
+  e = a.dY ? launch_pdl(dy_image_kernel<false>, ig, 256, 0, st, ip)
+           : launch_pdl(dy_image_kernel<true>, ig, 256, 0, st, ip);
+  if (e != cudaSuccess) return e;
+  GradParams p;
+  p.h = *head;
+  p.img = ip.img;
+  p.part = reinterpret_cast<float*>(b + g.o_part);
+  p.n = n;
+  p.dp = g.dp;
+  p.nunits = g.nunits;
+  p.ntt = g.ntt;
+  p.ntiles = g.ntiles;
+  p.slabs = g.slabs;
+  int gs = 0;
+  while ((1 << gs) < head->g) ++gs;
+  p.g_shift = gs;
+  p.a_words = head->r_c % 4 == 0 && head->r_r % 4 == 0;
+  p.err = err;
+  switch (g.nt) {
+    case 16: e = launch_grad_nt<16>(p, st); break;
+    case 32: e = launch_grad_nt<32>(p, st); break;
+    case 64: e = launch_grad_nt<64>(p, st); break;
+    case 128: e = launch_grad_nt<128>(p, st); break;
+    default: e = launch_grad_nt<256>(p, st); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int RR = head->r_c + head->r_r;
+  const FinishParams fp = {*head, p.part, n, g.dp, g.slabs, texp, a.dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
+  e = launch_pdl(grad_finish_kernel, dim3((unsigned)((n + 15) / 16), (unsigned)((head->D + 255) / 256)), 128,
+                 (size_t)RR * 64, st, fp);
+  *launches += 3;
+  return e;
+}
+
+}  // namespace archead

@@ -13,12 +13,18 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Scratch of one chunk of archead_nll_grad: its logits, about 2 GB at most.
+// Tokens per chunk of the gradients: about 2 GB of scratch for FP32 logits, whole token tiles of
+// the product where that allows, and at most 65536 (the kernels' grids).
 constexpr int64_t kChunkBytes = 2ll << 30;
 
 int64_t grad_chunk(int64_t N, int64_t V) {
-  const int64_t c = std::max<int64_t>(kChunkBytes / (V * 4), 1);
+  const int64_t c = std::min<int64_t>(std::max<int64_t>(kChunkBytes / (V * 4), 1), 65536);
   return std::min(N, c >= 256 ? c / 256 * 256 : c);
+}
+// The last chunk is shorter and may be split otherwise.
+size_t chunk_scratch(const archead_head* head, int64_t N, int64_t chunk) {
+  const size_t whole = head_grad_scratch_bytes(head, chunk);
+  return N % chunk ? std::max(whole, head_grad_scratch_bytes(head, N % chunk)) : whole;
 }
 
 // Runs `launch` with scratch of the given size; the common end of every entry point here.
@@ -64,7 +70,7 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t chunk = grad_chunk(N, V);
   const size_t yb = (size_t)chunk * V * 4, yoff = (yb + 255) / 256 * 256;
-  return with_scratch(yoff + head_grad_scratch_bytes(head, chunk), st,
+  return with_scratch(yoff + chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
     float* Y = reinterpret_cast<float*>(b);
     cudaError_t e = cudaSuccess;
@@ -73,10 +79,8 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
       if (archead_logits(H + n0 * D, head, Y, n, V, D, r_c, r_r, g, stream) != ARCHEAD_OK)
         return cudaErrorUnknown;
       *launches += archead_last_launches();
-      e = launch_softmax_grad(Y, targets + n0, nll + n0, lse + n0, dnll + n0, n, V, err, st,
-                              launches);
-      if (e == cudaSuccess)
-        e = launch_head_grad(Y, head, n, dnll + n0, dH + n0 * D, b + yoff, st, launches);
+      const HeadGrad a = {nullptr, Y, targets + n0, nll + n0, lse + n0, dnll + n0};
+      e = launch_head_grad(a, head, n, dH + n0 * D, b + yoff, err, st, launches);
     }
     return e;
   });
@@ -93,9 +97,15 @@ int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH,
   if (!dY || !dH) return ARCHEAD_ERR_NULLPTR;
   if (!aligned(dY, 4) || !aligned(dH, 16)) return ARCHEAD_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return with_scratch(head_grad_scratch_bytes(head, N), st,
+  const int64_t chunk = grad_chunk(N, V);
+  return with_scratch(chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
-    return launch_head_grad(dY, head, N, nullptr, dH, b, st, launches);
+    cudaError_t e = cudaSuccess;
+    for (int64_t n0 = 0; n0 < N && e == cudaSuccess; n0 += chunk) {
+      const HeadGrad a = {dY + n0 * V, nullptr, nullptr, nullptr, nullptr, nullptr};
+      e = launch_head_grad(a, head, std::min(chunk, N - n0), dH + n0 * D, b, err, st, launches);
+    }
+    return e;
   });
 }
 

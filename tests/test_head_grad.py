@@ -6,8 +6,13 @@ Tolerances, from the arithmetic.  A value is rounded to BF16 at the end (half a 
 relative).  Before that each dY entry and each low-rank factor entry is rounded once to FP16
 (2^-11 each) and sums are FP32: at most 2^-10 (1 + 2^-3) of sum_v |dY_v| |W|_vd, with |W| the
 sum of the magnitudes of the residual and of the factors' products.  nll_grad's dY comes from
-logits whose own error is bounded by 1e-4 max|Y| in the logits' tests, so that much more of
-each probability."""
+logits whose own error is bounded by 1e-4 max|Y| in the logits' tests, so that much
+more of each probability.
+FP16 also has a smallest step, 2^-24.  The product takes dY'[n, v] = dY[n, v] S'_v 2^e, S'_v the
+row's scale (row_scale below) and 2^e such that the largest possible entry, max|dY[n]| max S',
+lies between 2^12 and 2^14: half a step, 2^-25, is at most 2^-37 of that maximum, and it meets
+the entry W_vd / S'_v.  So 2^-37 max|dY[n]| sum_v |W|_vd max S' / S'_v comes to the bound: it shows
+only where everything larger in the row meets weights of exactly 0."""
 import ctypes
 import os
 
@@ -48,6 +53,24 @@ def magnitudes(head):
             M = M + np.abs(oracle.dequant_int8_rowwise(head[a], head["s" + a])) @ np.abs(
                 oracle.dequant_int8_groupwise(head[b], head["s" + b], head["g"]))
     return W, M
+
+
+def row_scale(head):
+    """S'_v: the scale in units of which a row of the head is held in FP16."""
+    if head.get("format") == "row8":
+        return head["row_scale"].astype(np.float64)
+    S = oracle.bf16_bits_to_f64(head["r_super"])
+    m = 128 * np.maximum(head["sAc"] * (head["r_c"] > 0), head["sAw"] * (head["r_r"] > 0)).astype(np.float64)
+    log = lambda x: np.floor(np.log2(np.where(x > 0, x, 1)))
+    k = np.maximum(log(m) - log(S) - 13, -3)
+    return np.where(m == 0, S, np.where((S == 0) | (k > 40), 2.0 ** (log(m) - 13), S * 2.0 ** k))
+
+
+def smallest_step(head, M, dY):
+    """The bound's last term, N x D."""
+    s = row_scale(head)
+    share = np.divide(s.max(), s, out=np.zeros_like(s), where=s > 0)
+    return 2.0 ** -37 * np.abs(dY.astype(np.float64)).max(1, keepdims=True) * (share @ M)
 
 
 def close(got, want, tol, what=""):
@@ -103,7 +126,8 @@ def test_logits_grad_matches_fp64(cuda_ok, name, N):
     got = ah.logits_grad(torch.from_numpy(dY).cuda(), dh)
     ah.check()
     want = dY.astype(np.float64) @ W
-    close(got, want, BF16 * np.abs(want) + PROD * (np.abs(dY).astype(np.float64) @ M), name)
+    close(got, want, BF16 * np.abs(want) + PROD * (np.abs(dY).astype(np.float64) @ M)
+          + smallest_step(head, M, dY), name)
 
 
 def nll_case(head, W, N, seed):
@@ -119,9 +143,10 @@ def nll_case(head, W, N, seed):
     return H, tg, Y, lse, P, dnll.astype(np.float32)
 
 
-def nll_tol(P, Y, M, dnll, want):
+def nll_tol(head, P, Y, M, dnll, want):
     d = np.abs(dnll.astype(np.float64))[:, None]
-    return BF16 * np.abs(want) + (PROD + 1e-4 * np.abs(Y).max()) * d * (np.abs(P) @ M)
+    return (BF16 * np.abs(want) + (PROD + 1e-4 * np.abs(Y).max()) * d * (np.abs(P) @ M)
+            + d * smallest_step(head, M, P))
 
 
 @pytest.mark.gpu
@@ -145,7 +170,7 @@ def test_nll_grad_matches_fp64(cuda_ok, name, N):
     got = ah.nll_grad(Hd, dh, t, nl, ls, dev)
     ah.check()
     want = dnll.astype(np.float64)[:, None] * (P @ W)
-    close(got, want, nll_tol(P, Y, M, dnll, want), name)
+    close(got, want, nll_tol(head, P, Y, M, dnll, want), name)
     assert not got[torch.from_numpy(masked).cuda()].any()
     assert torch.equal(got, ah.nll_grad(Hd, dh, t, nl, ls, dev))  # equal calls, equal bits
 
@@ -179,7 +204,7 @@ def test_nll_grad_of_confident_tokens(cuda_ok, N):
     # largest logit, so every probability by that much relative, and the target's entry
     # 1 - p by as much of p
     slip = 4 * 2.0 ** -24 * np.abs(Y).max(1)[:, None]
-    tol = nll_tol(P, Y, M, np.ones(N, np.float32), want) + 2 * slip * M[tg]
+    tol = nll_tol(head, P, Y, M, np.ones(N, np.float32), want) + 2 * slip * M[tg]
     close(got, want, tol)
     assert nl.min() < 1e-3  # such tokens were there
 
@@ -197,7 +222,7 @@ def test_nll_grad_against_differences(cuda_ok):
     ah.check()
     H64 = H.double().numpy()
     want = dnll.astype(np.float64)[:, None] * (P @ W)
-    tol = nll_tol(P, Y, M, dnll, want)
+    tol = nll_tol(head, P, Y, M, dnll, want)
     for seed in range(4):
         u = np.random.default_rng(seed).normal(size=H64.shape)
         f = [(dnll * oracle.nll_from_logits((H64 + s * u) @ W.T, tg)).sum() for s in (1e-5, -1e-5)]
@@ -320,7 +345,7 @@ def test_training_step_of_the_operators_together(cuda_ok, N):
         # dnll comes from FP32 NLLs off by up to 1e-4 max|Y| each (as logits are), which moves a
         # ratio, and a pair's score by the sum over its tokens, by that much relative
         slip = 1e-4 * np.abs(Y).max() * (2 if which == "policy" else 1 + 0.3 * N) * np.abs(d).max()
-        close(got, want, nll_tol(P, Y, M, d, want) + slip * (np.abs(P) @ M), which)
+        close(got, want, nll_tol(head, P, Y, M, d, want) + slip * (np.abs(P) @ M), which)
 
 
 @pytest.mark.gpu
