@@ -6,10 +6,13 @@
 // a = [Q8(A_c) | Q8(A_w)], b = [Q8(B_c) ; Q8(B_w)].  The long axis is the vocabulary, so the
 // packed head is the transposed operand: D[d, n] = sum_v A[v, d] B[n, v] with A the dequantised
 // head (vocabulary rows are K, its columns the 128 lanes of the accumulator) and B the FP16 image
-// of dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh).  u is one more tile of columns, A then
-// being a / S'.
+// of dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh).  u is one more tile of columns, whose A,
+// a / S', is prepared once per call in the layout of an A stage and copied (built from the INT8
+// rows in the product's loop it took three times as long as a residual tile and set the pace of
+// every round: N = 777, ranks 64 + 64: 3150 us against 760 us).
 //
-//  * grad_rows_kernel: S'_v per row and their maximum; clears the per-token maxima.
+//  * grad_rows_kernel: S'_v per row and their maximum, the factor image; clears the per-token
+//    maxima.
 //  * dy_amax_kernel, dy_image_kernel: the image, from dY or from logits (softmax gradient).
 //  * grad_tc_kernel: the product.  A work item is 256 columns (two accumulators of 128 lanes) x
 //    NT tokens x a slab of the vocabulary; its FP32 sums go to scratch.
@@ -36,33 +39,85 @@ struct RowsParams {
   float* spmax;      // kRowBlocks
   unsigned* amax;    // per token, cleared here (n), or nullptr
   int64_t n;
+  char* fimg;        // factor image, or nullptr without ranks
+  int fcols;         // its columns: r_c + r_r rounded up to 64
+  int a_words;       // factor rows readable as aligned 32-bit words
 };
 
-__global__ void __launch_bounds__(256) grad_rows_kernel(const RowsParams p) {
+// Four factor entries j .. j+3 of row v in [A_c | A_w], zeros past r_c + r_r.
+__device__ __forceinline__ uint32_t grad_factor_word(const archead_head& h, int a_words, int64_t v, int j) {
+  const int rc = h.r_c, rr = h.r_r;
+  if (a_words) {
+    if (j < rc) return __ldg(reinterpret_cast<const uint32_t*>(h.Ac + v * rc + j));
+    if (j < rc + rr) return __ldg(reinterpret_cast<const uint32_t*>(h.Aw + v * rr + (j - rc)));
+    return 0u;
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int jj = j + u;
+    int8_t b = 0;
+    if (jj < rc) b = __ldg(h.Ac + v * rc + jj);
+    else if (jj < rc + rr) b = __ldg(h.Aw + v * rr + (jj - rc));
+    w |= (uint32_t)(uint8_t)b << (8 * u);
+  }
+  return w;
+}
+
+__device__ __forceinline__ GradRow head_row(const archead_head& h, int64_t v, float* sac, float* saw) {
+  *sac = h.r_c ? __ldg(h.sAc + v) : 0.f;
+  *saw = h.r_r ? __ldg(h.sAw + v) : 0.f;
+  return grad_row(bf16_bits_to_float(__ldg(h.r_super + v)), *sac, *saw);
+}
+
+__global__ void __launch_bounds__(1024) grad_rows_kernel(const RowsParams p) {
   allow_dependent_launch();
-  __shared__ float red[8];
-  const int64_t t0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+  __shared__ float red[32];
+  const int64_t t0 = blockIdx.x * 1024ll + threadIdx.x, step = gridDim.x * 1024ll;
   float m = 0.f;
   for (int64_t v = t0; v < p.vpad; v += step) {
     float s = 0.f;
     if (v < p.h.V) {
-      if (p.h.format == ARCHEAD_FMT_ROW8)
-        s = p.h.row_scale[v];
-      else
-        s = grad_row(bf16_bits_to_float(p.h.r_super[v]), p.h.r_c ? p.h.sAc[v] : 0.f,
-                     p.h.r_r ? p.h.sAw[v] : 0.f).sp;
+      float sac, saw;
+      s = p.h.format == ARCHEAD_FMT_ROW8 ? p.h.row_scale[v] : head_row(p.h, v, &sac, &saw).sp;
     }
     p.sp[v] = s;
     m = fmaxf(m, fabsf(s));
   }
   if (p.amax)
     for (int64_t i = t0; i < p.n; i += step) p.amax[i] = 0u;
+  if (p.fimg) {  // eight factor entries of a row at a time
+    const int per = p.fcols >> 3;
+    for (int64_t i = t0; i < p.vpad * per; i += step) {
+      const int64_t v = i / per;
+      const int c = (int)(i - v * per), k = (int)(v & 63);
+      uint32_t o[4] = {0u, 0u, 0u, 0u};
+      if (v < p.h.V) {
+        float sac, saw;
+        const GradRow gr = head_row(p.h, v, &sac, &saw);
+        const float rcp = gr.sp != 0.f ? 1.f / gr.sp : 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j = 8 * c + 4 * q;
+          const uint32_t fw = grad_factor_word(p.h, p.a_words, v, j);
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = __fmul_rn((float)(int8_t)((fw >> (8 * e)) & 0xFFu), j + e < p.h.r_c ? sac : saw) * rcp;
+          o[2 * q] = h2_bits(__floats2half2_rn(x[0], x[1]));
+          o[2 * q + 1] = h2_bits(__floats2half2_rn(x[2], x[3]));
+        }
+      }
+      *reinterpret_cast<uint4*>(p.fimg + (v >> 6) * p.fcols * 128 + (c >> 3) * 8192 + (k >> 3) * 1024 +
+                                (k & 7) * 128 + (((c ^ k) & 7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+    for (int i = 1; i < 32; ++i) m = fmaxf(m, red[i]);
     p.spmax[blockIdx.x] = m;
   }
 }
@@ -193,7 +248,8 @@ struct GradParams {
   int ntiles;      // column tiles: ceil(D / 256), one more for the ranks
   int slabs;
   int g_shift;
-  int a_words;  // factor rows readable as aligned 32-bit words
+  const char* fimg;  // factor image: per 64 rows, fcols x 128 bytes
+  int fcols;
   unsigned* err;
 };
 
@@ -270,26 +326,6 @@ __device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t s
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
-}
-
-// Four factor entries j .. j+3 of row v in [A_c | A_w], zeros past r_c + r_r.
-__device__ __forceinline__ uint32_t grad_factor_word(const GradParams& p, int64_t v, int j) {
-  const int rc = p.h.r_c, rr = p.h.r_r;
-  if (p.a_words) {
-    if (j < rc) return __ldg(reinterpret_cast<const uint32_t*>(p.h.Ac + v * rc + j));
-    if (j < rc + rr) return __ldg(reinterpret_cast<const uint32_t*>(p.h.Aw + v * rr + (j - rc)));
-    return 0u;
-  }
-  uint32_t w = 0;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int jj = j + u;
-    int8_t b = 0;
-    if (jj < rc) b = __ldg(p.h.Ac + v * rc + jj);
-    else if (jj < rc + rr) b = __ldg(p.h.Aw + v * rr + (jj - rc));
-    w |= (uint32_t)(uint8_t)b << (8 * u);
-  }
-  return w;
 }
 
 // Scales and codes of one vocabulary row for one block of 128 columns (CPC codes).
@@ -372,21 +408,48 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     const int k = 32 * (rg & 1) + lane;  // row in the stage
     const uint32_t a_row = tc::smem_u32(As) + (uint32_t)(b * 2) * 8192 + (k >> 3) * 1024 + (k & 7) * 128;
     const uint32_t x7 = k & 7;
-    int64_t seq = 0;  // units so far
+    int64_t seq = 0;      // units so far
+    int64_t copied = -1;  // last stage copied from the factor image
     int ps = 0;
     uint32_t pp = 0;
     bool ok = true;
     for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+      if (it.rank) {
+        // Whole stages from the factor image, copied by one of the four warps of a half; the
+        // others only keep pace (a warp that skipped stages would lose count of the phases).
+        const uint32_t bytes = (uint32_t)p.fcols * 128u;
+        grid_dependency_wait();  // the image comes from a kernel before this one
+        for (int64_t u = it.u0; u < it.u1; ++u, ++seq) {
+          const int64_t ks = 2 * seq + h;
+          const int slot = (int)(ks % C::SA);
+          const int64_t use = ks / C::SA;
+          if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&a_empty[slot], (uint32_t)(use - 1) & 1u, p.err))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if ((warp & 5) == 0) {
+              tc::mbar_arrive_expect_tx(&a_full[slot], bytes);
+              tc::bulk_g2s(As + slot * kAStage, p.fimg + (2 * u + h) * bytes, bytes, &a_full[slot]);
+              copied = ks;
+            } else {
+              tc::mbar_arrive(&a_full[slot]);
+            }
+          }
+          __syncwarp();
+        }
+        continue;
+      }
       const bool work = b < it.nacc;
       const int64_t col = 256ll * it.dt + 128 * b;
-      RowLoad nx = load_grad_row<CPC>(p, it.u0 * kUnit + s, col, work && !it.rank);
+      RowLoad nx = load_grad_row<CPC>(p, it.u0 * kUnit + s, col, work);
       for (int64_t u = it.u0; u < it.u1; ++u, ++seq) {
         const RowLoad r = nx;
         const int64_t v = u * kUnit + s;
-        if (u + 1 < it.u1) nx = load_grad_row<CPC>(p, v + kUnit, col, work && !it.rank);
+        if (u + 1 < it.u1) nx = load_grad_row<CPC>(p, v + kUnit, col, work);
         uint32_t w[16];
         uint4 raw[8];
-        if (CPC != 0 && !it.rank) {
+        if (CPC != 0) {
           if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err))) {
             ok = false;
             break;
@@ -436,28 +499,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
                             h2_bits(bytes_to_half2(q[2 * e + 1], 0x4140)), h2_bits(bytes_to_half2(q[2 * e + 1], 0x4342)));
               }
             }
-          } else if (it.rank) {
-            const GradRow gr = grad_row(r.S, r.sac, r.saw);
-            const float rcp = gr.sp != 0.f ? 1.f / gr.sp : 0.f;
-            const int rc = p.h.r_c, RR = p.h.r_c + p.h.r_r;
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-              const int j0 = 128 * b + 8 * c;
-              uint32_t o[4] = {0u, 0u, 0u, 0u};
-              if (j0 < RR && v < p.h.V) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const uint32_t fw = grad_factor_word(p, v, j0 + 4 * q);
-                  float x[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    x[e] = __fmul_rn((float)(int8_t)((fw >> (8 * e)) & 0xFFu), j0 + 4 * q + e < rc ? r.sac : r.saw) * rcp;
-                  o[2 * q] = h2_bits(__floats2half2_rn(x[0], x[1]));
-                  o[2 * q + 1] = h2_bits(__floats2half2_rn(x[2], x[3]));
-                }
-              }
-              st_shared16(dst + (c >> 3) * 8192 + (((c & 7) ^ x7) << 4), o[0], o[1], o[2], o[3]);
-            }
           } else {
             const float cs = grad_row(r.S, r.sac, r.saw).cs;
 #pragma unroll
@@ -480,6 +521,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
         if (lane == 0) tc::mbar_arrive(&a_full[slot]);
       }
     }
+    if (!ok && copied >= 0)  // a copy may still be in flight
+      tc::mbar_wait(&a_full[copied % C::SA], (uint32_t)(copied / C::SA) & 1u, p.err);
   } else if (warp < kDequantWarps + 4) {
     // ---- epilogue: lane = column of the tile; raw sums to scratch ----
     const int e = warp - kDequantWarps;
@@ -720,7 +763,8 @@ int sm_count() {
 struct GradPlan {
   int nt, ntt, ntiles, slabs;
   int64_t npad, nunits, dp;
-  size_t o_img, o_sp, o_spmax, o_amax, o_texp, o_part, bytes;
+  int fcols;
+  size_t o_img, o_fimg, o_sp, o_spmax, o_amax, o_texp, o_part, bytes;
 };
 
 GradPlan grad_plan(const archead_head& h, int64_t n) {
@@ -755,6 +799,8 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
     return r;
   };
   g.o_img = take((size_t)g.npad * g.nunits * kUnit * 2);
+  g.fcols = (RR + 63) / 64 * 64;
+  g.o_fimg = take((size_t)g.nunits * kUnit * g.fcols * 2);
   g.o_sp = take((size_t)g.nunits * kUnit * 4);
   g.o_spmax = take(kRowBlocks * 4);
   g.o_amax = take((size_t)n * 4);
@@ -808,8 +854,10 @@ cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_
   float* spmax = reinterpret_cast<float*>(b + g.o_spmax);
   unsigned* amax = reinterpret_cast<unsigned*>(b + g.o_amax);
   int* texp = reinterpret_cast<int*>(b + g.o_texp);
-  const RowsParams rp = {*head, g.nunits * kUnit, sp, spmax, a.dY ? amax : nullptr, n};
-  grad_rows_kernel<<<kRowBlocks, 256, 0, st>>>(rp);
+  const RowsParams rp = {*head, g.nunits * kUnit, sp, spmax, a.dY ? amax : nullptr, n,
+                         g.fcols ? b + g.o_fimg : nullptr, g.fcols,
+                         head->r_c % 4 == 0 && head->r_r % 4 == 0};
+  grad_rows_kernel<<<kRowBlocks, 1024, 0, st>>>(rp);
   ++*launches;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -860,7 +908,8 @@ cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_
   int gs = 0;
   while ((1 << gs) < head->g) ++gs;
   p.g_shift = gs;
-  p.a_words = head->r_c % 4 == 0 && head->r_r % 4 == 0;
+  p.fimg = b + g.o_fimg;
+  p.fcols = g.fcols;
   p.err = err;
   switch (g.nt) {
     case 16: e = launch_grad_nt<16>(p, st); break;
