@@ -337,6 +337,45 @@ int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err) {
 
 void set_last_launches(int n) { t_last_launches = n; }
 
+// N <= 16 runs on the decode kernel, which writes logits
+bool tc_image_fits(const archead_head* head, const Shapes& s) {
+  return head->format == ARCHEAD_FMT_SC4 && s.N > 16 && tc_plan(s, 2).nt > 0;
+}
+
+int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, const TcImage& image,
+                 cudaStream_t st, int* launches) {
+  DeviceState* ds;
+  const int rc = current_state(&ds);
+  if (rc) return rc;
+  const TcPlan plan = tc_plan(s, 2);
+  const int64_t Npad = (s.N + plan.nt - 1) / plan.nt * plan.nt;
+  Carve cv;
+  const size_t o_hh = cv.take((size_t)Npad * (s.D + 128 * plan.nrb) * 2);
+  const size_t o_tsc = cv.take((size_t)s.N * 4);
+  const size_t split_bytes = tc_split_scratch_bytes(s, plan);
+  const size_t o_scr = split_bytes ? cv.take(split_bytes) : 0;
+  const size_t o_cnt = cv.take((size_t)((s.V + 127) / 128) * 4);
+  void* base = nullptr;
+  if (cudaMallocFromPoolAsync(&base, cv.off, ds->pool, st) != cudaSuccess) {
+    cudaGetLastError();
+    return ARCHEAD_ERR_NOMEM;
+  }
+  char* b = static_cast<char*>(base);
+  __half* Hh = reinterpret_cast<__half*>(b + o_hh);
+  float* tsc = reinterpret_cast<float*>(b + o_tsc);
+  unsigned* cnt = reinterpret_cast<unsigned*>(b + o_cnt);
+  cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches);
+  if (e == cudaSuccess) {
+    prof_mark(0, st);
+    e = launch_residual_tc(Hh, tsc, head, s, plan, nullptr, nullptr, nullptr, nullptr,
+                           split_bytes ? reinterpret_cast<float*>(b + o_scr) : nullptr, cnt,
+                           ds->err, st, launches, &image);
+    prof_mark(1, st);
+  }
+  cudaFreeAsync(base, st);
+  return e == cudaSuccess ? ARCHEAD_OK : ARCHEAD_ERR_CUDA;
+}
+
 // Device address of this device's error word (the device must be current).
 unsigned* error_word_address() {
   void* addr = nullptr;

@@ -174,7 +174,7 @@ struct TcPlan {
   int nrb;  // rank blocks after the nkb blocks of H
   int sp;   // stages of the shared-memory ring of packed blocks
 };
-TcPlan tc_plan(const Shapes& s, bool nll);
+TcPlan tc_plan(const Shapes& s, int mode);  // mode: 0 logits, 1 fused NLL, 2 gradient image
 // FP16 element offset of (token nn of token tile tt, column kk < 128 of block kb) in the
 // blocked image with nkbt blocks per token tile: two 64-column halves of nt rows x 128
 // bytes, the 16-byte chunk c of row nn stored at chunk c ^ (nn % 8) (the K-major 128-byte
@@ -200,11 +200,25 @@ size_t tc_split_scratch_bytes(const Shapes& s, const TcPlan& plan);
 // scratch / counters (tc_split_scratch_bytes, launch_prologue_blocked): the split of a
 // single token tile over the CTAs; with several token tiles, counters[0] is the work
 // counter from which the CTAs take their items in order (nullptr: a fixed round-robin).
+// image != nullptr: the softmax gradient's FP16 image instead (see grad_common.cuh).
+struct GradToken {  // what a token's entries of the image take
+  float lse;        // its log-sum-exp (NaN: its target is invalid)
+  float factor;     // 2^f
+  float at_target;  // the target's entry, exp(-nll) - 1
+  int32_t target;
+};
+struct TcImage {
+  char* img;
+  const float* snorm;  // per vocabulary row (padded to 128) S'_v 2^-es, 0 past V
+  const GradToken* tok;
+  int nt;  // token tile of the image
+};
 cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead_head* head,
                                const Shapes& s, const TcPlan& plan, float* Y,
                                const int32_t* targets,
                                float2* part, float* tlogit, float* scratch, unsigned* counters,
-                               unsigned* err, cudaStream_t st, int* launches);
+                               unsigned* err, cudaStream_t st, int* launches,
+                               const TcImage* image = nullptr);
 
 // Decode path (N <= 16): persistent bulk-copy-fed warp-MMA kernel with H resident in
 // shared memory.  nt8 = 0 when the shape does not fit (then the token-block kernel runs).
@@ -278,19 +292,32 @@ cudaError_t launch_nll_merge(const float* partials, int G, int64_t N, float* nll
 cudaError_t launch_repack(const uint8_t* canon, uint8_t* dev, int64_t V, int64_t D,
                           cudaStream_t st);
 
-// Gradient product dH = dY W through the packed head for n tokens (csrc/grad_tc.cu).  dY comes
-// as it is, or from logits as dY[n, v] = exp(Y[n, v] - lse[n]) - [v = targets[n]] with the
-// target's entry taken from its NLL (exp(-nll) - 1); row n of the product is multiplied by
-// dnll[n] (nullptr: 1) and is zero where that is.  scratch: head_grad_scratch_bytes.
+// Gradient product dH = dY W through the packed head for n tokens (csrc/grad_tc.cu), in steps:
+//  1. grad_rows: the head's row scales and factor operand into the scratch;
+//  2. the FP16 image of dY: grad_image_dy from dY itself, or from the logits with dY[n, v] =
+//     exp(Y[n, v] - lse[n]) - [v = targets[n]] (the target's entry from its NLL, exp(-nll) - 1):
+//     grad_image_softmax from logits in memory, or grad_tokens, whose TcImage the tcgen05 logits
+//     kernel then fills;
+//  3. grad_product: row n times dnll[n] (nullptr: 1), zero where that is 0.
+// scratch: head_grad_scratch_bytes, the same for all steps.
 struct HeadGrad {
-  const float* dY;      // n x V, or nullptr:
-  const float* logits;  // n x V
+  const archead_head* head;
+  int64_t n;
+  char* scratch;
+  unsigned* err;
+  cudaStream_t st;
+  int* launches;
+};
+struct SoftmaxTokens {
   const int32_t* targets;
   const float *nll, *lse, *dnll;
 };
 size_t head_grad_scratch_bytes(const archead_head* head, int64_t n);
-cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_t n, uint16_t* dH,
-                             void* scratch, unsigned* err, cudaStream_t st, int* launches);
+cudaError_t grad_rows(const HeadGrad& a, bool dy);  // dy: grad_image_dy follows
+cudaError_t grad_image_dy(const HeadGrad& a, const float* dY);
+cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const SoftmaxTokens& t);
+cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image);
+cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH);
 
 // Losses on per-token NLLs (csrc/losses.cu).
 struct PolicyArgs {
@@ -321,6 +348,11 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsig
 // pool (none for 0 bytes); freed with cudaFreeAsync on the same stream.
 int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err);
 void set_last_launches(int n);
+// Logits of N tokens straight into the softmax gradient's image by the tcgen05 kernel.  One
+// launch sequence on st with scratch of its own; tc_image_fits says whether the shape runs there.
+bool tc_image_fits(const archead_head* head, const Shapes& s);
+int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, const TcImage& image,
+                 cudaStream_t st, int* launches);
 int validate_head_args(const archead_head* head, int64_t N, int64_t V, int64_t D, int r_c,
                        int r_r, int g);
 unsigned* error_word_address();

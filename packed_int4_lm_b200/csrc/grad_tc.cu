@@ -133,20 +133,25 @@ __device__ __forceinline__ int spmax_exp(const float* spmax) {
 }
 
 // Per token the largest |dY| (as bits: a NaN is the largest), one warp per 2048 entries.
-__global__ void __launch_bounds__(256) dy_amax_kernel(const float* __restrict__ dY, int64_t n,
-                                                      int64_t V, unsigned* amax) {
+struct AmaxParams {
+  const float* dY;
+  int64_t n, V;
+  unsigned* amax;
+};
+__global__ void __launch_bounds__(256) dy_amax_kernel(const AmaxParams p) {
+  const int64_t V = p.V;
   allow_dependent_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t per = (V + 2047) / 2048, total = per * n;
+  const int64_t per = (V + 2047) / 2048, total = per * p.n;
   for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < total; i += gridDim.x * 8ll) {
     const int64_t t = i / per, v0 = (i - t * per) * 2048;
     const int64_t v1 = v0 + 2048 < V ? v0 + 2048 : V;
     unsigned m = 0;
     for (int64_t v = v0 + lane; v < v1; v += 32)
-      m = max(m, __float_as_uint(dY[t * V + v]) & 0x7fffffffu);
+      m = max(m, __float_as_uint(__ldg(p.dY + t * V + v)) & 0x7fffffffu);
     m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) atomicMax(amax + t, m);
+    if (lane == 0) atomicMax(p.amax + t, m);
   }
 }
 
@@ -157,11 +162,7 @@ struct ImageParams {
   const float* sp;
   const float* spmax;
   const unsigned* amax;  // dY: per-token maxima
-  // logits: dY = exp(Y - lse) - [v = target], the target's entry from its NLL
-  const int32_t* targets;
-  const float* nll;
-  const float* lse;
-  const float* dnll;
+  SoftmaxTokens t;       // logits: dY = exp(Y - lse) - [v = target]
   char* img;
   int* texp;  // per token: dH = 2^texp times the product
   unsigned* err;
@@ -177,6 +178,37 @@ __device__ __forceinline__ int dy_exp(unsigned amax) {
 __device__ __forceinline__ int softmax_exp(float nll, float lse) {
   const float b = fmaxf(fmaxf(-expm1f(-nll), 0x1p-18f), fabsf(lse) * 0x1p-21f);
   return b <= 3.402823466e38f ? 12 - ilogbf(b) : 0;
+}
+
+// What the tcgen05 logits kernel needs to write the image itself: the row scales in units of the
+// largest, and per token a GradToken (and texp).
+struct TokensParams {
+  int64_t n, V, vpad;
+  const float* sp;
+  const float* spmax;
+  SoftmaxTokens t;
+  float* snorm;
+  GradToken* tok;
+  int* texp;
+  unsigned* err;
+};
+__global__ void __launch_bounds__(256) grad_tokens_kernel(const TokensParams p) {
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int es = spmax_exp(p.spmax);
+  float e0, e1;
+  pow2_pair(-es, &e0, &e1);
+  const int64_t i0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+  for (int64_t v = i0; v < p.vpad; v += step) p.snorm[v] = p.sp[v] * e0 * e1;
+  for (int64_t n = i0; n < p.n; n += step) {
+    const float nll = p.t.nll[n], lse = p.t.lse[n];
+    const int32_t t = p.t.targets[n];
+    const bool bad = (t < 0 || t >= p.V) && p.t.dnll[n] != 0.f;
+    if (bad) atomicOr(p.err, kErrTarget);
+    const int f = softmax_exp(nll, lse);
+    p.tok[n] = GradToken{bad ? __int_as_float(0x7fc00000) : lse, ldexpf(1.f, f), expm1f(-nll), t};
+    p.texp[n] = es - f;
+  }
 }
 
 // One warp per 64 vocabulary rows and group of 32 tokens: each lane two rows, one 128-byte
@@ -196,9 +228,9 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   bool bad = false;
   if (mine < p.n) {
     if (kSoftmax) {
-      const int32_t t = p.targets[mine];
-      f = softmax_exp(p.nll[mine], p.lse[mine]);
-      bad = (t < 0 || t >= p.V) && p.dnll[mine] != 0.f;
+      const int32_t t = p.t.targets[mine];
+      f = softmax_exp(p.t.nll[mine], p.t.lse[mine]);
+      bad = (t < 0 || t >= p.V) && p.t.dnll[mine] != 0.f;
     } else {
       f = dy_exp(p.amax[mine]);
     }
@@ -221,10 +253,10 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
       if (v < p.V) y0 = row[v];
       if (v + 1 < p.V) y1 = row[v + 1];
       if (kSoftmax) {
-        const float l = bk ? __int_as_float(0x7fc00000) : p.lse[n];
-        const int64_t t = p.targets[n];
-        y0 = v < p.V ? (v == t ? expm1f(-p.nll[n]) : expf(y0 - l)) : 0.f;
-        y1 = v + 1 < p.V ? (v + 1 == t ? expm1f(-p.nll[n]) : expf(y1 - l)) : 0.f;
+        const float l = bk ? __int_as_float(0x7fc00000) : p.t.lse[n];
+        const int64_t t = p.t.targets[n];
+        y0 = v < p.V ? (v == t ? expm1f(-p.t.nll[n]) : expf(y0 - l)) : 0.f;
+        y1 = v + 1 < p.V ? (v + 1 == t ? expm1f(-p.t.nll[n]) : expf(y1 - l)) : 0.f;
       }
       float a, b;
       pow2_pair(fk, &a, &b);
@@ -764,7 +796,7 @@ struct GradPlan {
   int nt, ntt, ntiles, slabs;
   int64_t npad, nunits, dp;
   int fcols;
-  size_t o_img, o_fimg, o_sp, o_spmax, o_amax, o_texp, o_part, bytes;
+  size_t o_img, o_fimg, o_sp, o_snorm, o_spmax, o_amax, o_texp, o_tok, o_part, bytes;
 };
 
 GradPlan grad_plan(const archead_head& h, int64_t n) {
@@ -802,9 +834,11 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   g.fcols = (RR + 63) / 64 * 64;
   g.o_fimg = take((size_t)g.nunits * kUnit * g.fcols * 2);
   g.o_sp = take((size_t)g.nunits * kUnit * 4);
+  g.o_snorm = take((size_t)g.nunits * kUnit * 4);
   g.o_spmax = take(kRowBlocks * 4);
   g.o_amax = take((size_t)n * 4);
   g.o_texp = take((size_t)n * 4);
+  g.o_tok = take((size_t)n * sizeof(GradToken));
   g.o_part = take((size_t)g.slabs * n * g.dp * 4);
   g.bytes = o;
   return g;
@@ -842,89 +876,90 @@ cudaError_t launch_grad_nt(const GradParams& p, cudaStream_t st) {
   return launch_grad_cfg<NT, 1>(p, st);
 }
 
+struct GradParts {
+  char *img, *fimg;
+  float *sp, *snorm, *spmax;
+  unsigned* amax;
+  int* texp;
+  GradToken* tok;
+  float* part;
+};
+GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
+  char* b = a.scratch;
+  return {b + g.o_img, b + g.o_fimg, reinterpret_cast<float*>(b + g.o_sp),
+          reinterpret_cast<float*>(b + g.o_snorm), reinterpret_cast<float*>(b + g.o_spmax),
+          reinterpret_cast<unsigned*>(b + g.o_amax), reinterpret_cast<int*>(b + g.o_texp),
+          reinterpret_cast<GradToken*>(b + g.o_tok), reinterpret_cast<float*>(b + g.o_part)};
+}
+
+cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
+  const GradPlan g = grad_plan(*a.head, a.n);
+  const GradParts b = grad_parts(a, g);
+  const ImageParams p = {src, a.n, g.npad, a.head->V, g.nt, b.sp, b.spmax, b.amax,
+                         t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
+  const dim3 grid((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + 31) / 32));
+  ++*a.launches;
+  return t ? launch_pdl(dy_image_kernel<true>, grid, 256, 0, a.st, p)
+           : launch_pdl(dy_image_kernel<false>, grid, 256, 0, a.st, p);
+}
+
 }  // namespace
 
 size_t head_grad_scratch_bytes(const archead_head* head, int64_t n) { return grad_plan(*head, n).bytes; }
 
-cudaError_t launch_head_grad(const HeadGrad& a, const archead_head* head, int64_t n, uint16_t* dH,
-                             void* scratch, unsigned* err, cudaStream_t st, int* launches) {
-  const GradPlan g = grad_plan(*head, n);
-  char* b = static_cast<char*>(scratch);
-  float* sp = reinterpret_cast<float*>(b + g.o_sp);
-  float* spmax = reinterpret_cast<float*>(b + g.o_spmax);
-  unsigned* amax = reinterpret_cast<unsigned*>(b + g.o_amax);
-  int* texp = reinterpret_cast<int*>(b + g.o_texp);
-  const RowsParams rp = {*head, g.nunits * kUnit, sp, spmax, a.dY ? amax : nullptr, n,
-                         g.fcols ? b + g.o_fimg : nullptr, g.fcols,
-                         head->r_c % 4 == 0 && head->r_r % 4 == 0};
-  grad_rows_kernel<<<kRowBlocks, 1024, 0, st>>>(rp);
-  ++*launches;
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.dY) {
-    const int64_t blocks = ((head->V + 2047) / 2048 * n + 7) / 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, dy_amax_kernel, a.dY, n, head->V, amax)) != cudaSuccess) return e;
-    ++*launches;
-  }
-  ImageParams ip;
-  ip.src = a.dY ? a.dY : a.logits;
-  ip.n = n;
-  ip.npad = g.npad;
-  ip.V = head->V;
-  ip.nt = g.nt;
-  ip.sp = sp;
-  ip.spmax = spmax;
-  ip.amax = amax;
-  ip.targets = a.targets;
-  ip.nll = a.nll;
-  ip.lse = a.lse;
-  ip.dnll = a.dnll;
-  ip.img = b + g.o_img;
-  ip.texp = texp;
-  ip.err = err;
-  const dim3 ig((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + 31) / 32));
-  e = a.dY ? launch_pdl(dy_image_kernel<false>, ig, 256, 0, st, ip)
-           : launch_pdl(dy_image_kernel<true>, ig, 256, 0, st, ip);
-  if (e != cudaSuccess) return e;
-  GradParams p;
-  p.h = *head;
-  p.img = ip.img;
-  p.part = reinterpret_cast<float*>(b + g.o_part);
-  p.n = n;
-  p.dp = g.dp;
-  p.nunits = g.nunits;
-  p.ntt = g.ntt;
-  p.ntiles = g.ntiles;
-  p.slabs = g.slabs;
+cudaError_t grad_rows(const HeadGrad& a, bool dy) {
+  const archead_head& h = *a.head;
+  const GradPlan g = grad_plan(h, a.n);
+  const GradParts b = grad_parts(a, g);
+  const RowsParams p = {h, g.nunits * kUnit, b.sp, b.spmax, dy ? b.amax : nullptr, a.n,
+                        g.fcols ? b.fimg : nullptr, g.fcols, h.r_c % 4 == 0 && h.r_r % 4 == 0};
+  grad_rows_kernel<<<kRowBlocks, 1024, 0, a.st>>>(p);
+  ++*a.launches;
+  return cudaGetLastError();
+}
+
+cudaError_t grad_image_dy(const HeadGrad& a, const float* dY) {
+  const GradParts b = grad_parts(a, grad_plan(*a.head, a.n));
+  const int64_t blocks = ((a.head->V + 2047) / 2048 * a.n + 7) / 8;
+  const AmaxParams p = {dY, a.n, a.head->V, b.amax};
+  const cudaError_t e = launch_pdl(dy_amax_kernel, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)), 256, 0, a.st, p);
+  ++*a.launches;
+  return e == cudaSuccess ? grad_image(a, dY, nullptr) : e;
+}
+
+cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const SoftmaxTokens& t) {
+  return grad_image(a, logits, &t);
+}
+
+cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image) {
+  const GradPlan g = grad_plan(*a.head, a.n);
+  const GradParts b = grad_parts(a, g);
+  const TokensParams p = {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.snorm, b.tok, b.texp, a.err};
+  *image = TcImage{b.img, b.snorm, b.tok, g.nt};
+  ++*a.launches;
+  return launch_pdl(grad_tokens_kernel, dim3(148), 256, 0, a.st, p);
+}
+
+cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
+  const archead_head& h = *a.head;
+  const GradPlan g = grad_plan(h, a.n);
+  const GradParts b = grad_parts(a, g);
   int gs = 0;
-  while ((1 << gs) < head->g) ++gs;
-  p.g_shift = gs;
-  p.fimg = b + g.o_fimg;
-  p.fcols = g.fcols;
-  p.err = err;
+  while ((1 << gs) < h.g) ++gs;
+  const GradParams p = {h, b.img, b.part, a.n, g.dp, g.nunits, g.ntt, g.ntiles, g.slabs, gs, b.fimg, g.fcols, a.err};
+  cudaError_t e;
   switch (g.nt) {
-    case 16: e = launch_grad_nt<16>(p, st); break;
-    case 32: e = launch_grad_nt<32>(p, st); break;
-    case 64: e = launch_grad_nt<64>(p, st); break;
-    case 128: e = launch_grad_nt<128>(p, st); break;
-    default: e = launch_grad_nt<256>(p, st); break;
+    case 16: e = launch_grad_nt<16>(p, a.st); break;
+    case 32: e = launch_grad_nt<32>(p, a.st); break;
+    case 64: e = launch_grad_nt<64>(p, a.st); break;
+    case 128: e = launch_grad_nt<128>(p, a.st); break;
+    default: e = launch_grad_nt<256>(p, a.st); break;
   }
   if (e != cudaSuccess) return e;
-  const int RR = head->r_c + head->r_r;
-  const FinishParams fp = {*head, p.part, n, g.dp, g.slabs, texp, a.dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
-  e = launch_pdl(grad_finish_kernel, dim3((unsigned)((n + 15) / 16), (unsigned)((head->D + 255) / 256)), 128,
-                 (size_t)RR * 64, st, fp);
-  *launches += 3;
-  return e;
+  const FinishParams fp = {h, b.part, a.n, g.dp, g.slabs, b.texp, dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
+  *a.launches += 2;
+  return launch_pdl(grad_finish_kernel, dim3((unsigned)((a.n + 15) / 16), (unsigned)((h.D + 255) / 256)), 128,
+                    (size_t)(h.r_c + h.r_r) * 64, a.st, fp);
 }
 
 }  // namespace archead

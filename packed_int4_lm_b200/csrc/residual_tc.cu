@@ -33,7 +33,8 @@
 //    accumulator (two of them below NT = 128, so the next item's MMAs overlap the
 //    previous item's epilogue);
 //  * warps 4-7 (epilogue): tcgen05.ld of an accumulator row, times S'_v, stored into Y, or
-//    reduced on chip into split-vocabulary log-sum-exp partials (fused NLL).
+//    reduced on chip into split-vocabulary log-sum-exp partials (fused NLL), or turned into
+//    the softmax gradient's FP16 image (the operand of the gradient product, MODE 2).
 // Scheduling: with a single token tile (decode) the (tile, K block) units are split evenly
 // over the CTAs and a tile at the edge of two ranges is finished from two partial
 // accumulators; otherwise the CTAs take items in order (the token tile varying fastest
@@ -43,6 +44,7 @@
 // vocabulary tile find its packed blocks in L2.
 // Every mbarrier wait is bounded (about a second of SM cycles); a wait that gives up sets
 // the device error word, the CTA drains what it issued and frees its tensor memory.
+#include "grad_common.cuh"
 #include "tc_common.cuh"
 
 namespace archead {
@@ -93,6 +95,7 @@ struct TcParams {
   float* scratch;
   unsigned* counters;
   unsigned* err;
+  TcImage image;  // MODE 2
 };
 
 template <int NT>
@@ -124,11 +127,18 @@ constexpr size_t nll_scratch_bytes() {
   return (size_t)16 * 128 * 4 + (size_t)NT * 4;
 }
 
+// shared memory of the epilogue by MODE: nothing, the fused NLL's scratch, or a GradToken per
+// token
 template <int NT>
-size_t tc_smem_bytes(int sb, int sp, int G, bool nll) {
+constexpr size_t mode_scratch_bytes(int mode) {
+  return mode == 1 ? nll_scratch_bytes<NT>() : (mode == 2 ? (size_t)NT * sizeof(GradToken) : 0);
+}
+
+template <int NT>
+size_t tc_smem_bytes(int sb, int sp, int G, int mode) {
   using C = TcCfg<NT>;
   return (size_t)sb * C::HSTAGE + (size_t)sp * kPkBytes + 2 * round16((size_t)128 * G) +
-         (nll ? nll_scratch_bytes<NT>() : 0) + (size_t)NT * 4 + 1024;
+         mode_scratch_bytes<NT>(mode) + (size_t)NT * 4 + 1024;
 }
 
 // The k-th work item of this CTA: its tile's first row, its row limit, its token tile.
@@ -304,7 +314,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
   unsigned char* after_codes = cds + 2 * round16(code_bytes);
   float* nll_y = reinterpret_cast<float*>(after_codes);  // [16][128]
   int32_t* tgt_s = reinterpret_cast<int32_t*>(nll_y + 16 * 128);  // [NT]
-  float* tsc_s = reinterpret_cast<float*>(after_codes + (MODE ? nll_scratch_bytes<NT>() : 0));
+  GradToken* gtok_s = reinterpret_cast<GradToken*>(after_codes);  // MODE 2: [NT]
+  float* tsc_s = reinterpret_cast<float*>(after_codes + mode_scratch_bytes<NT>(MODE));
   uint64_t* bars = reinterpret_cast<uint64_t*>(tsc_s + NT);  // tsc_s: [NT] token scales
   uint64_t* b_full = bars;
   uint64_t* b_empty = b_full + kMaxSB;
@@ -713,6 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
         if (e < NT) {
           if (MODE == 1) tgt_s[e] = tok0 + e < p.N ? __ldg(p.targets + tok0 + e) : -1;
+          if (MODE == 2 && tok0 + e < p.N) gtok_s[e] = p.image.tok[tok0 + e];
           tsc_s[e] = tok0 + e < p.N ? __ldg(p.tsc + tok0 + e) : 1.f;
         }
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
@@ -721,6 +733,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
       const int64_t v = it.row0 + e;
       const bool live = v < it.row_end;
       const float sp = row_scale(load_row(p, v)).sp;  // loads overlap the wait below
+      const float gs = MODE == 2 ? __ldg(p.image.snorm + v) : 0.f;  // (0 past V)
       // one outcome for all four epilogue warps: they share named barriers below
       if (!tc::bar_and(1, 128, tc::mbar_wait(&acc_full[ab], use & 1, p.err))) break;
       tc::fence_after_sync();
@@ -813,6 +826,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
                 if (q < nq) __stcs(yp, y[q]);  // streaming: Y does not displace the B image
                 yp += p.V;
               }
+            }
+          } else if (MODE == 2) {
+            // softmax gradient: (exp(y - lse) - [v = target]) 2^f S'_v 2^-es, rounded to FP16 at
+            // its place in the image.  __expf: its error grows with the exponent but stays below
+            // 2^-18 for probabilities above 2^-40, far inside the rounding to FP16.
+            const int64_t t16 = tok0 + 16 * c16;
+            const int64_t nq = p.N - t16;
+            const int64_t gt = t16 / p.image.nt;
+            const int r = (int)(v & 63);
+            char* base = p.image.img + ((gt * 2 * p.n_vtiles + (v >> 6)) * p.image.nt + (t16 - gt * p.image.nt)) * 128 + 2 * (r & 7);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const GradToken g = gtok_s[16 * c16 + q];
+              float x = __expf(y[q] - g.lse);
+              if (v == g.target) x = g.at_target;
+              x = live ? x * g.factor * gs : 0.f;
+              if (q < nq)  // (t16 is a multiple of 16, so the token's place mod 8 is q mod 8)
+                *reinterpret_cast<__half*>(base + q * 128 + ((((r >> 3) ^ q) & 7) << 4)) = __float2half_rn(x);
             }
           } else {
             // ---- fused NLL: per token of the chunk, (max, sum exp) over the tile's rows ----
@@ -936,7 +967,7 @@ int tc_residency(const cudaFuncAttributes& fa, size_t smem, int tmem_cols, int r
 
 template <int NT, int CPC, int MODE>
 cudaError_t launch_tc_cfg(const TcParams& p, cudaStream_t st) {
-  const size_t smem = tc_smem_bytes<NT>(p.sb, p.spk, (int)(p.D >> p.g_shift), MODE == 1);
+  const size_t smem = tc_smem_bytes<NT>(p.sb, p.spk, (int)(p.D >> p.g_shift), MODE);
   auto kern = residual_tc_kernel<NT, CPC, MODE>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -978,16 +1009,16 @@ cudaError_t launch_tc_mode(const TcParams& p, int nt, int g, cudaStream_t st) {
 
 // First (B stages, packed stages) pair whose shared memory fits the budget; nt = 0 if none.
 template <int NT>
-TcPlan fit_rings(const int (*pairs)[2], int npairs, int G, bool nll, size_t budget) {
+TcPlan fit_rings(const int (*pairs)[2], int npairs, int G, int mode, size_t budget) {
   for (int i = 0; i < npairs; ++i)
-    if (tc_smem_bytes<NT>(pairs[i][0], pairs[i][1], G, nll) <= budget)
+    if (tc_smem_bytes<NT>(pairs[i][0], pairs[i][1], G, mode) <= budget)
       return TcPlan{NT, pairs[i][0], 0, pairs[i][1]};
   return TcPlan{0, 0, 0, 0};
 }
 
 }  // namespace
 
-TcPlan tc_plan(const Shapes& s, bool nll) {
+TcPlan tc_plan(const Shapes& s, int mode) {
   // Shared memory per SM is 228 KB with 1 KB reserved per CTA: two CTAs per SM take at
   // most 113 KB each.
   const size_t two_per_sm = 228 * 1024 / 2 - 1024;
@@ -995,15 +1026,15 @@ TcPlan tc_plan(const Shapes& s, bool nll) {
   TcPlan pl = {0, 0, 0, 0};
   if (s.N > 64) {
     static const int p128[][2] = {{2, 4}, {2, 3}, {2, 2}};
-    pl = fit_rings<128>(p128, 3, G, nll, two_per_sm);
+    pl = fit_rings<128>(p128, 3, G, mode, two_per_sm);
   }
   if (!pl.nt) {
     static const int p16[][2] = {{8, 6}, {7, 6}, {6, 6}, {5, 6}, {4, 6}, {3, 6}, {2, 6}, {2, 4}};
     static const int p32[][2] = {{6, 6}, {5, 6}, {4, 6}, {3, 6}, {2, 6}, {2, 4}};
     static const int p64[][2] = {{4, 4}, {3, 4}, {2, 4}};
-    if (s.N <= 16) pl = fit_rings<16>(p16, 8, G, nll, two_per_sm);
-    else if (s.N <= 32) pl = fit_rings<32>(p32, 6, G, nll, two_per_sm);
-    else pl = fit_rings<64>(p64, 3, G, nll, two_per_sm);
+    if (s.N <= 16) pl = fit_rings<16>(p16, 8, G, mode, two_per_sm);
+    else if (s.N <= 32) pl = fit_rings<32>(p32, 6, G, mode, two_per_sm);
+    else pl = fit_rings<64>(p64, 3, G, mode, two_per_sm);
   }
   pl.nrb = (s.r_c + s.r_r + 31) / 32;
   return pl;
@@ -1039,8 +1070,10 @@ cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead
                                const Shapes& s, const TcPlan& plan, float* Y,
                                const int32_t* targets,
                                float2* part, float* tlogit, float* scratch, unsigned* counters,
-                               unsigned* err, cudaStream_t st, int* launches) {
+                               unsigned* err, cudaStream_t st, int* launches,
+                               const TcImage* image) {
   TcParams p;
+  p.image = image ? *image : TcImage{};
   p.Hb = Hb;
   p.tsc = tsc;
   p.nib = head->r_nib;
@@ -1085,8 +1118,9 @@ cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead
   p.counters = counters;
   if (plan.nt == 0 || plan.sb < 2 || plan.sb > kMaxSB || plan.sp < 2 || plan.sp > kMaxSP)
     return cudaErrorInvalidValue;
-  cudaError_t e = Y ? launch_tc_mode<0>(p, plan.nt, s.g, st)
-                    : launch_tc_mode<1>(p, plan.nt, s.g, st);
+  cudaError_t e = image ? launch_tc_mode<2>(p, plan.nt, s.g, st)
+                  : Y   ? launch_tc_mode<0>(p, plan.nt, s.g, st)
+                        : launch_tc_mode<1>(p, plan.nt, s.g, st);
   ++*launches;
   return e;
 }

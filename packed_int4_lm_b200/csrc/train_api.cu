@@ -13,12 +13,13 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Tokens per chunk of the gradients: about 2 GB of scratch for FP32 logits, whole token tiles of
-// the product where that allows, and at most 65536 (the kernels' grids).
+// Tokens per chunk of the gradients: about 2 GB of scratch for the FP16 image (and FP32 logits,
+// where those go through memory), whole token tiles of the product where that allows, and at
+// most 65536 (the kernels' grids).
 constexpr int64_t kChunkBytes = 2ll << 30;
 
-int64_t grad_chunk(int64_t N, int64_t V) {
-  const int64_t c = std::min<int64_t>(std::max<int64_t>(kChunkBytes / (V * 4), 1), 65536);
+int64_t grad_chunk(int64_t N, int64_t V, int bytes) {
+  const int64_t c = std::min<int64_t>(std::max<int64_t>(kChunkBytes / (V * bytes), 1), 65536);
   return std::min(N, c >= 256 ? c / 256 * 256 : c);
 }
 // The last chunk is shorter and may be split otherwise.
@@ -32,15 +33,16 @@ template <typename F>
 int with_scratch(size_t bytes, cudaStream_t st, F launch) {
   void* base;
   unsigned* err;
-  const int rc = take_scratch(bytes, st, &base, &err);
+  int rc = take_scratch(bytes, st, &base, &err);
   if (rc) return rc;
   int launches = 0;
-  const cudaError_t e = launch(static_cast<char*>(base), err, &launches);
+  rc = launch(static_cast<char*>(base), err, &launches);
   if (base) cudaFreeAsync(base, st);
-  if (e != cudaSuccess) return ARCHEAD_ERR_CUDA;
-  set_last_launches(launches);
-  return ARCHEAD_OK;
+  if (rc == ARCHEAD_OK) set_last_launches(launches);
+  return rc;
 }
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? ARCHEAD_OK : ARCHEAD_ERR_CUDA; }
 
 int check_tokens(const int32_t* cu, const float* const* f, int nf, int64_t N, int64_t B) {
   if (N < 0 || N > 0x7fffffffLL || B < 0 || B >= 0x7fffffffLL) return ARCHEAD_ERR_SHAPE;
@@ -68,21 +70,36 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
       !aligned(lse, 4) || !aligned(dnll, 4))
     return ARCHEAD_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t chunk = grad_chunk(N, V);
-  const size_t yb = (size_t)chunk * V * 4, yoff = (yb + 255) / 256 * 256;
+  // the tcgen05 kernel writes the image itself; the others leave logits in memory
+  Shapes s = {N, V, D, r_c, r_r, g};
+  const bool fused = tc_image_fits(head, s);
+  const int64_t chunk = grad_chunk(N, V, fused ? 2 : 6);
+  const size_t yb = fused ? 0 : (size_t)chunk * V * 4, yoff = (yb + 255) / 256 * 256;
   return with_scratch(yoff + chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
     float* Y = reinterpret_cast<float*>(b);
-    cudaError_t e = cudaSuccess;
-    for (int64_t n0 = 0; n0 < N && e == cudaSuccess; n0 += chunk) {
-      const int64_t n = std::min(chunk, N - n0);
-      if (archead_logits(H + n0 * D, head, Y, n, V, D, r_c, r_r, g, stream) != ARCHEAD_OK)
-        return cudaErrorUnknown;
-      *launches += archead_last_launches();
-      const HeadGrad a = {nullptr, Y, targets + n0, nll + n0, lse + n0, dnll + n0};
-      e = launch_head_grad(a, head, n, dH + n0 * D, b + yoff, err, st, launches);
+    for (int64_t n0 = 0; n0 < N; n0 += chunk) {
+      s.N = std::min(chunk, N - n0);
+      const HeadGrad a = {head, s.N, b + yoff, err, st, launches};
+      const SoftmaxTokens t = {targets + n0, nll + n0, lse + n0, dnll + n0};
+      if (grad_rows(a, false) != cudaSuccess) return static_cast<int>(ARCHEAD_ERR_CUDA);
+      if (fused && tc_image_fits(head, s)) {
+        TcImage image;
+        if (grad_tokens(a, t, &image) != cudaSuccess)
+          return static_cast<int>(ARCHEAD_ERR_CUDA);
+        const int rc = run_tc_image(H + n0 * D, head, s, image, st, launches);
+        if (rc) return rc;
+      } else {
+        const int rc = archead_logits(H + n0 * D, head, Y, s.N, V, D, r_c, r_r, g, stream);
+        if (rc) return rc;
+        *launches += archead_last_launches();
+        if (grad_image_softmax(a, Y, t) != cudaSuccess)
+          return static_cast<int>(ARCHEAD_ERR_CUDA);
+      }
+      if (grad_product(a, dnll + n0, dH + n0 * D) != cudaSuccess)
+        return static_cast<int>(ARCHEAD_ERR_CUDA);
     }
-    return e;
+    return static_cast<int>(ARCHEAD_OK);
   });
 }
 
@@ -97,15 +114,17 @@ int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH,
   if (!dY || !dH) return ARCHEAD_ERR_NULLPTR;
   if (!aligned(dY, 4) || !aligned(dH, 16)) return ARCHEAD_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t chunk = grad_chunk(N, V);
+  const int64_t chunk = grad_chunk(N, V, 2);
   return with_scratch(chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
-    cudaError_t e = cudaSuccess;
-    for (int64_t n0 = 0; n0 < N && e == cudaSuccess; n0 += chunk) {
-      const HeadGrad a = {dY + n0 * V, nullptr, nullptr, nullptr, nullptr, nullptr};
-      e = launch_head_grad(a, head, std::min(chunk, N - n0), dH + n0 * D, b, err, st, launches);
+    for (int64_t n0 = 0; n0 < N; n0 += chunk) {
+      const HeadGrad a = {head, std::min(chunk, N - n0), b, err, st, launches};
+      cudaError_t e = grad_rows(a, true);
+      if (e == cudaSuccess) e = grad_image_dy(a, dY + n0 * V);
+      if (e == cudaSuccess) e = grad_product(a, nullptr, dH + n0 * D);
+      if (e != cudaSuccess) return cuda_status(e);
     }
-    return e;
+    return static_cast<int>(ARCHEAD_OK);
   });
 }
 
@@ -130,7 +149,7 @@ int archead_policy_loss(const float* nll, const float* nll_old, const float* nll
                         nll_ref ? kl_coef : 0.0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_scratch(policy_scratch_bytes(a), st, [&](char* b, unsigned* err, int* launches) {
-    return launch_policy_loss(a, b, err, st, launches);
+    return cuda_status(launch_policy_loss(a, b, err, st, launches));
   });
 }
 
@@ -157,7 +176,7 @@ int archead_preference_loss(const float* nll, const float* nll_ref, const float*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_scratch(preference_scratch_bytes(a), st,
                       [&](char* b, unsigned* err, int* launches) {
-    return launch_preference_loss(a, b, err, st, launches);
+    return cuda_status(launch_preference_loss(a, b, err, st, launches));
   });
 }
 
