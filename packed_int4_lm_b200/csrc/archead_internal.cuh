@@ -201,17 +201,13 @@ size_t tc_split_scratch_bytes(const Shapes& s, const TcPlan& plan);
 // single token tile over the CTAs; with several token tiles, counters[0] is the work
 // counter from which the CTAs take their items in order (nullptr: a fixed round-robin).
 // image != nullptr: the softmax gradient's FP16 image instead (see grad_common.cuh).
-struct GradToken {  // what a token's entries of the image take
-  float lse;        // its log-sum-exp (NaN: its target is invalid)
-  float factor;     // 2^f
-  float at_target;  // the target's entry, exp(-nll) - 1
-  int32_t target;
-};
 struct TcImage {
   char* img;
-  const float* snorm;  // per vocabulary row (padded to 128) S'_v 2^-es, 0 past V
-  const GradToken* tok;
-  int nt;  // token tile of the image
+  // per vocabulary row (padded to 128): log2 |S'_v 2^-es| (-infinity for 0 and past V) and the
+  // FP16x2 sign bits of S'_v
+  const float2* row;
+  const float* tok;  // per token: f - lse log2 e (NaN: its target is invalid)
+  int nt;            // token tile of the image
 };
 cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead_head* head,
                                const Shapes& s, const TcPlan& plan, float* Y,
@@ -297,7 +293,7 @@ cudaError_t launch_repack(const uint8_t* canon, uint8_t* dev, int64_t V, int64_t
 //  2. the FP16 image of dY: grad_image_dy from dY itself, or from the logits with dY[n, v] =
 //     exp(Y[n, v] - lse[n]) - [v = targets[n]] (the target's entry from its NLL, exp(-nll) - 1):
 //     grad_image_softmax from logits in memory, or grad_tokens, whose TcImage the tcgen05 logits
-//     kernel then fills;
+//     kernel then fills, and grad_targets, which sets the targets' entries;
 //  3. grad_product: row n times dnll[n] (nullptr: 1), zero where that is 0.
 // scratch: head_grad_scratch_bytes, the same for all steps.
 struct HeadGrad {
@@ -317,6 +313,7 @@ cudaError_t grad_rows(const HeadGrad& a, bool dy);  // dy: grad_image_dy follows
 cudaError_t grad_image_dy(const HeadGrad& a, const float* dY);
 cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const SoftmaxTokens& t);
 cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image);
+cudaError_t grad_targets(const HeadGrad& a, const SoftmaxTokens& t);
 cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH);
 
 // Losses on per-token NLLs (csrc/losses.cu).

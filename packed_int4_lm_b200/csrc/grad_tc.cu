@@ -180,35 +180,52 @@ __device__ __forceinline__ int softmax_exp(float nll, float lse) {
   return b <= 3.402823466e38f ? 12 - ilogbf(b) : 0;
 }
 
-// What the tcgen05 logits kernel needs to write the image itself: the row scales in units of the
-// largest, and per token a GradToken (and texp).
+// What the tcgen05 logits kernel needs to write the image itself (TcImage), and texp.
 struct TokensParams {
   int64_t n, V, vpad;
   const float* sp;
   const float* spmax;
   SoftmaxTokens t;
-  float* snorm;
-  GradToken* tok;
+  float2* row;
+  float* tok;
   int* texp;
+  char* img;
+  int nt;
   unsigned* err;
 };
 __global__ void __launch_bounds__(256) grad_tokens_kernel(const TokensParams p) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int es = spmax_exp(p.spmax);
-  float e0, e1;
-  pow2_pair(-es, &e0, &e1);
   const int64_t i0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
-  for (int64_t v = i0; v < p.vpad; v += step) p.snorm[v] = p.sp[v] * e0 * e1;
+  for (int64_t v = i0; v < p.vpad; v += step) {
+    const float s = p.sp[v];
+    p.row[v] = make_float2(log2f(fabsf(s)) - (float)es, __uint_as_float(s < 0.f ? 0x80008000u : 0u));
+  }
   for (int64_t n = i0; n < p.n; n += step) {
-    const float nll = p.t.nll[n], lse = p.t.lse[n];
+    const float lse = p.t.lse[n];
     const int32_t t = p.t.targets[n];
     const bool bad = (t < 0 || t >= p.V) && p.t.dnll[n] != 0.f;
     if (bad) atomicOr(p.err, kErrTarget);
-    const int f = softmax_exp(nll, lse);
-    p.tok[n] = GradToken{bad ? __int_as_float(0x7fc00000) : lse, ldexpf(1.f, f), expm1f(-nll), t};
+    const int f = softmax_exp(p.t.nll[n], lse);
+    p.tok[n] = bad ? __int_as_float(0x7fc00000) : fmaf(lse, -1.44269504f, (float)f);
     p.texp[n] = es - f;
   }
+}
+
+// The targets' entries: (exp(-nll) - 1) 2^f S'_t 2^-es.
+__global__ void __launch_bounds__(256) grad_targets_kernel(const TokensParams p) {
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int64_t n = blockIdx.x * 256ll + threadIdx.x;
+  if (n >= p.n) return;
+  const int32_t t = p.t.targets[n];
+  if (t < 0 || t >= p.V) return;
+  float a, b;
+  pow2_pair(-p.texp[n], &a, &b);
+  const int64_t tt = n / p.nt;
+  *reinterpret_cast<__half*>(p.img + grad_image_offset(tt, t >> 6, p.vpad >> 6, p.nt, (int)(n - tt * p.nt), t & 63)) =
+      __float2half_rn(expm1f(-p.t.nll[n]) * a * p.sp[t] * b);
 }
 
 // One warp per 64 vocabulary rows and group of 32 tokens: each lane two rows, one 128-byte
@@ -796,7 +813,7 @@ struct GradPlan {
   int nt, ntt, ntiles, slabs;
   int64_t npad, nunits, dp;
   int fcols;
-  size_t o_img, o_fimg, o_sp, o_snorm, o_spmax, o_amax, o_texp, o_tok, o_part, bytes;
+  size_t o_img, o_fimg, o_sp, o_row, o_spmax, o_amax, o_texp, o_tok, o_part, bytes;
 };
 
 GradPlan grad_plan(const archead_head& h, int64_t n) {
@@ -834,11 +851,11 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   g.fcols = (RR + 63) / 64 * 64;
   g.o_fimg = take((size_t)g.nunits * kUnit * g.fcols * 2);
   g.o_sp = take((size_t)g.nunits * kUnit * 4);
-  g.o_snorm = take((size_t)g.nunits * kUnit * 4);
+  g.o_row = take((size_t)g.nunits * kUnit * 8);
   g.o_spmax = take(kRowBlocks * 4);
   g.o_amax = take((size_t)n * 4);
   g.o_texp = take((size_t)n * 4);
-  g.o_tok = take((size_t)n * sizeof(GradToken));
+  g.o_tok = take((size_t)n * 4);
   g.o_part = take((size_t)g.slabs * n * g.dp * 4);
   g.bytes = o;
   return g;
@@ -878,18 +895,30 @@ cudaError_t launch_grad_nt(const GradParams& p, cudaStream_t st) {
 
 struct GradParts {
   char *img, *fimg;
-  float *sp, *snorm, *spmax;
+  float *sp, *spmax, *tok, *part;
+  float2* row;
   unsigned* amax;
   int* texp;
-  GradToken* tok;
-  float* part;
 };
 GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
   char* b = a.scratch;
-  return {b + g.o_img, b + g.o_fimg, reinterpret_cast<float*>(b + g.o_sp),
-          reinterpret_cast<float*>(b + g.o_snorm), reinterpret_cast<float*>(b + g.o_spmax),
-          reinterpret_cast<unsigned*>(b + g.o_amax), reinterpret_cast<int*>(b + g.o_texp),
-          reinterpret_cast<GradToken*>(b + g.o_tok), reinterpret_cast<float*>(b + g.o_part)};
+  GradParts q;
+  q.img = b + g.o_img;
+  q.fimg = b + g.o_fimg;
+  q.sp = reinterpret_cast<float*>(b + g.o_sp);
+  q.spmax = reinterpret_cast<float*>(b + g.o_spmax);
+  q.tok = reinterpret_cast<float*>(b + g.o_tok);
+  q.part = reinterpret_cast<float*>(b + g.o_part);
+  q.row = reinterpret_cast<float2*>(b + g.o_row);
+  q.amax = reinterpret_cast<unsigned*>(b + g.o_amax);
+  q.texp = reinterpret_cast<int*>(b + g.o_texp);
+  return q;
+}
+
+TokensParams tokens_params(const HeadGrad& a, const SoftmaxTokens& t) {
+  const GradPlan g = grad_plan(*a.head, a.n);
+  const GradParts b = grad_parts(a, g);
+  return {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.row, b.tok, b.texp, b.img, g.nt, a.err};
 }
 
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
@@ -932,12 +961,15 @@ cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const Sof
 }
 
 cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image) {
-  const GradPlan g = grad_plan(*a.head, a.n);
-  const GradParts b = grad_parts(a, g);
-  const TokensParams p = {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.snorm, b.tok, b.texp, a.err};
-  *image = TcImage{b.img, b.snorm, b.tok, g.nt};
+  const TokensParams p = tokens_params(a, t);
+  *image = TcImage{p.img, p.row, p.tok, p.nt};
   ++*a.launches;
   return launch_pdl(grad_tokens_kernel, dim3(148), 256, 0, a.st, p);
+}
+
+cudaError_t grad_targets(const HeadGrad& a, const SoftmaxTokens& t) {
+  ++*a.launches;
+  return launch_pdl(grad_targets_kernel, dim3((unsigned)((a.n + 255) / 256)), 256, 0, a.st, tokens_params(a, t));
 }
 
 cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {

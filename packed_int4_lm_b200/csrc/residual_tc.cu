@@ -127,11 +127,11 @@ constexpr size_t nll_scratch_bytes() {
   return (size_t)16 * 128 * 4 + (size_t)NT * 4;
 }
 
-// shared memory of the epilogue by MODE: nothing, the fused NLL's scratch, or a GradToken per
+// shared memory of the epilogue by MODE: nothing, the fused NLL's scratch, or two floats per
 // token
 template <int NT>
 constexpr size_t mode_scratch_bytes(int mode) {
-  return mode == 1 ? nll_scratch_bytes<NT>() : (mode == 2 ? (size_t)NT * sizeof(GradToken) : 0);
+  return mode == 1 ? nll_scratch_bytes<NT>() : (mode == 2 ? (size_t)NT * sizeof(float2) : 0);
 }
 
 template <int NT>
@@ -293,6 +293,12 @@ __device__ __forceinline__ uint32_t factor_word(const TcParams& p, int64_t v, in
   return w;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* ptr) {
   asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr));
 }
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
   unsigned char* after_codes = cds + 2 * round16(code_bytes);
   float* nll_y = reinterpret_cast<float*>(after_codes);  // [16][128]
   int32_t* tgt_s = reinterpret_cast<int32_t*>(nll_y + 16 * 128);  // [NT]
-  GradToken* gtok_s = reinterpret_cast<GradToken*>(after_codes);  // MODE 2: [NT]
+  float2* gtok_s = reinterpret_cast<float2*>(after_codes);  // MODE 2: [NT]
   float* tsc_s = reinterpret_cast<float*>(after_codes + mode_scratch_bytes<NT>(MODE));
   uint64_t* bars = reinterpret_cast<uint64_t*>(tsc_s + NT);  // tsc_s: [NT] token scales
   uint64_t* b_full = bars;
@@ -724,7 +730,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
         if (e < NT) {
           if (MODE == 1) tgt_s[e] = tok0 + e < p.N ? __ldg(p.targets + tok0 + e) : -1;
-          if (MODE == 2 && tok0 + e < p.N) gtok_s[e] = p.image.tok[tok0 + e];
+          if (MODE == 2)
+            gtok_s[e] = tok0 + e < p.N ? make_float2(__ldg(p.tsc + tok0 + e) * 1.44269504f, __ldg(p.image.tok + tok0 + e))
+                                       : make_float2(0.f, 0.f);
           tsc_s[e] = tok0 + e < p.N ? __ldg(p.tsc + tok0 + e) : 1.f;
         }
         asm volatile("bar.sync 1, 128;\n" ::: "memory");
@@ -733,7 +741,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
       const int64_t v = it.row0 + e;
       const bool live = v < it.row_end;
       const float sp = row_scale(load_row(p, v)).sp;  // loads overlap the wait below
-      const float gs = MODE == 2 ? __ldg(p.image.snorm + v) : 0.f;  // (0 past V)
+      const float2 grow = MODE == 2 ? __ldg(p.image.row + v) : make_float2(0.f, 0.f);
+      const float glog = grow.x;
+      const uint32_t gsign = __float_as_uint(grow.y);
       // one outcome for all four epilogue warps: they share named barriers below
       if (!tc::bar_and(1, 128, tc::mbar_wait(&acc_full[ab], use & 1, p.err))) break;
       tc::fence_after_sync();
@@ -805,10 +815,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
 #pragma unroll
         for (int c = 0; c < HC / 16; ++c) {
           const int c16 = h * (HC / 16) + c;  // 16-token chunk of the tile
+          const uint32_t* r16 = r[c];
           float y[16];
           const float4* ts4 = reinterpret_cast<const float4*>(tsc_s + 16 * c16);
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {  // the logit of token q: accumulator x S'_v x 2^e_q
+          for (int q4 = 0; MODE != 2 && q4 < 4; ++q4) {  // the logit of token q: accumulator x S'_v x 2^e_q
             const float4 f = ts4[q4];
             y[4 * q4 + 0] = __uint_as_float(r[c][4 * q4 + 0]) * sp * f.x;
             y[4 * q4 + 1] = __uint_as_float(r[c][4 * q4 + 1]) * sp * f.y;
@@ -828,22 +839,30 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
               }
             }
           } else if (MODE == 2) {
-            // softmax gradient: (exp(y - lse) - [v = target]) 2^f S'_v 2^-es, rounded to FP16 at
-            // its place in the image.  __expf: its error grows with the exponent but stays below
-            // 2^-18 for probabilities above 2^-40, far inside the rounding to FP16.
+            // Softmax gradient exp(y - lse) 2^f S'_v 2^-es, rounded to FP16 at its place in the
+            // image, as one power of two: y = acc S'' 2^e_n (gtok_s.x holds 2^e_n log2 e), the
+            // token's other terms are gtok_s.y and the row's glog.  The exponent is an FP32 value,
+            // so the result is off by 2^-24 of |lse| log2 e at most, far inside the rounding to
+            // FP16.  Targets' entries are set afterwards.  Adjacent lanes exchange values of two
+            // tokens, so each stores two adjacent rows of one token.
             const int64_t t16 = tok0 + 16 * c16;
             const int64_t nq = p.N - t16;
             const int64_t gt = t16 / p.image.nt;
-            const int r = (int)(v & 63);
-            char* base = p.image.img + ((gt * 2 * p.n_vtiles + (v >> 6)) * p.image.nt + (t16 - gt * p.image.nt)) * 128 + 2 * (r & 7);
+            const int odd = lane & 1, r = (int)(v & 62);
+            char* base = p.image.img + 4 * ((r >> 1) & 3) +
+                         ((gt * 2 * p.n_vtiles + (v >> 6)) * p.image.nt + (t16 - gt * p.image.nt) + odd) * 128;
+            const uint32_t chunk = (uint32_t)((r >> 3) ^ odd) << 4;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const GradToken g = gtok_s[16 * c16 + q];
-              float x = __expf(y[q] - g.lse);
-              if (v == g.target) x = g.at_target;
-              x = live ? x * g.factor * gs : 0.f;
-              if (q < nq)  // (t16 is a multiple of 16, so the token's place mod 8 is q mod 8)
-                *reinterpret_cast<__half*>(base + q * 128 + ((((r >> 3) ^ q) & 7) << 4)) = __float2half_rn(x);
+            for (int q = 0; q < 16; q += 2) {
+              const float4 g = *reinterpret_cast<const float4*>(gtok_s + 16 * c16 + q);
+              const float x0 = exp2_approx(fmaf(__uint_as_float(r16[q]), sp * g.x, g.y + glog));
+              const float x1 = exp2_approx(fmaf(__uint_as_float(r16[q + 1]), sp * g.z, g.w + glog));
+              const uint32_t mine = h2_bits(__floats2half2_rn(x0, x1)) ^ gsign;
+              const uint32_t his = __shfl_xor_sync(0xffffffffu, mine, 1);
+              // even lane: its own and the odd lane's low halves; odd lane: the high halves
+              const uint32_t two = __byte_perm(mine, his, odd ? 0x3276 : 0x5410);
+              if (q + odd < nq)
+                *reinterpret_cast<uint32_t*>(base + q * 128 + (chunk ^ (uint32_t)((q & 7) << 4))) = two;
             }
           } else {
             // ---- fused NLL: per token of the chunk, (max, sum exp) over the tile's rows ----

@@ -89,6 +89,7 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
           return static_cast<int>(ARCHEAD_ERR_CUDA);
         const int rc = run_tc_image(H + n0 * D, head, s, image, st, launches);
         if (rc) return rc;
+        if (grad_targets(a, t) != cudaSuccess) return static_cast<int>(ARCHEAD_ERR_CUDA);
       } else {
         const int rc = archead_logits(H + n0 * D, head, Y, s.N, V, D, r_c, r_r, g, stream);
         if (rc) return rc;
