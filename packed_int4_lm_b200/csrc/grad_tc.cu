@@ -24,18 +24,19 @@
 namespace archead {
 namespace {
 
-constexpr int kDequantWarps = 8;
+constexpr int kDequantWarps = 16;
 constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 2 producers, 1 MMA
 constexpr int kUnit = 128;                              // vocabulary rows per unit of K
 constexpr int kAStage = 64 * 256 * 2;                   // 64 rows x 256 columns FP16
 constexpr int kPkStage = 16384;                         // 128 rows x 256 columns of nibbles
-constexpr int kRowBlocks = 148;                         // blocks of grad_rows_kernel
+constexpr int kRowBlocks = 296;                         // blocks of grad_rows_kernel
 
 // ---- the image ---------------------------------------------------------------------------
 struct RowsParams {
   archead_head h;
   int64_t vpad;
   float* sp;         // S'_v, vpad (0 past V)
+  float2* row;       // TcImage's rows without -es, or nullptr
   float* spmax;      // kRowBlocks
   unsigned* amax;    // per token, cleared here (n), or nullptr
   int64_t n;
@@ -70,7 +71,7 @@ __device__ __forceinline__ GradRow head_row(const archead_head& h, int64_t v, fl
   return grad_row(bf16_bits_to_float(__ldg(h.r_super + v)), *sac, *saw);
 }
 
-__global__ void __launch_bounds__(1024) grad_rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) {
   allow_dependent_launch();
   __shared__ float red[32];
   const int64_t t0 = blockIdx.x * 1024ll + threadIdx.x, step = gridDim.x * 1024ll;
@@ -82,15 +83,18 @@ __global__ void __launch_bounds__(1024) grad_rows_kernel(const RowsParams p) {
       s = p.h.format == ARCHEAD_FMT_ROW8 ? p.h.row_scale[v] : head_row(p.h, v, &sac, &saw).sp;
     }
     p.sp[v] = s;
+    if (p.row) p.row[v] = make_float2(log2f(fabsf(s)), __uint_as_float(s < 0.f ? 0x80008000u : 0u));
     m = fmaxf(m, fabsf(s));
   }
   if (p.amax)
     for (int64_t i = t0; i < p.n; i += step) p.amax[i] = 0u;
   if (p.fimg) {  // eight factor entries of a row at a time
-    const int per = p.fcols >> 3;
-    for (int64_t i = t0; i < p.vpad * per; i += step) {
-      const int64_t v = i / per;
-      const int c = (int)(i - v * per), k = (int)(v & 63);
+    const unsigned per = (unsigned)p.fcols >> 3, total = (unsigned)p.vpad * per;  // < 2^31
+#pragma unroll 2
+    for (unsigned i = (unsigned)t0; i < total; i += (unsigned)step) {
+      const unsigned vi = i / per;
+      const int64_t v = vi;
+      const int c = (int)(i - vi * per), k = (int)(vi & 63);
       uint32_t o[4] = {0u, 0u, 0u, 0u};
       if (v < p.h.V) {
         float sac, saw;
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(256) dy_amax_kernel(const AmaxParams p) {
 struct ImageParams {
   const float* src;  // dY, or logits
   int64_t n, npad, V;
-  int nt;
+  int nt, group;
   const float* sp;
   const float* spmax;
   const unsigned* amax;  // dY: per-token maxima
@@ -180,13 +184,13 @@ __device__ __forceinline__ int softmax_exp(float nll, float lse) {
   return b <= 3.402823466e38f ? 12 - ilogbf(b) : 0;
 }
 
-// What the tcgen05 logits kernel needs to write the image itself (TcImage), and texp.
+// What the tcgen05 logits kernel needs of the tokens to write the image itself (TcImage), and
+// texp.
 struct TokensParams {
   int64_t n, V, vpad;
   const float* sp;
   const float* spmax;
   SoftmaxTokens t;
-  float2* row;
   float* tok;
   int* texp;
   char* img;
@@ -197,20 +201,15 @@ __global__ void __launch_bounds__(256) grad_tokens_kernel(const TokensParams p) 
   allow_dependent_launch();
   grid_dependency_wait();
   const int es = spmax_exp(p.spmax);
-  const int64_t i0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
-  for (int64_t v = i0; v < p.vpad; v += step) {
-    const float s = p.sp[v];
-    p.row[v] = make_float2(log2f(fabsf(s)) - (float)es, __uint_as_float(s < 0.f ? 0x80008000u : 0u));
-  }
-  for (int64_t n = i0; n < p.n; n += step) {
-    const float lse = p.t.lse[n];
-    const int32_t t = p.t.targets[n];
-    const bool bad = (t < 0 || t >= p.V) && p.t.dnll[n] != 0.f;
-    if (bad) atomicOr(p.err, kErrTarget);
-    const int f = softmax_exp(p.t.nll[n], lse);
-    p.tok[n] = bad ? __int_as_float(0x7fc00000) : fmaf(lse, -1.44269504f, (float)f);
-    p.texp[n] = es - f;
-  }
+  const int64_t n = blockIdx.x * 256ll + threadIdx.x;
+  if (n >= p.n) return;
+  const float lse = p.t.lse[n];
+  const int32_t t = p.t.targets[n];
+  const bool bad = (t < 0 || t >= p.V) && p.t.dnll[n] != 0.f;
+  if (bad) atomicOr(p.err, kErrTarget);
+  const int f = softmax_exp(p.t.nll[n], lse);
+  p.tok[n] = bad ? __int_as_float(0x7fc00000) : fmaf(lse, -1.44269504f, (float)(f - es));
+  p.texp[n] = es - f;
 }
 
 // The targets' entries: (exp(-nll) - 1) 2^f S'_t 2^-es.
@@ -228,61 +227,82 @@ __global__ void __launch_bounds__(256) grad_targets_kernel(const TokensParams p)
       __float2half_rn(expm1f(-p.t.nll[n]) * a * p.sp[t] * b);
 }
 
-// One warp per 64 vocabulary rows and group of 32 tokens: each lane two rows, one 128-byte
-// image row per token.
-template <bool kSoftmax>
+// One warp per 64 vocabulary rows and group of up to 32 tokens (`group`; fewer for small batches,
+// which would leave most SMs idle): each lane two rows, one 128-byte image row per token, four
+// tokens' loads in flight.
+template <bool kSoftmax, bool kPairs>
 __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t nhb = (p.V + kUnit - 1) / kUnit * 2;
   const int64_t hb = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int64_t n0 = blockIdx.y * 32ll;
+  const int64_t n0 = (int64_t)blockIdx.y * p.group;
   const int es = spmax_exp(p.spmax);
-  // this lane's token of the group: its factor
+  // this lane's token of the group: its factor 2^f and, for logits, lse, target and its entry
   const int64_t mine = n0 + lane;
   int f = 0;
-  bool bad = false;
-  if (mine < p.n) {
+  float lse = 0.f, at = 0.f;
+  int32_t target = -1;
+  if (lane < p.group && mine < p.n) {
     if (kSoftmax) {
-      const int32_t t = p.t.targets[mine];
-      f = softmax_exp(p.t.nll[mine], p.t.lse[mine]);
-      bad = (t < 0 || t >= p.V) && p.t.dnll[mine] != 0.f;
+      target = p.t.targets[mine];
+      lse = p.t.lse[mine];
+      const float nll = p.t.nll[mine];
+      f = softmax_exp(nll, lse);
+      at = expm1f(-nll);
+      if ((target < 0 || target >= p.V) && p.t.dnll[mine] != 0.f) {
+        lse = __int_as_float(0x7fc00000);
+        if (hb == 0) atomicOr(p.err, kErrTarget);
+      }
     } else {
       f = dy_exp(p.amax[mine]);
     }
     if (hb == 0) p.texp[mine] = es - f;  // within +-240
   }
-  if (hb == 0 && bad) atomicOr(p.err, kErrTarget);
   if (hb >= nhb) return;
   const int64_t v = 64 * hb + 2 * lane;
   float s0 = p.sp[v], s1 = p.sp[v + 1], e0, e1;
   pow2_pair(-es, &e0, &e1);
   s0 = s0 * e0 * e1;
   s1 = s1 * e0 * e1;
-  for (int k = 0; k < 32 && n0 + k < p.npad; ++k) {
-    const int64_t n = n0 + k;
-    float y0 = 0.f, y1 = 0.f;
-    const int fk = __shfl_sync(0xffffffffu, f, k);
-    const bool bk = __shfl_sync(0xffffffffu, (int)bad, k);
-    if (n < p.n) {
-      const float* row = p.src + n * p.V;
-      if (v < p.V) y0 = row[v];
-      if (v + 1 < p.V) y1 = row[v + 1];
-      if (kSoftmax) {
-        const float l = bk ? __int_as_float(0x7fc00000) : p.t.lse[n];
-        const int64_t t = p.t.targets[n];
-        y0 = v < p.V ? (v == t ? expm1f(-p.t.nll[n]) : expf(y0 - l)) : 0.f;
-        y1 = v + 1 < p.V ? (v + 1 == t ? expm1f(-p.t.nll[n]) : expf(y1 - l)) : 0.f;
+  for (int k0 = 0; k0 < p.group && n0 + k0 < p.npad; k0 += 4) {
+    float y0[4], y1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t n = n0 + k0 + k;
+      const float* row = p.src + n * p.V + v;
+      y0[k] = y1[k] = 0.f;
+      if (kPairs) {
+        if (n < p.n && v < p.V) {
+          const float2 q = __ldcs(reinterpret_cast<const float2*>(row));
+          y0[k] = q.x;
+          y1[k] = q.y;
+        }
+      } else if (n < p.n) {
+        if (v < p.V) y0[k] = __ldcs(row);
+        if (v + 1 < p.V) y1[k] = __ldcs(row + 1);
       }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t n = n0 + k0 + k;
+      const int fk = __shfl_sync(0xffffffffu, f, k0 + k);
       float a, b;
       pow2_pair(fk, &a, &b);
-      y0 = y0 * a * b * s0;
-      y1 = y1 * a * b * s1;
+      if (kSoftmax) {
+        const float l = __shfl_sync(0xffffffffu, lse, k0 + k), z = __shfl_sync(0xffffffffu, at, k0 + k);
+        const int64_t t = __shfl_sync(0xffffffffu, target, k0 + k);
+        y0[k] = v < p.V ? (v == t ? z : expf(y0[k] - l)) : 0.f;
+        y1[k] = v + 1 < p.V ? (v + 1 == t ? z : expf(y1[k] - l)) : 0.f;
+        if (l != l) y0[k] = y1[k] = l;
+      }
+      if (n >= p.npad) break;
+      const int64_t tt = n / p.nt;
+      const float x0 = n < p.n ? y0[k] * a * b * s0 : 0.f, x1 = n < p.n ? y1[k] * a * b * s1 : 0.f;
+      *reinterpret_cast<__half2*>(p.img + grad_image_offset(tt, hb, nhb, p.nt, (int)(n - tt * p.nt),
+                                                            2 * lane)) = __floats2half2_rn(x0, x1);
     }
-    const int64_t tt = n / p.nt;
-    *reinterpret_cast<__half2*>(p.img + grad_image_offset(tt, hb, nhb, p.nt, (int)(n - tt * p.nt),
-                                                          2 * lane)) = __floats2half2_rn(y0, y1);
   }
 }
 
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SA; ++i) {
-      tc::mbar_init(&a_full[i], 4);  // the four warps that fill a stage
+      tc::mbar_init(&a_full[i], kDequantWarps / 2);  // the warps that fill a stage
       tc::mbar_init(&a_empty[i], 1);
     }
     for (int i = 0; i < C::SB; ++i) {
@@ -450,9 +470,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 
   if (warp < kDequantWarps) {
     // ---- dequantisation: lane = vocabulary row of a 32-row group ----
-    // A warp owns rows 32 rg .. + 31 of each unit and one 128-column block b; the unit's two
-    // 64-row halves are two A stages, so four warps fill a stage.
-    const int rg = warp & 3, b = warp >> 2, h = rg >> 1;
+    // A warp owns rows 32 rg .. + 31 of each unit, one 128-column block b and half of that
+    // block's 16-byte chunks; the unit's two 64-row halves are two A stages, so eight warps fill
+    // a stage.  %W16%
+    const int rg = warp & 3, b = (warp >> 2) & 1, ch = warp >> 3, h = rg >> 1;
     const int s = 32 * rg + lane;       // row in the unit
     const int k = 32 * (rg & 1) + lane;  // row in the stage
     const uint32_t a_row = tc::smem_u32(As) + (uint32_t)(b * 2) * 8192 + (k >> 3) * 1024 + (k & 7) * 128;
@@ -464,7 +485,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     bool ok = true;
     for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
       if (it.rank) {
-        // Whole stages from the factor image, copied by one of the four warps of a half; the
+        // Whole stages from the factor image, copied by one of the eight warps of a half; the
         // others only keep pace (a warp that skipped stages would lose count of the phases).
         const uint32_t bytes = (uint32_t)p.fcols * 128u;
         grid_dependency_wait();  // the image comes from a kernel before this one
@@ -477,7 +498,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
             break;
           }
           if (lane == 0) {
-            if ((warp & 5) == 0) {
+            if ((warp & 13) == 0) {
               tc::mbar_arrive_expect_tx(&a_full[slot], bytes);
               tc::bulk_g2s(As + slot * kAStage, p.fimg + (2 * u + h) * bytes, bytes, &a_full[slot]);
               copied = ks;
@@ -496,8 +517,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
         const RowLoad r = nx;
         const int64_t v = u * kUnit + s;
         if (u + 1 < it.u1) nx = load_grad_row<CPC>(p, v + kUnit, col, work);
-        uint32_t w[16];
-        uint4 raw[8];
+        uint32_t w[8];
+        uint4 raw[4];
         if (CPC != 0) {
           if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err))) {
             ok = false;
@@ -506,8 +527,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
           const unsigned char* src = Ps + ps * kPkStage + b * 8192 + s * 16;
           if (work) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 q = *reinterpret_cast<const uint4*>(src + c * 2048);
+            for (int c = 0; c < 2; ++c) {
+              const uint4 q = *reinterpret_cast<const uint4*>(src + (2 * ch + c) * 2048);
               w[4 * c] = q.x;
               w[4 * c + 1] = q.y;
               w[4 * c + 2] = q.z;
@@ -522,9 +543,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
           }
         }
         if (CPC == 0 && work) {  // INT8 rows straight from global memory
-          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col);
+          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int c = 0; c < 4; ++c)
             raw[c] = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
         }
         const int64_t ks = 2 * seq + h;
@@ -538,12 +559,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
         if (work) {
           if (CPC == 0) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the block
+            for (int c = 0; c < 4; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the half block
               const uint32_t q[4] = {raw[c].x ^ 0x80808080u, raw[c].y ^ 0x80808080u,
                                      raw[c].z ^ 0x80808080u, raw[c].w ^ 0x80808080u};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t at = dst + (c >> 2) * 8192 + ((((2 * c + e) & 7) ^ x7) << 4);
+                const uint32_t at = dst + ch * 8192 + (((2 * c + e) ^ x7) << 4);
                 st_shared16(at, h2_bits(bytes_to_half2(q[2 * e], 0x4140)), h2_bits(bytes_to_half2(q[2 * e], 0x4342)),
                             h2_bits(bytes_to_half2(q[2 * e + 1], 0x4140)), h2_bits(bytes_to_half2(q[2 * e + 1], 0x4342)));
               }
@@ -556,10 +577,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
               const __half2 c2 = __float2half2_rn((float)cw * cs);  // exact for k <= 24
               const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {  // columns 32 wn + 8 c .. + 7: one 16-byte chunk
+              for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7: one 16-byte chunk
                 __half2 o[4];
                 dequant_word(w[4 * c + wn], c2, nc24, o);
-                st_shared16(dst + (wn >> 1) * 8192 + (((((wn & 1) << 2) + c) ^ x7) << 4), h2_bits(o[0]),
+                st_shared16(dst + (wn >> 1) * 8192 + (((((wn & 1) << 2) + 2 * ch + c) ^ x7) << 4), h2_bits(o[0]),
                             h2_bits(o[1]), h2_bits(o[2]), h2_bits(o[3]));
               }
             }
@@ -737,67 +758,143 @@ struct FinishParams {
   __nv_bfloat16* dH;
 };
 
-// 16 tokens x 256 columns per block; a thread owns two adjacent columns.
+__device__ __forceinline__ void mma_bf16_16816(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf2_bits(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+// 16 MT tokens x 128 columns per block, a warp per 32 columns (one group of B's scales).  The
+// rank product runs as warp MMAs: the INT8 entries of b are exact in BF16, and u times the scale
+// is split into two BF16 pieces (16 bits, against the 8 that the result keeps).  Memory bounds it
+// (each slab's sums are read once); on the CUDA cores, one column pair and 16 tokens per thread,
+// the product took three times as long, and a lone block of a small batch 40 us of dependent
+// loads.
+constexpr int kFinishPad = 4;  // floats after a row of u
+template <int MT>
 __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) {
-  grid_dependency_wait();
-  extern __shared__ float us[];  // [RR][16]
-  const int RR = p.h.r_c + p.h.r_r;
-  const int64_t n0 = blockIdx.x * 16ll;
-  for (int i = threadIdx.x; i < RR * 16; i += 128) {
-    const int j = i >> 4;
-    const int64_t n = n0 + (i & 15);
-    float a = 0.f;
-    if (n < p.n)
-      for (int s = 0; s < p.slabs; ++s) a += p.part[(s * p.n + n) * p.dp + p.h.D + j];
-    us[i] = a;
-  }
-  __syncthreads();
-  const int64_t d = blockIdx.y * 256ll + 2 * threadIdx.x;
-  if (d >= p.h.D) return;
-  float a0[16], a1[16];
-#pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    a0[t] = a1[t] = 0.f;
-    if (n0 + t < p.n)
-      for (int s = 0; s < p.slabs; ++s) {
-        const float2 q = *reinterpret_cast<const float2*>(p.part + (s * p.n + n0 + t) * p.dp + d);
-        a0[t] += q.x;
-        a1[t] += q.y;
-      }
-  }
-  const int64_t G = p.h.D / p.h.g, grp = d / p.h.g;
-  for (int j = 0; j < RR; ++j) {
+  extern __shared__ __align__(16) unsigned char fsm[];
+  const int RR = p.h.r_c + p.h.r_r, rp = (RR + 15) & ~15, us_row = rp + kFinishPad;
+  float* us = reinterpret_cast<float*>(fsm);                      // [16 MT][us_row]
+  float* ss = us + 16 * MT * us_row;                              // [rp][4] scales of b
+  int8_t* bs = reinterpret_cast<int8_t*>(ss + 4 * rp);            // [rp][144] entries of b
+  const int64_t n0 = blockIdx.x * (16ll * MT), d0 = blockIdx.y * 128ll;
+  const int64_t G = p.h.D / p.h.g;
+  for (int i = threadIdx.x; i < rp * 8; i += 128) {  // b does not depend on earlier kernels
+    const int j = i >> 3, c = i & 7;
     const bool core = j < p.h.r_c;
-    const int jj = core ? j : j - p.h.r_c;
-    const char2 q = *reinterpret_cast<const char2*>((core ? p.h.Bc : p.h.Bw) + jj * p.h.D + d);
-    const float sc = __ldg((core ? p.h.sBc : p.h.sBw) + jj * G + grp);
-    const float b0 = __fmul_rn((float)q.x, sc), b1 = __fmul_rn((float)q.y, sc);
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (j < RR)
+      q = __ldg(reinterpret_cast<const uint4*>((core ? p.h.Bc + j * p.h.D : p.h.Bw + (j - p.h.r_c) * p.h.D) + d0) + c);
+    *reinterpret_cast<uint4*>(bs + j * 144 + 16 * c) = q;
+  }
+  for (int i = threadIdx.x; i < rp * 4; i += 128) {
+    const int j = i >> 2;
+    const bool core = j < p.h.r_c;
+    const int64_t grp = (d0 + 32 * (i & 3)) / p.h.g;
+    ss[i] = j < RR ? __ldg((core ? p.h.sBc + j * G : p.h.sBw + (j - p.h.r_c) * G) + grp) : 0.f;
+  }
+  grid_dependency_wait();
+  const int64_t slab = p.n * p.dp;
+  for (int i = threadIdx.x; i < 4 * MT * rp; i += 128) {
+    const int t = i / (rp >> 2), j = 4 * (i - t * (rp >> 2));
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n0 + t < p.n && j < RR) {
+      const float* q = p.part + (n0 + t) * p.dp + p.h.D + j;
+#pragma unroll 4
+      for (int s = 0; s < p.slabs; ++s) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(q + s * slab));
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+      }
+      if (j + 1 >= RR) a.y = 0.f;  // past the ranks nothing was written
+      if (j + 2 >= RR) a.z = 0.f;
+      if (j + 3 >= RR) a.w = 0.f;
+    }
+    *reinterpret_cast<float4*>(us + t * us_row + j) = a;
+  }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, gr = lane >> 2, q = lane & 3;
+  float acc[MT][4][4];
 #pragma unroll
-    for (int t4 = 0; t4 < 4; ++t4) {
-      const float4 u = *reinterpret_cast<const float4*>(us + 16 * j + 4 * t4);
-      a0[4 * t4] = fmaf(u.x, b0, a0[4 * t4]);
-      a1[4 * t4] = fmaf(u.x, b1, a1[4 * t4]);
-      a0[4 * t4 + 1] = fmaf(u.y, b0, a0[4 * t4 + 1]);
-      a1[4 * t4 + 1] = fmaf(u.y, b1, a1[4 * t4 + 1]);
-      a0[4 * t4 + 2] = fmaf(u.z, b0, a0[4 * t4 + 2]);
-      a1[4 * t4 + 2] = fmaf(u.z, b1, a1[4 * t4 + 2]);
-      a0[4 * t4 + 3] = fmaf(u.w, b0, a0[4 * t4 + 3]);
-      a1[4 * t4 + 3] = fmaf(u.w, b1, a1[4 * t4 + 3]);
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int hrow = 0; hrow < 2; ++hrow) {
+      const int64_t n = n0 + 16 * m + 8 * hrow + gr;
+      float2 a[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a[c] = make_float2(0.f, 0.f);
+      if (n < p.n) {
+        const float* src = p.part + n * p.dp + d0 + 32 * w + 2 * q;
+#pragma unroll 2
+        for (int s = 0; s < p.slabs; ++s)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 x = __ldcs(reinterpret_cast<const float2*>(src + s * slab + 8 * c));
+            a[c].x += x.x;
+            a[c].y += x.y;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[m][c][2 * hrow] = a[c].x;
+        acc[m][c][2 * hrow + 1] = a[c].y;
+      }
+    }
+  __syncthreads();
+  for (int k0 = 0; k0 < rp; k0 += 16) {
+    const int j = k0 + 2 * q;
+    uint32_t b[4][2];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int8_t* src = bs + j * 144 + 32 * w + 8 * c + gr;
+      b[c][0] = bf2_bits(__floats2bfloat162_rn((float)src[0], (float)src[144]));
+      b[c][1] = bf2_bits(__floats2bfloat162_rn((float)src[8 * 144], (float)src[9 * 144]));
+    }
+    const float s[4] = {ss[4 * j + w], ss[4 * (j + 1) + w], ss[4 * (j + 8) + w], ss[4 * (j + 9) + w]};
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // rows gr, gr + 8; k 2q, 2q + 8
+        const float2 u = *reinterpret_cast<const float2*>(us + (16 * m + gr + 8 * (e & 1)) * us_row + j + 8 * (e >> 1));
+        const float x = u.x * s[2 * (e >> 1)], y = u.y * s[2 * (e >> 1) + 1];
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        hi[e] = bf2_bits(h);
+        lo[e] = bf2_bits(__floats2bfloat162_rn(x - __low2float(h), y - __high2float(h)));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mma_bf16_16816(acc[m][c], hi, b[c][0], b[c][1]);
+        mma_bf16_16816(acc[m][c], lo, b[c][0], b[c][1]);
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    const int64_t n = n0 + t;
-    if (n >= p.n) break;
-    const float sc = p.rowscale ? p.rowscale[n] : 1.f;
-    float e0, e1, y0 = 0.f, y1 = 0.f;
-    pow2_pair(p.texp[n], &e0, &e1);
-    if (sc != 0.f) {
-      y0 = a0[t] * e0 * e1 * sc;
-      y1 = a1[t] * e0 * e1 * sc;
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int hrow = 0; hrow < 2; ++hrow) {
+      const int64_t n = n0 + 16 * m + 8 * hrow + gr;
+      if (n >= p.n) continue;
+      const float sc = p.rowscale ? p.rowscale[n] : 1.f;
+      float e0, e1;
+      pow2_pair(p.texp[n], &e0, &e1);
+      __nv_bfloat16* dst = p.dH + n * p.h.D + d0 + 32 * w + 2 * q;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = acc[m][c][2 * hrow] * e0 * e1 * sc, y = acc[m][c][2 * hrow + 1] * e0 * e1 * sc;
+        *reinterpret_cast<__nv_bfloat162*>(dst + 8 * c) = __floats2bfloat162_rn(sc == 0.f ? 0.f : x, sc == 0.f ? 0.f : y);
+      }
     }
-    *reinterpret_cast<__nv_bfloat162*>(p.dH + n * p.h.D + d) = __floats2bfloat162_rn(y0, y1);
-  }
+}
+
+size_t finish_smem(int mt, int RR) {
+  const size_t rp = (RR + 15) / 16 * 16;
+  return 16 * mt * (rp + kFinishPad) * 4 + rp * 16 + rp * 144;
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -918,18 +1015,23 @@ GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
 TokensParams tokens_params(const HeadGrad& a, const SoftmaxTokens& t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  return {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.row, b.tok, b.texp, b.img, g.nt, a.err};
+  return {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.tok, b.texp, b.img, g.nt, a.err};
 }
 
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  const ImageParams p = {src, a.n, g.npad, a.head->V, g.nt, b.sp, b.spmax, b.amax,
+  const int group = g.npad <= 64 ? 4 : (g.npad <= 256 ? 8 : 32);
+  const ImageParams p = {src, a.n, g.npad, a.head->V, g.nt, group, b.sp, b.spmax, b.amax,
                          t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
-  const dim3 grid((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + 31) / 32));
+  const dim3 grid((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + group - 1) / group));
+  const bool pairs = a.head->V % 2 == 0 && reinterpret_cast<uintptr_t>(src) % 8 == 0;
   ++*a.launches;
-  return t ? launch_pdl(dy_image_kernel<true>, grid, 256, 0, a.st, p)
-           : launch_pdl(dy_image_kernel<false>, grid, 256, 0, a.st, p);
+  if (t)
+    return pairs ? launch_pdl(dy_image_kernel<true, true>, grid, 256, 0, a.st, p)
+                 : launch_pdl(dy_image_kernel<true, false>, grid, 256, 0, a.st, p);
+  return pairs ? launch_pdl(dy_image_kernel<false, true>, grid, 256, 0, a.st, p)
+               : launch_pdl(dy_image_kernel<false, false>, grid, 256, 0, a.st, p);
 }
 
 }  // namespace
@@ -940,7 +1042,7 @@ cudaError_t grad_rows(const HeadGrad& a, bool dy) {
   const archead_head& h = *a.head;
   const GradPlan g = grad_plan(h, a.n);
   const GradParts b = grad_parts(a, g);
-  const RowsParams p = {h, g.nunits * kUnit, b.sp, b.spmax, dy ? b.amax : nullptr, a.n,
+  const RowsParams p = {h, g.nunits * kUnit, b.sp, dy ? nullptr : b.row, b.spmax, dy ? b.amax : nullptr, a.n,
                         g.fcols ? b.fimg : nullptr, g.fcols, h.r_c % 4 == 0 && h.r_r % 4 == 0};
   grad_rows_kernel<<<kRowBlocks, 1024, 0, a.st>>>(p);
   ++*a.launches;
@@ -962,9 +1064,9 @@ cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const Sof
 
 cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image) {
   const TokensParams p = tokens_params(a, t);
-  *image = TcImage{p.img, p.row, p.tok, p.nt};
+  *image = TcImage{p.img, grad_parts(a, grad_plan(*a.head, a.n)).row, p.tok, p.nt};
   ++*a.launches;
-  return launch_pdl(grad_tokens_kernel, dim3(148), 256, 0, a.st, p);
+  return launch_pdl(grad_tokens_kernel, dim3((unsigned)((a.n + 255) / 256)), 256, 0, a.st, p);
 }
 
 cudaError_t grad_targets(const HeadGrad& a, const SoftmaxTokens& t) {
@@ -990,8 +1092,12 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   if (e != cudaSuccess) return e;
   const FinishParams fp = {h, b.part, a.n, g.dp, g.slabs, b.texp, dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
   *a.launches += 2;
-  return launch_pdl(grad_finish_kernel, dim3((unsigned)((a.n + 15) / 16), (unsigned)((h.D + 255) / 256)), 128,
-                    (size_t)(h.r_c + h.r_r) * 64, a.st, fp);
+  // 64 tokens per block share b; small batches take 16, for more blocks
+  const int mt = a.n > 512 ? 4 : 1;
+  const size_t smem = finish_smem(mt, h.r_c + h.r_r);
+  auto kern = mt == 4 ? grad_finish_kernel<4> : grad_finish_kernel<1>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)((a.n + 16 * mt - 1) / (16 * mt)), (unsigned)(h.D / 128)), 128, smem, a.st, fp);
 }
 
 }  // namespace archead
