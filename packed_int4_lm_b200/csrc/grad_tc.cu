@@ -4,18 +4,20 @@
 //   u[n, j]  = sum_v dY[n, v] a[v, j],
 //
 // a = [Q8(A_c) | Q8(A_w)], b = [Q8(B_c) ; Q8(B_w)].  The long axis is the vocabulary, so the
-// packed head is the transposed operand: D[d, n] = sum_v A[v, d] B[n, v] with A the dequantised
-// head (vocabulary rows are K, its columns the 128 lanes of the accumulator) and B the FP16 image
-// of dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh).  u is one more tile of columns, whose A,
-// a / S', is prepared once per call in the layout of an A stage and copied (built from the INT8
-// rows in the product's loop it took three times as long as a residual tile and set the pace of
-// every round: N = 777, ranks 64 + 64: 3150 us against 760 us).
+// packed head is a transposed operand: D[n, d] = sum_v A[n, v] B[v, d] with A the FP16 image of
+// dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh; 128 tokens are the lanes of an accumulator)
+// and B the dequantised head, whose vocabulary rows are K and whose columns lie side by side
+// (MN-major).  The other way round, with the head as A, an instruction takes 128 cycles to read
+// its 128 columns however few tokens there are: N = 1 took 190 us against %N1% us.
+// u is one more tile of columns, whose B, a / S', is prepared once per call in the layout of a W
+// stage and copied (built from the INT8 rows in the product's loop it took three times as long as
+// a residual tile and set the pace of every round: N = 777, ranks 64 + 64: 3150 us against 760 us).
 //
 //  * grad_rows_kernel: S'_v per row and their maximum, the factor image; clears the per-token
 //    maxima.
 //  * dy_amax_kernel, dy_image_kernel: the image, from dY or from logits (softmax gradient).
-//  * grad_tc_kernel: the product.  A work item is 256 columns (two accumulators of 128 lanes) x
-//    NT tokens x a slab of the vocabulary; its FP32 sums go to scratch.
+//  * grad_tc_kernel: the product.  A work item is 256 columns x up to 256 tokens (two
+//    accumulators) x a slab of the vocabulary; its FP32 sums go to scratch.
 //  * grad_finish_kernel: adds the slabs in order, adds u b, scales and rounds to BF16.
 // Nothing is accumulated in memory, so equal calls give equal bits.
 #include "grad_common.cuh"
@@ -27,7 +29,7 @@ namespace {
 constexpr int kDequantWarps = 16;
 constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 2 producers, 1 MMA
 constexpr int kUnit = 128;                              // vocabulary rows per unit of K
-constexpr int kAStage = 64 * 256 * 2;                   // 64 rows x 256 columns FP16
+constexpr int kWStage = 32 * 256 * 2;                   // 32 rows x 256 columns FP16
 constexpr int kPkStage = 16384;                         // 128 rows x 256 columns of nibbles
 constexpr int kRowBlocks = 296;                         // blocks of grad_rows_kernel
 
@@ -36,6 +38,7 @@ struct RowsParams {
   archead_head h;
   int64_t vpad;
   float* sp;         // S'_v, vpad (0 past V)
+  float* cs;         // 2^-k per row (grad_row), vpad (0 past V)
   float2* row;       // TcImage's rows without -es, or nullptr
   float* spmax;      // kRowBlocks
   unsigned* amax;    // per token, cleared here (n), or nullptr
@@ -77,12 +80,19 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
   const int64_t t0 = blockIdx.x * 1024ll + threadIdx.x, step = gridDim.x * 1024ll;
   float m = 0.f;
   for (int64_t v = t0; v < p.vpad; v += step) {
-    float s = 0.f;
+    float s = 0.f, c = 0.f;
     if (v < p.h.V) {
       float sac, saw;
-      s = p.h.format == ARCHEAD_FMT_ROW8 ? p.h.row_scale[v] : head_row(p.h, v, &sac, &saw).sp;
+      if (p.h.format == ARCHEAD_FMT_ROW8) {
+        s = p.h.row_scale[v];
+      } else {
+        const GradRow gr = head_row(p.h, v, &sac, &saw);
+        s = gr.sp;
+        c = gr.cs;
+      }
     }
     p.sp[v] = s;
+    p.cs[v] = c;
     if (p.row) p.row[v] = make_float2(log2f(fabsf(s)), __uint_as_float(s < 0.f ? 0x80008000u : 0u));
     m = fmaxf(m, fabsf(s));
   }
@@ -94,7 +104,7 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
     for (unsigned i = (unsigned)t0; i < total; i += (unsigned)step) {
       const unsigned vi = i / per;
       const int64_t v = vi;
-      const int c = (int)(i - vi * per), k = (int)(vi & 63);
+      const int c = (int)(i - vi * per), k = (int)(vi & 31);
       uint32_t o[4] = {0u, 0u, 0u, 0u};
       if (v < p.h.V) {
         float sac, saw;
@@ -112,7 +122,7 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
           o[2 * q + 1] = h2_bits(__floats2half2_rn(x[2], x[3]));
         }
       }
-      *reinterpret_cast<uint4*>(p.fimg + (v >> 6) * p.fcols * 128 + (c >> 3) * 8192 + (k >> 3) * 1024 +
+      *reinterpret_cast<uint4*>(p.fimg + (v >> 5) * p.fcols * 64 + (c >> 3) * 4096 + (k >> 3) * 1024 +
                                 (k & 7) * 128 + (((c ^ k) & 7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
@@ -310,39 +320,49 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
 struct GradParams {
   archead_head h;
   const char* img;
+  const float* cs;
   float* part;  // [slab][n][dp]
   int64_t n, dp;
   int64_t nunits;  // units of 128 vocabulary rows
-  int ntt;         // token tiles
+  int nimg;        // token tiles of the image
+  int ntt;         // token tiles of the product: MT tiles of the image each
   int ntiles;      // column tiles: ceil(D / 256), one more for the ranks
   int slabs;
   int g_shift;
-  const char* fimg;  // factor image: per 64 rows, fcols x 128 bytes
+  const char* fimg;  // factor image: per 32 rows, fcols x 64 bytes
   int fcols;
   unsigned* err;
 };
 
-template <int NT>
+// IT: tokens per tile of the image (at most 128); MT: image tiles (accumulators) per item.
+template <int IT, int MT>
 struct GradCfg {
-  // Shared memory (227 KB): rings of A stages (32 KB: 64 rows x 256 columns), packed stages
-  // (16 KB: 128 rows x 256 columns) and B stages (64 rows x NT tokens).
-  static constexpr int SA = NT >= 128 ? 3 : 4;
-  static constexpr int SP = NT == 256 ? 2 : (NT == 128 ? 3 : 4);
-  static constexpr int SB = NT == 256 ? 3 : 4;
-  static constexpr int BSTAGE = NT * 128;
-  static constexpr int SETS = NT == 256 ? 1 : 2;  // accumulator pairs
-  static constexpr int TMEM_COLS = 2 * NT * SETS < 32 ? 32 : 2 * NT * SETS;
-  static constexpr size_t SMEM = (size_t)SA * kAStage + SP * kPkStage + SB * BSTAGE + 1024 + 512;
-  static_assert(SMEM <= 227 * 1024 && TMEM_COLS <= 512, "does not fit an SM");
+  // Shared memory (227 KB): rings of W stages (32 rows x 256 columns, 16 KB), image stages (64
+  // rows x IT tokens, one per accumulator) and packed stages (128 rows x 256 columns, 16 KB).
+  // A copy takes about 3000 cycles from the release of its slot (a commit's 700 among them), so
+  // the image ring covers four steps of 1024 cycles with two accumulators; the W ring is a
+  // multiple of the unit's four stages, so a warp always fills the same slots.
+  static constexpr int SW = MT == 2 ? 4 : 8;
+  static constexpr int SI = MT == 2 ? 8 : (IT == 128 ? 4 : 8);
+  static constexpr int SP = MT == 2 ? 2 : (IT == 128 ? 2 : (IT == 64 ? 2 : 4));
+  static constexpr int ISTAGE = IT * 128;
+  static constexpr int SETS = 2 / MT;  // accumulator sets of 256 MT columns
+  static constexpr size_t SMEM = (size_t)SW * kWStage + SI * ISTAGE + SP * kPkStage + 1024 + 512;
+  static_assert(SMEM <= 227 * 1024, "does not fit an SM");
+  // the MMA reads 128 rows from an image stage: past a smaller one lies the packed ring (those
+  // lanes are never stored)
+  static_assert(SP * kPkStage >= 128 * 128, "reads past the last image stage stay inside");
 };
 
 struct GradItem {
   int64_t u0, u1;
   int slab, tt, dt;
-  int nacc;   // accumulators of 128 columns: 1 or 2
+  int m;      // accumulators
+  int cols;   // columns: 256, 128 (the last tile of an odd D / 128) or the ranks' image's
   bool rank;  // the tile of the rank sums
 };
 
+template <int MT>
 __device__ __forceinline__ bool grad_item(const GradParams& p, int64_t k, GradItem& it) {
   const int64_t i = blockIdx.x + k * gridDim.x;
   const int64_t per = (int64_t)p.ntt * p.ntiles;
@@ -353,10 +373,9 @@ __device__ __forceinline__ bool grad_item(const GradParams& p, int64_t k, GradIt
   it.dt = (int)(r - (int64_t)it.tt * p.ntiles);
   it.u0 = p.nunits * it.slab / p.slabs;
   it.u1 = p.nunits * (it.slab + 1) / p.slabs;
-  const int64_t nd = (p.h.D + 255) >> 8;
-  it.rank = it.dt >= nd;
-  const int64_t cols = it.rank ? p.h.r_c + p.h.r_r : p.h.D - 256ll * it.dt;
-  it.nacc = cols > 128 ? 2 : 1;
+  it.m = p.nimg - it.tt * MT < MT ? p.nimg - it.tt * MT : MT;
+  it.rank = it.dt >= (int)((p.h.D + 255) >> 8);
+  it.cols = it.rank ? p.fcols : (p.h.D - 256ll * it.dt >= 256 ? 256 : 128);
   return true;
 }
 
@@ -384,8 +403,8 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
       : "memory");
 }
 
-// Two signed bytes (the low two of w's bytes sel, sel + 1) as exact FP16: 1024 + 128 + b is a
-// half whose low mantissa byte is b ^ 0x80.
+// Two signed bytes of w (its bytes sel picks, offset by 128) as exact FP16: the half 1024 + 128 + b
+// has the low mantissa byte b ^ 0x80.
 __device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w_flipped), "r"(0x64646464u), "r"(sel));
@@ -397,43 +416,52 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, 
                : "memory");
 }
 
-// Scales and codes of one vocabulary row for one block of 128 columns (CPC codes).
+// mbar_wait for a wait of many microseconds: sleeps between polls, which would otherwise take
+// issue slots and power from the warps that work.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > (1ll << 31)) {
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+    __nanosleep(200);
+  }
+  return true;
+}
+
+// The code bytes (CPC of them) and 2^-k of one vocabulary row, for one block of 128 columns.
 struct RowLoad {
   uint32_t code;
-  float S, sac, saw;
+  float cs;
 };
 template <int CPC>
-__device__ __forceinline__ RowLoad load_grad_row(const GradParams& p, int64_t v, int64_t col, bool codes) {
-  RowLoad r = {0u, 0.f, 0.f, 0.f};
+__device__ __forceinline__ RowLoad load_grad_row(const GradParams& p, int64_t v, int64_t col) {
+  RowLoad r = {0u, 0.f};
   if (CPC == 0) return r;
-  if (v < p.h.V) {
-    r.S = bf16_bits_to_float(__ldg(p.h.r_super + v));
-    if (p.h.r_c) r.sac = __ldg(p.h.sAc + v);
-    if (p.h.r_r) r.saw = __ldg(p.h.sAw + v);
-  }
-  if (codes) {  // rows past V are padded
-    const uint8_t* c = p.h.r_code + v * (p.h.D >> p.g_shift) + (col >> p.g_shift);
-    if (CPC == 1) r.code = __ldg(c);
-    else if (CPC == 2) r.code = __ldg(reinterpret_cast<const uint16_t*>(c));
-    else r.code = __ldg(reinterpret_cast<const uint32_t*>(c));
-  }
+  r.cs = __ldg(p.cs + v);  // rows past V are padded, as are their codes
+  const uint8_t* c = p.h.r_code + v * (p.h.D >> p.g_shift) + (col >> p.g_shift);
+  if (CPC == 1) r.code = __ldg(c);
+  else if (CPC == 2) r.code = __ldg(reinterpret_cast<const uint16_t*>(c));
+  else r.code = __ldg(reinterpret_cast<const uint32_t*>(c));
   return r;
 }
 
-template <int NT, int CPC>
+template <int IT, int MT, int CPC>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradParams p) {
-  using C = GradCfg<NT>;
+  using C = GradCfg<IT, MT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* As = smem;
-  unsigned char* Bs = As + C::SA * kAStage;
-  unsigned char* Ps = Bs + C::SB * C::BSTAGE;
+  unsigned char* Ws = smem;
+  unsigned char* Is = Ws + C::SW * kWStage;
+  unsigned char* Ps = Is + C::SI * C::ISTAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(Ps + C::SP * kPkStage);
-  uint64_t* a_full = bars;
-  uint64_t* a_empty = a_full + C::SA;
-  uint64_t* b_full = a_empty + C::SA;
-  uint64_t* b_empty = b_full + C::SB;
-  uint64_t* p_full = b_empty + C::SB;
+  uint64_t* w_full = bars;
+  uint64_t* w_empty = w_full + C::SW;
+  uint64_t* i_full = w_empty + C::SW;
+  uint64_t* i_empty = i_full + C::SI;
+  uint64_t* p_full = i_empty + C::SI;
   uint64_t* p_empty = p_full + C::SP;
   uint64_t* acc_full = p_empty + C::SP;
   uint64_t* acc_empty = acc_full + C::SETS;
@@ -442,13 +470,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::SA; ++i) {
-      tc::mbar_init(&a_full[i], kDequantWarps / 2);  // the warps that fill a stage
-      tc::mbar_init(&a_empty[i], 1);
+    for (int i = 0; i < C::SW; ++i) {
+      tc::mbar_init(&w_full[i], kDequantWarps / 4);  // the warps that fill a stage
+      tc::mbar_init(&w_empty[i], 1);
     }
-    for (int i = 0; i < C::SB; ++i) {
-      tc::mbar_init(&b_full[i], 1);
-      tc::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < C::SI; ++i) {
+      tc::mbar_init(&i_full[i], 1);
+      tc::mbar_init(&i_empty[i], 1);
     }
     for (int i = 0; i < C::SP; ++i) {
       tc::mbar_init(&p_full[i], 1);
@@ -461,7 +489,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     tc::mbar_init(mma_done, 1);
     tc::mbar_fence_init();
   }
-  if (warp == kDequantWarps + 6) tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
+  if (warp == kDequantWarps + 6) tc::tmem_alloc(tmem_slot, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -470,154 +498,180 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 
   if (warp < kDequantWarps) {
     // ---- dequantisation: lane = vocabulary row of a 32-row group ----
-    // A warp owns rows 32 rg .. + 31 of each unit, one 128-column block b and half of that
-    // block's 16-byte chunks; the unit's two 64-row halves are two A stages, so eight warps fill
-    // a stage.  %W16%
-    const int rg = warp & 3, b = (warp >> 2) & 1, ch = warp >> 3, h = rg >> 1;
-    const int s = 32 * rg + lane;       // row in the unit
-    const int k = 32 * (rg & 1) + lane;  // row in the stage
-    const uint32_t a_row = tc::smem_u32(As) + (uint32_t)(b * 2) * 8192 + (k >> 3) * 1024 + (k & 7) * 128;
-    const uint32_t x7 = k & 7;
-    int64_t seq = 0;      // units so far
-    int64_t copied = -1;  // last stage copied from the factor image
+    // A warp owns rows 32 rg .. + 31 of each unit (a W stage), one 128-column block b and half of
+    // that block's 16-byte chunks; four warps fill a stage.
+    const int rg = warp & 3, b = (warp >> 2) & 1, ch = warp >> 3;
+    const int s = 32 * rg + lane;  // row in the unit
+    const uint32_t w_row = tc::smem_u32(Ws) + (uint32_t)(b * 2) * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
+    const uint32_t x7 = lane & 7;
+    // where the chunk of columns 32 wn + 16 ch + 8 c lies in its 128-byte row (wn even, c = 0)
+    const uint32_t at0 = (uint32_t)((2 * ch) ^ x7) << 4;
+    const unsigned char* const p_src = Ps + b * 8192 + s * 16 + 2 * ch * 2048;
+    constexpr int SU = C::SW / 4;  // units in the W ring
+    int wu = 0;                    // this unit's place in it: slot 4 wu + rg
+    uint32_t wp = 1;               // parity of the slot's last release (the first use waits for none)
     int ps = 0;
     uint32_t pp = 0;
+    int copied = -1;               // slot of the last copy from the factor image, its parity
+    uint32_t copied_par = 0;
     bool ok = true;
-    for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+    grid_dependency_wait();  // the row table and the factor image come from kernels before this
+    auto next_w = [&]() {
+      if (++wu == SU) {
+        wu = 0;
+        wp ^= 1u;
+      }
+    };
+    for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
       if (it.rank) {
-        // Whole stages from the factor image, copied by one of the eight warps of a half; the
-        // others only keep pace (a warp that skipped stages would lose count of the phases).
-        const uint32_t bytes = (uint32_t)p.fcols * 128u;
-        grid_dependency_wait();  // the image comes from a kernel before this one
-        for (int64_t u = it.u0; u < it.u1; ++u, ++seq) {
-          const int64_t ks = 2 * seq + h;
-          const int slot = (int)(ks % C::SA);
-          const int64_t use = ks / C::SA;
-          if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&a_empty[slot], (uint32_t)(use - 1) & 1u, p.err))) {
+        // Whole stages from the factor image, copied by one of a stage's four warps; the others
+        // only keep pace (a warp that skipped stages would lose count of the phases).
+        const uint32_t bytes = (uint32_t)p.fcols * 64u;
+        for (int64_t u = it.u0; u < it.u1; ++u) {
+          const int slot = 4 * wu + rg;
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err))) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            if ((warp & 13) == 0) {
-              tc::mbar_arrive_expect_tx(&a_full[slot], bytes);
-              tc::bulk_g2s(As + slot * kAStage, p.fimg + (2 * u + h) * bytes, bytes, &a_full[slot]);
-              copied = ks;
+            if (warp < 4) {
+              tc::mbar_arrive_expect_tx(&w_full[slot], bytes);
+              tc::bulk_g2s(Ws + slot * kWStage, p.fimg + (4 * u + rg) * bytes, bytes, &w_full[slot]);
+              copied = slot;
+              copied_par = wp ^ 1u;
             } else {
-              tc::mbar_arrive(&a_full[slot]);
+              tc::mbar_arrive(&w_full[slot]);
             }
           }
           __syncwarp();
+          next_w();
         }
         continue;
       }
-      const bool work = b < it.nacc;
-      const int64_t col = 256ll * it.dt + 128 * b;
-      RowLoad nx = load_grad_row<CPC>(p, it.u0 * kUnit + s, col, work);
-      for (int64_t u = it.u0; u < it.u1; ++u, ++seq) {
-        const RowLoad r = nx;
-        const int64_t v = u * kUnit + s;
-        if (u + 1 < it.u1) nx = load_grad_row<CPC>(p, v + kUnit, col, work);
-        uint32_t w[8];
-        uint4 raw[4];
-        if (CPC != 0) {
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err))) {
-            ok = false;
-            break;
-          }
-          const unsigned char* src = Ps + ps * kPkStage + b * 8192 + s * 16;
-          if (work) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint4 q = *reinterpret_cast<const uint4*>(src + (2 * ch + c) * 2048);
-              w[4 * c] = q.x;
-              w[4 * c + 1] = q.y;
-              w[4 * c + 2] = q.z;
-              w[4 * c + 3] = q.w;
-            }
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&p_empty[ps]);
-          if (++ps == C::SP) {
-            ps = 0;
-            pp ^= 1u;
-          }
+      const bool work = 128 * b < it.cols;
+      const int64_t col = 256ll * it.dt + (work ? 128 * b : 0);
+      // One unit ahead: its packed chunks are read into registers while this unit's entries are
+      // stored, and the barriers of the next steps are probed before their answers are needed.
+      RowLoad r = load_grad_row<CPC>(p, it.u0 * kUnit + s, col);
+      uint4 q[2];
+      auto take_packed = [&](bool ready) -> bool {  // q = the next packed unit
+        if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err)))
+          return false;
+        if (work) {
+          q[0] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage);
+          q[1] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage + 2048);
         }
-        if (CPC == 0 && work) {  // INT8 rows straight from global memory
-          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            raw[c] = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
+        return true;
+      };
+      auto free_packed = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_empty[ps]);
+        if (++ps == C::SP) {
+          ps = 0;
+          pp ^= 1u;
         }
-        const int64_t ks = 2 * seq + h;
-        const int slot = (int)(ks % C::SA);
-        const int64_t use = ks / C::SA;
-        if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&a_empty[slot], (uint32_t)(use - 1) & 1u, p.err))) {
+      };
+      if (CPC != 0) {
+        if (!take_packed(false)) {
           ok = false;
           break;
         }
-        const uint32_t dst = a_row + slot * kAStage;
-        if (work) {
-          if (CPC == 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the half block
-              const uint32_t q[4] = {raw[c].x ^ 0x80808080u, raw[c].y ^ 0x80808080u,
-                                     raw[c].z ^ 0x80808080u, raw[c].w ^ 0x80808080u};
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t at = dst + ch * 8192 + (((2 * c + e) ^ x7) << 4);
-                st_shared16(at, h2_bits(bytes_to_half2(q[2 * e], 0x4140)), h2_bits(bytes_to_half2(q[2 * e], 0x4342)),
-                            h2_bits(bytes_to_half2(q[2 * e + 1], 0x4140)), h2_bits(bytes_to_half2(q[2 * e + 1], 0x4342)));
-              }
-            }
-          } else {
-            const float cs = grad_row(r.S, r.sac, r.saw).cs;
+        free_packed();
+      }
+      for (int64_t u = it.u0; u < it.u1; ++u) {
+        const int64_t v = u * kUnit + s;
+        const int slot = 4 * wu + rg;
+        const bool more = u + 1 < it.u1;
+        const bool w_ready = tc::mbar_test(&w_empty[slot], wp);
+        bool p_ready = CPC != 0 && more && tc::mbar_test(&p_full[ps], pp);
+        // The entries are made in registers before the wait for the stage's slot, so a slot is
+        // empty only for the stores.
+        uint32_t o[8][4];  // 16-byte chunks of eight columns
+        if (CPC != 0) {
+          const RowLoad now = r;
+          if (more) r = load_grad_row<CPC>(p, v + kUnit, col);
+          if (work) {
 #pragma unroll
             for (int wn = 0; wn < 4; ++wn) {  // window of 32 columns
-              const uint32_t cw = CPC == 1 ? r.code : (CPC == 2 ? (r.code >> (8 * (wn >> 1))) & 0xFFu : (r.code >> (8 * wn)) & 0xFFu);
-              const __half2 c2 = __float2half2_rn((float)cw * cs);  // exact for k <= 24
+              const uint32_t cw = CPC == 1 ? now.code : (CPC == 2 ? (now.code >> (8 * (wn >> 1))) & 0xFFu : (now.code >> (8 * wn)) & 0xFFu);
+              const __half2 c2 = __float2half2_rn((float)cw * now.cs);  // exact for k <= 24
               const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7: one 16-byte chunk
-                __half2 o[4];
-                dequant_word(w[4 * c + wn], c2, nc24, o);
-                st_shared16(dst + (wn >> 1) * 8192 + (((((wn & 1) << 2) + 2 * ch + c) ^ x7) << 4), h2_bits(o[0]),
-                            h2_bits(o[1]), h2_bits(o[2]), h2_bits(o[3]));
+              for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7
+                const uint32_t word = wn == 0 ? q[c].x : (wn == 1 ? q[c].y : (wn == 2 ? q[c].z : q[c].w));
+                __half2 e[4];
+                dequant_word(word, c2, nc24, e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[2 * wn + c][j] = h2_bits(e[j]);
               }
             }
           }
+          if (more && !take_packed(p_ready)) {
+            ok = false;
+            break;
+          }
+        } else if (work) {  // INT8 rows straight from global memory
+          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the half block
+            const uint4 raw = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u, raw.w ^ 0x80808080u};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[2 * c + (j >> 2)][j & 3] = h2_bits(bytes_to_half2(x[j >> 1], (j & 1) ? 0x4342 : 0x4140));
+          }
+        }
+        if (!__all_sync(0xffffffffu, w_ready) &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err))) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = w_row + slot * kWStage;
+        if (work) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            // SC4: window c / 2, chunk 4 (c / 2 % 2) + 2 ch + c % 2 of its 64-column atom; INT8: the
+            // atom ch, chunk c
+            const uint32_t at = CPC != 0 ? (c >> 2) * 4096 + (at0 ^ (uint32_t)((((c >> 1) & 1) * 4 + (c & 1)) << 4))
+                                         : ch * 4096 + (uint32_t)((c ^ x7) << 4);
+            st_shared16(dst + at, o[c][0], o[c][1], o[c][2], o[c][3]);
+          }
         }
         tc::fence_proxy_async_smem();  // the MMA reads the stage through the async proxy
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&a_full[slot]);
+        if (CPC != 0 && more) free_packed();
+        else __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&w_full[slot]);
+        next_w();
       }
     }
-    if (!ok && copied >= 0)  // a copy may still be in flight
-      tc::mbar_wait(&a_full[copied % C::SA], (uint32_t)(copied / C::SA) & 1u, p.err);
+    if (!ok && copied >= 0) tc::mbar_wait(&w_full[copied], copied_par, p.err);  // a copy may be in flight
   } else if (warp < kDequantWarps + 4) {
-    // ---- epilogue: lane = column of the tile; raw sums to scratch ----
+    // ---- epilogue: lane = token; raw sums to scratch ----
     const int e = warp - kDequantWarps;
     const uint32_t lane_off = (uint32_t)(32 * e) << 16;
-    for (int64_t i = 0; grad_item(p, i, it); ++i) {
+    for (int64_t i = 0; grad_item<MT>(p, i, it); ++i) {
       const int set = (int)(i % C::SETS);
       const int64_t use = i / C::SETS;
-      if (!tc::bar_and(1, 128, tc::mbar_wait(&acc_full[set], (uint32_t)use & 1u, p.err))) break;
+      if (!tc::bar_and(1, 128, mbar_wait_long(&acc_full[set], (uint32_t)use & 1u, p.err))) break;
       tc::fence_after_sync();
-      const int64_t tok0 = (int64_t)it.tt * NT;
-      const int64_t ntok = p.n - tok0 < NT ? p.n - tok0 : NT;
       const int RR = p.h.r_c + p.h.r_r;
+      const int live = it.rank ? (RR + 3) & ~3 : it.cols;  // (rows of scratch end on a multiple of 4)
+      const int t = 32 * e + lane;
 #pragma unroll 1
-      for (int a = 0; a < it.nacc; ++a) {
-        const int64_t c = 128 * a + 32 * e + lane;
-        const bool live = it.rank ? c < RR : true;
-        float* dst = p.part + ((int64_t)it.slab * p.n + tok0) * p.dp + (it.rank ? p.h.D : 256ll * it.dt) + c;
+      for (int m = 0; m < it.m; ++m) {
+        const int64_t n = ((int64_t)it.tt * MT + m) * IT + t;
+        const bool mine = t < IT && n < p.n;
+        float* dst = p.part + ((int64_t)it.slab * p.n + n) * p.dp + (it.rank ? p.h.D : 256ll * it.dt);
+        if (32 * e >= IT) break;  // (warp-uniform)
 #pragma unroll 1
-        for (int c0 = 0; c0 < NT; c0 += 16) {
+        for (int c0 = 0; c0 < it.cols; c0 += 16) {
           float y[16];
-          tc::tmem_ld16(tbase + (set * 2 + a) * NT + lane_off + c0, y);
-          if (live) {
+          tc::tmem_ld16(tbase + (set * MT + m) * 256 + lane_off + c0, y);
+          if (mine) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-              if (c0 + q < ntok) __stcs(dst + (c0 + q) * p.dp, y[q]);
+            for (int q = 0; q < 16; q += 4)
+              if (c0 + q < live)
+                __stcs(reinterpret_cast<float4*>(dst + c0 + q), make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]));
           }
         }
       }
@@ -632,9 +686,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
       int ps = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+      for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
         if (it.rank) continue;
-        const uint32_t bytes = (uint32_t)it.nacc * 8192u;
+        const uint32_t bytes = (uint32_t)it.cols * 64u;
         for (int64_t u = it.u0; u < it.u1; ++u) {
           if (np >= C::SP && !tc::mbar_wait(&p_empty[ps], ph ^ 1u, p.err)) {
             ok = false;
@@ -655,79 +709,95 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
           tc::mbar_wait(&p_full[q % C::SP], (uint32_t)(q / C::SP) & 1u, p.err);
     }
   } else if (warp == kDequantWarps + 5) {
-    // ---- B producer (one thread): the image, written by the kernel before this one ----
+    // ---- image producer (one thread); the image comes from the kernel before this one ----
     if (lane == 0) {
       grid_dependency_wait();
-      int64_t nb = 0;
-      int bs = 0;
+      const int64_t tile_bytes = p.nunits * 2 * C::ISTAGE;
+      int64_t ni = 0;
+      int is = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
-        const char* src = p.img + ((int64_t)it.tt * p.nunits * 2 + 2 * it.u0) * C::BSTAGE;
-        for (int64_t u = 2 * it.u0; u < 2 * it.u1; ++u) {
-          if (nb >= C::SB && !tc::mbar_wait(&b_empty[bs], ph ^ 1u, p.err)) {
-            ok = false;
-            break;
-          }
-          tc::mbar_arrive_expect_tx(&b_full[bs], C::BSTAGE);
-          tc::bulk_g2s(Bs + bs * C::BSTAGE, src, C::BSTAGE, &b_full[bs]);
-          src += C::BSTAGE;
-          ++nb;
-          if (++bs == C::SB) {
-            bs = 0;
-            ph ^= 1u;
+      for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
+        const char* src = p.img + (int64_t)it.tt * MT * tile_bytes + 2 * it.u0 * C::ISTAGE;
+        for (int64_t u = 2 * it.u0; ok && u < 2 * it.u1; ++u, src += C::ISTAGE) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (m >= it.m) break;
+            if (ni >= C::SI && !tc::mbar_wait(&i_empty[is], ph ^ 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            tc::mbar_arrive_expect_tx(&i_full[is], C::ISTAGE);
+            tc::bulk_g2s(Is + is * C::ISTAGE, src + m * tile_bytes, C::ISTAGE, &i_full[is]);
+            ++ni;
+            if (++is == C::SI) {
+              is = 0;
+              ph ^= 1u;
+            }
           }
         }
       }
       if (!ok)
-        for (int64_t q = nb < C::SB ? 0 : nb - C::SB; q < nb; ++q)
-          tc::mbar_wait(&b_full[q % C::SB], (uint32_t)(q / C::SB) & 1u, p.err);
+        for (int64_t q = ni < C::SI ? 0 : ni - C::SI; q < ni; ++q)
+          tc::mbar_wait(&i_full[q % C::SI], (uint32_t)(q / C::SI) & 1u, p.err);
     }
   } else {
     // ---- MMA issuer: the whole warp, one elected lane issues ----
-    const uint32_t idesc = tc::idesc_f16_m128(NT) | (1u << 15);  // A is MN-major
-    const uint64_t adesc0 = desc_mn_sw128(tc::smem_u32(As), 8192, 1024);
-    const uint64_t bdesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Bs));
-    int sa = 0, sb = 0;
-    uint32_t pa = 0, pb = 0;
+    // A step is 64 rows: two W stages and one image stage per accumulator.  Their barriers are
+    // probed together, then one thread issues the whole step.
+    const uint64_t bdesc0 = desc_mn_sw128(tc::smem_u32(Ws), 4096, 1024);
+    const uint64_t adesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Is));
+    int sw = 0, si = 0;
+    uint32_t pw = 0, pi = 0;
     bool ok = true;
-    for (int64_t i = 0; ok && grad_item(p, i, it); ++i) {
+    for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
       const int set = (int)(i % C::SETS);
       const int64_t use = i / C::SETS;
       if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[set], (uint32_t)(use - 1) & 1u, p.err)))
         break;
       tc::fence_after_sync();
-      const uint32_t d0 = tbase + set * 2 * NT;
+      const uint32_t idesc = tc::idesc_f16_m128(it.cols) | (1u << 16);  // B is MN-major
+      const uint32_t d = tbase + set * MT * 256;
       const int64_t k1 = 2 * (it.u1 - it.u0);
       for (int64_t kk = 0; kk < k1; ++kk) {
-        const bool ra = tc::mbar_try_wait(&a_full[sa], pa);
-        const bool rb = tc::mbar_try_wait(&b_full[sb], pb);
-        if (!__all_sync(0xffffffffu, (ra && rb) || (tc::mbar_wait(&a_full[sa], pa, p.err) &&
-                                                     tc::mbar_wait(&b_full[sb], pb, p.err)))) {
+        const int si1 = si + 1 == C::SI ? 0 : si + 1;
+        const uint32_t pi1 = si + 1 == C::SI ? pi ^ 1u : pi;
+        const bool two = MT == 2 && it.m == 2;
+        const bool r0 = tc::mbar_try_wait(&w_full[sw], pw), r1 = tc::mbar_try_wait(&w_full[sw + 1], pw);
+        const bool r2 = tc::mbar_try_wait(&i_full[si], pi), r3 = !two || tc::mbar_try_wait(&i_full[si1], pi1);
+        if (!__all_sync(0xffffffffu, r0 && r1 && r2 && r3) &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(&w_full[sw], pw, p.err) && tc::mbar_wait(&w_full[sw + 1], pw, p.err) &&
+                                         tc::mbar_wait(&i_full[si], pi, p.err) &&
+                                         (!two || tc::mbar_wait(&i_full[si1], pi1, p.err)))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint64_t ad = adesc0 + (uint64_t)((sa * kAStage) >> 4);
-        const uint64_t bd = bdesc0 + (uint64_t)((sb * C::BSTAGE) >> 4);
+        const uint64_t bd = bdesc0 + (uint64_t)((sw * kWStage) >> 4);
+        const uint64_t ad0 = adesc0 + (uint64_t)((si * C::ISTAGE) >> 4), ad1 = adesc0 + (uint64_t)((si1 * C::ISTAGE) >> 4);
         if (tc::elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // K steps of 16 rows: two 8-row atoms of A, 32 bytes of B
-            mma_f16_ss(d0, ad + ((j * 2048) >> 4), bd + ((j * 32) >> 4), idesc, (kk | j) != 0);
-            if (it.nacc == 2)
-              mma_f16_ss(d0 + NT, ad + ((16384 + j * 2048) >> 4), bd + ((j * 32) >> 4), idesc, (kk | j) != 0);
+          for (int j = 0; j < 4; ++j) {  // K steps of 16 rows: 32 bytes of A, two 8-row atoms of B
+            const uint64_t bj = bd + (uint64_t)(((j >> 1) * kWStage + (j & 1) * 2048) >> 4);
+            mma_f16_ss(d, ad0 + ((j * 32) >> 4), bj, idesc, (kk | j) != 0);
+            if (two) mma_f16_ss(d + 256, ad1 + ((j * 32) >> 4), bj, idesc, (kk | j) != 0);
+            if (j == 1) tc::mma_commit(&w_empty[sw]);
           }
-          tc::mma_commit(&a_empty[sa]);
-          tc::mma_commit(&b_empty[sb]);
+          tc::mma_commit(&w_empty[sw + 1]);
+          tc::mma_commit(&i_empty[si]);
+          if (two) tc::mma_commit(&i_empty[si1]);
         }
         __syncwarp();
-        if (++sa == C::SA) {
-          sa = 0;
-          pa ^= 1u;
+        sw += 2;
+        if (sw == C::SW) {
+          sw = 0;
+          pw ^= 1u;
         }
-        if (++sb == C::SB) {
-          sb = 0;
-          pb ^= 1u;
+        si = two ? si1 : si;
+        pi = two ? pi1 : pi;
+        if (++si == C::SI) {
+          si = 0;
+          pi ^= 1u;
         }
       }
       if (ok && tc::elect_one()) tc::mma_commit(&acc_full[set]);
@@ -743,7 +813,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
   __syncthreads();
   if (warp == kDequantWarps + 6) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tbase, C::TMEM_COLS);
+    tc::tmem_dealloc(tbase, 512);
   }
 }
 
@@ -907,31 +977,34 @@ int sm_count() {
 }
 
 struct GradPlan {
-  int nt, ntt, ntiles, slabs;
+  int it, mt;  // tokens per image tile, image tiles per item
+  int nimg, ntt, ntiles, slabs;
   int64_t npad, nunits, dp;
   int fcols;
-  size_t o_img, o_fimg, o_sp, o_row, o_spmax, o_amax, o_texp, o_tok, o_part, bytes;
+  size_t o_img, o_fimg, o_sp, o_cs, o_row, o_spmax, o_amax, o_texp, o_tok, o_part, bytes;
 };
 
 GradPlan grad_plan(const archead_head& h, int64_t n) {
   GradPlan g;
   const int RR = h.r_c + h.r_r;
-  g.nt = n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : 256)));
-  g.ntt = (int)((n + g.nt - 1) / g.nt);
-  g.npad = (int64_t)g.ntt * g.nt;
+  g.it = n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 64 ? 64 : 128));
+  g.mt = n <= 128 ? 1 : 2;
+  g.nimg = (int)((n + g.it - 1) / g.it);
+  g.ntt = (g.nimg + g.mt - 1) / g.mt;
+  g.npad = (int64_t)g.nimg * g.it;
   g.ntiles = (int)((h.D + 255) / 256) + (RR > 0);
   g.nunits = (h.V + kUnit - 1) / kUnit;
   g.dp = (h.D + RR + 3) / 4 * 4;
   // Slabs of the vocabulary: CTAs run items of equal length side by side, so the time is that of
-  // ceil(items / CTAs) rounds of 1 / slabs each, plus the partial sums' way through memory (an
-  // element written and read costs about as long as 1.2e-6 of a full-length tile).
+  // ceil(items / CTAs) rounds of 1 / slabs each, plus the partial sums' way through memory.
+  // Measured: about 1.2 us per unit of 128 rows with two accumulators, 0.7 us with one.
   const int64_t tiles = (int64_t)g.ntt * g.ntiles;
   const int64_t sms = sm_count();
   double best = 1e300;
   g.slabs = 1;
   for (int s = 1; s <= 64 && s * 4 <= g.nunits + 3; ++s) {
     const double rounds = (double)((tiles * s + sms - 1) / sms) / s;
-    const double tile_us = g.nunits * (g.nt == 256 ? 1.25 : (g.nt == 128 ? 0.8 : 0.55));
+    const double tile_us = g.nunits * (g.mt == 2 ? 1.2 : 0.7);
     const double cost = rounds * tile_us + 8.0 * s * n * g.dp / 4e6;
     if (cost < best * 0.995) {
       best = cost;
@@ -948,6 +1021,7 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   g.fcols = (RR + 63) / 64 * 64;
   g.o_fimg = take((size_t)g.nunits * kUnit * g.fcols * 2);
   g.o_sp = take((size_t)g.nunits * kUnit * 4);
+  g.o_cs = take((size_t)g.nunits * kUnit * 4);
   g.o_row = take((size_t)g.nunits * kUnit * 8);
   g.o_spmax = take(kRowBlocks * 4);
   g.o_amax = take((size_t)n * 4);
@@ -973,26 +1047,27 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, int threads, size_t smem, cudaStrea
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int NT, int CPC>
+template <int IT, int MT, int CPC>
 cudaError_t launch_grad_cfg(const GradParams& p, cudaStream_t st) {
-  auto kern = grad_tc_kernel<NT, CPC>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradCfg<NT>::SMEM);
+  auto kern = grad_tc_kernel<IT, MT, CPC>;
+  constexpr size_t smem = GradCfg<IT, MT>::SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)p.ntt * p.ntiles * p.slabs, sms = sm_count();
-  return launch_pdl(kern, dim3((unsigned)(items < sms ? items : sms)), kGradThreads, GradCfg<NT>::SMEM, st, p);
+  return launch_pdl(kern, dim3((unsigned)(items < sms ? items : sms)), kGradThreads, smem, st, p);
 }
 
-template <int NT>
-cudaError_t launch_grad_nt(const GradParams& p, cudaStream_t st) {
-  if (p.h.format == ARCHEAD_FMT_ROW8) return launch_grad_cfg<NT, 0>(p, st);
-  if (p.h.g == 32) return launch_grad_cfg<NT, 4>(p, st);
-  if (p.h.g == 64) return launch_grad_cfg<NT, 2>(p, st);
-  return launch_grad_cfg<NT, 1>(p, st);
+template <int IT, int MT>
+cudaError_t launch_grad_it(const GradParams& p, cudaStream_t st) {
+  if (p.h.format == ARCHEAD_FMT_ROW8) return launch_grad_cfg<IT, MT, 0>(p, st);
+  if (p.h.g == 32) return launch_grad_cfg<IT, MT, 4>(p, st);
+  if (p.h.g == 64) return launch_grad_cfg<IT, MT, 2>(p, st);
+  return launch_grad_cfg<IT, MT, 1>(p, st);
 }
 
 struct GradParts {
   char *img, *fimg;
-  float *sp, *spmax, *tok, *part;
+  float *sp, *cs, *spmax, *tok, *part;
   float2* row;
   unsigned* amax;
   int* texp;
@@ -1003,6 +1078,7 @@ GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
   q.img = b + g.o_img;
   q.fimg = b + g.o_fimg;
   q.sp = reinterpret_cast<float*>(b + g.o_sp);
+  q.cs = reinterpret_cast<float*>(b + g.o_cs);
   q.spmax = reinterpret_cast<float*>(b + g.o_spmax);
   q.tok = reinterpret_cast<float*>(b + g.o_tok);
   q.part = reinterpret_cast<float*>(b + g.o_part);
@@ -1015,14 +1091,14 @@ GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
 TokensParams tokens_params(const HeadGrad& a, const SoftmaxTokens& t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  return {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.tok, b.texp, b.img, g.nt, a.err};
+  return {a.n, a.head->V, g.nunits * kUnit, b.sp, b.spmax, t, b.tok, b.texp, b.img, g.it, a.err};
 }
 
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
   const int group = g.npad <= 64 ? 4 : (g.npad <= 256 ? 8 : 32);
-  const ImageParams p = {src, a.n, g.npad, a.head->V, g.nt, group, b.sp, b.spmax, b.amax,
+  const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, group, b.sp, b.spmax, b.amax,
                          t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
   const dim3 grid((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + group - 1) / group));
   const bool pairs = a.head->V % 2 == 0 && reinterpret_cast<uintptr_t>(src) % 8 == 0;
@@ -1042,7 +1118,7 @@ cudaError_t grad_rows(const HeadGrad& a, bool dy) {
   const archead_head& h = *a.head;
   const GradPlan g = grad_plan(h, a.n);
   const GradParts b = grad_parts(a, g);
-  const RowsParams p = {h, g.nunits * kUnit, b.sp, dy ? nullptr : b.row, b.spmax, dy ? b.amax : nullptr, a.n,
+  const RowsParams p = {h, g.nunits * kUnit, b.sp, b.cs, dy ? nullptr : b.row, b.spmax, dy ? b.amax : nullptr, a.n,
                         g.fcols ? b.fimg : nullptr, g.fcols, h.r_c % 4 == 0 && h.r_r % 4 == 0};
   grad_rows_kernel<<<kRowBlocks, 1024, 0, a.st>>>(p);
   ++*a.launches;
@@ -1080,14 +1156,17 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   const GradParts b = grad_parts(a, g);
   int gs = 0;
   while ((1 << gs) < h.g) ++gs;
-  const GradParams p = {h, b.img, b.part, a.n, g.dp, g.nunits, g.ntt, g.ntiles, g.slabs, gs, b.fimg, g.fcols, a.err};
+  const GradParams p = {h, b.img, b.cs, b.part, a.n, g.dp, g.nunits, g.nimg, g.ntt, g.ntiles, g.slabs, gs, b.fimg, g.fcols, a.err};
   cudaError_t e;
-  switch (g.nt) {
-    case 16: e = launch_grad_nt<16>(p, a.st); break;
-    case 32: e = launch_grad_nt<32>(p, a.st); break;
-    case 64: e = launch_grad_nt<64>(p, a.st); break;
-    case 128: e = launch_grad_nt<128>(p, a.st); break;
-    default: e = launch_grad_nt<256>(p, a.st); break;
+  if (g.mt == 2) {
+    e = launch_grad_it<128, 2>(p, a.st);
+  } else {
+    switch (g.it) {
+      case 16: e = launch_grad_it<16, 1>(p, a.st); break;
+      case 32: e = launch_grad_it<32, 1>(p, a.st); break;
+      case 64: e = launch_grad_it<64, 1>(p, a.st); break;
+      default: e = launch_grad_it<128, 1>(p, a.st); break;
+    }
   }
   if (e != cudaSuccess) return e;
   const FinishParams fp = {h, b.part, a.n, g.dp, g.slabs, b.texp, dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
