@@ -27,7 +27,7 @@ namespace archead {
 namespace {
 
 constexpr int kDequantWarps = 16;
-constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 2 producers, 1 MMA
+constexpr int kGradThreads = 32 * (kDequantWarps + 8);  // + 4 epilogue, 2 producers, 2 MMA
 constexpr int kUnit = 128;                              // vocabulary rows per unit of K
 constexpr int kWStage = 32 * 256 * 2;                   // 32 rows x 256 columns FP16
 constexpr int kPkStage = 16384;                         // 128 rows x 256 columns of nibbles
@@ -341,12 +341,15 @@ struct GradCfg {
   // rows x IT tokens, one per accumulator) and packed stages (128 rows x 256 columns, 16 KB).
   // A copy takes about 3000 cycles from the release of its slot (a commit's 700 among them), so
   // the image ring covers four steps of 1024 cycles with two accumulators; the W ring is a
-  // multiple of the unit's four stages, so a warp always fills the same slots.
+  // multiple of the unit's four stages, so a warp always fills the same slots.  Two threads issue
+  // MMAs, each into its own accumulator of 256 columns: one alone left the tensor cores idle for
+  // about 350 cycles between steps (barrier round trips; an issue returns when the MMA before it
+  // is nearly done).  With MT = 2 an accumulator is an image tile; with MT = 1 the steps alternate
+  // between the two, which the epilogue adds.
   static constexpr int SW = MT == 2 ? 4 : 8;
   static constexpr int SI = MT == 2 ? 8 : (IT == 128 ? 4 : 8);
   static constexpr int SP = MT == 2 ? 2 : (IT == 128 ? 2 : (IT == 64 ? 2 : 4));
   static constexpr int ISTAGE = IT * 128;
-  static constexpr int SETS = 2 / MT;  // accumulator sets of 256 MT columns
   static constexpr size_t SMEM = (size_t)SW * kWStage + SI * ISTAGE + SP * kPkStage + 1024 + 512;
   static_assert(SMEM <= 227 * 1024, "does not fit an SM");
   // the MMA reads 128 rows from an image stage: past a smaller one lies the packed ring (those
@@ -464,15 +467,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
   uint64_t* p_full = i_empty + C::SI;
   uint64_t* p_empty = p_full + C::SP;
   uint64_t* acc_full = p_empty + C::SP;
-  uint64_t* acc_empty = acc_full + C::SETS;
-  uint64_t* mma_done = acc_empty + C::SETS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* mma_done = acc_empty + 1;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SW; ++i) {
-      tc::mbar_init(&w_full[i], kDequantWarps / 4);  // the warps that fill a stage
-      tc::mbar_init(&w_empty[i], 1);
+      tc::mbar_init(&w_full[i], MT == 2 ? 4 : 2);  // the warps that fill a stage
+      tc::mbar_init(&w_empty[i], MT);              // the issuers that read it
     }
     for (int i = 0; i < C::SI; ++i) {
       tc::mbar_init(&i_full[i], 1);
@@ -480,13 +483,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     }
     for (int i = 0; i < C::SP; ++i) {
       tc::mbar_init(&p_full[i], 1);
-      tc::mbar_init(&p_empty[i], kDequantWarps);
+      tc::mbar_init(&p_empty[i], kDequantWarps / (3 - MT));
     }
-    for (int i = 0; i < C::SETS; ++i) {
-      tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 128);
-    }
-    tc::mbar_init(mma_done, 1);
+    tc::mbar_init(acc_full, 2);
+    tc::mbar_init(acc_empty, 128);
+    tc::mbar_init(&mma_done[0], 1);
+    tc::mbar_init(&mma_done[1], 1);
     tc::mbar_fence_init();
   }
   if (warp == kDequantWarps + 6) tc::tmem_alloc(tmem_slot, 512);
@@ -498,53 +500,49 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 
   if (warp < kDequantWarps) {
     // ---- dequantisation: lane = vocabulary row of a 32-row group ----
-    // A warp owns rows 32 rg .. + 31 of each unit (a W stage), one 128-column block b and half of
-    // that block's 16-byte chunks; four warps fill a stage.
-    const int rg = warp & 3, b = (warp >> 2) & 1, ch = warp >> 3;
+    // A warp owns rows 32 rg .. + 31 (a W stage) and one 128-column block b: with two accumulators
+    // half of that block's 16-byte chunks in every unit; with one, where units follow one another
+    // twice as fast, all of them in every other unit, which halves what a unit pays for barriers
+    // and fences (N = 1: %UG%).
+    constexpr int NH = 3 - MT;  // halves of the chunks per warp, and groups of warps by unit
+    const int rg = warp & 3, b = (warp >> 2) & 1, grp = warp >> 3;
     const int s = 32 * rg + lane;  // row in the unit
     const uint32_t w_row = tc::smem_u32(Ws) + (uint32_t)(b * 2) * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
     const uint32_t x7 = lane & 7;
-    // where the chunk of columns 32 wn + 16 ch + 8 c lies in its 128-byte row (wn even, c = 0)
-    const uint32_t at0 = (uint32_t)((2 * ch) ^ x7) << 4;
-    const unsigned char* const p_src = Ps + b * 8192 + s * 16 + 2 * ch * 2048;
-    constexpr int SU = C::SW / 4;  // units in the W ring
-    int wu = 0;                    // this unit's place in it: slot 4 wu + rg
-    uint32_t wp = 1;               // parity of the slot's last release (the first use waits for none)
-    int ps = 0;
+    const unsigned char* const p_src = Ps + b * 8192 + s * 16;
+    const int slot = NH == 2 ? 4 * grp + rg : rg;  // its place in the W ring (one or two units)
+    static_assert(C::SW == 4 * NH && C::SP % NH == 0, "a slot belongs to one group of warps");
+    uint32_t wp = 1;  // parity of the slot's last release (the first use waits for none)
+    int ps = NH == 2 ? grp : 0;
     uint32_t pp = 0;
-    int copied = -1;               // slot of the last copy from the factor image, its parity
-    uint32_t copied_par = 0;
+    int64_t seq = 0;  // units of this CTA so far
+    bool copied = false;  // a copy from the factor image was the slot's last use
     bool ok = true;
     grid_dependency_wait();  // the row table and the factor image come from kernels before this
-    auto next_w = [&]() {
-      if (++wu == SU) {
-        wu = 0;
-        wp ^= 1u;
-      }
-    };
     for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
+      // this warp's units of the item
+      const int64_t ua = NH == 2 ? it.u0 + ((seq ^ grp) & 1) : it.u0;
+      seq += it.u1 - it.u0;
       if (it.rank) {
-        // Whole stages from the factor image, copied by one of a stage's four warps; the others
-        // only keep pace (a warp that skipped stages would lose count of the phases).
+        // Whole stages from the factor image, copied by one of a stage's warps; the others only
+        // keep pace (a warp that skipped stages would lose count of the phases).
         const uint32_t bytes = (uint32_t)p.fcols * 64u;
-        for (int64_t u = it.u0; u < it.u1; ++u) {
-          const int slot = 4 * wu + rg;
+        for (int64_t u = ua; u < it.u1; u += NH) {
           if (!__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err))) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            if (warp < 4) {
+            if (b == 0 && (NH == 2 || grp == 0)) {
               tc::mbar_arrive_expect_tx(&w_full[slot], bytes);
               tc::bulk_g2s(Ws + slot * kWStage, p.fimg + (4 * u + rg) * bytes, bytes, &w_full[slot]);
-              copied = slot;
-              copied_par = wp ^ 1u;
+              copied = true;
             } else {
               tc::mbar_arrive(&w_full[slot]);
             }
           }
           __syncwarp();
-          next_w();
+          wp ^= 1u;
         }
         continue;
       }
@@ -552,107 +550,112 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
       const int64_t col = 256ll * it.dt + (work ? 128 * b : 0);
       // One unit ahead: its packed chunks are read into registers while this unit's entries are
       // stored, and the barriers of the next steps are probed before their answers are needed.
-      RowLoad r = load_grad_row<CPC>(p, it.u0 * kUnit + s, col);
-      uint4 q[2];
+      RowLoad r = {0u, 0.f};
+      if (ua < it.u1) r = load_grad_row<CPC>(p, ua * kUnit + s, col);
+      uint4 q[2 * NH];
       auto take_packed = [&](bool ready) -> bool {  // q = the next packed unit
         if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err)))
           return false;
         if (work) {
-          q[0] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage);
-          q[1] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage + 2048);
+#pragma unroll
+          for (int c = 0; c < 2 * NH; ++c)
+            q[c] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage + (NH == 2 ? c : 2 * grp + c) * 2048);
         }
         return true;
       };
       auto free_packed = [&]() {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&p_empty[ps]);
-        if (++ps == C::SP) {
-          ps = 0;
+        ps += NH;
+        if (ps >= C::SP) {
+          ps -= C::SP;
           pp ^= 1u;
         }
       };
-      if (CPC != 0) {
+      if (CPC != 0 && ua < it.u1) {
         if (!take_packed(false)) {
           ok = false;
           break;
         }
         free_packed();
       }
-      for (int64_t u = it.u0; u < it.u1; ++u) {
+      for (int64_t u = ua; u < it.u1; u += NH) {
         const int64_t v = u * kUnit + s;
-        const int slot = 4 * wu + rg;
-        const bool more = u + 1 < it.u1;
+        const bool more = u + NH < it.u1;
         const bool w_ready = tc::mbar_test(&w_empty[slot], wp);
-        bool p_ready = CPC != 0 && more && tc::mbar_test(&p_full[ps], pp);
-        // The entries are made in registers before the wait for the stage's slot, so a slot is
-        // empty only for the stores.
-        uint32_t o[8][4];  // 16-byte chunks of eight columns
-        if (CPC != 0) {
-          const RowLoad now = r;
-          if (more) r = load_grad_row<CPC>(p, v + kUnit, col);
-          if (work) {
+        const bool p_ready = CPC != 0 && more && tc::mbar_test(&p_full[ps], pp);
+        const RowLoad now = r;
+        if (CPC != 0 && more) r = load_grad_row<CPC>(p, v + NH * kUnit, col);
 #pragma unroll
-            for (int wn = 0; wn < 4; ++wn) {  // window of 32 columns
-              const uint32_t cw = CPC == 1 ? now.code : (CPC == 2 ? (now.code >> (8 * (wn >> 1))) & 0xFFu : (now.code >> (8 * wn)) & 0xFFu);
-              const __half2 c2 = __float2half2_rn((float)cw * now.cs);  // exact for k <= 24
-              const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
+        for (int hh = 0; hh < NH; ++hh) {
+          const int ch = NH == 2 ? hh : grp;  // half of the block's chunks
+          // The entries are made in registers before the wait for the stage's slot, so a slot is
+          // empty only for the stores.
+          uint32_t o[8][4];  // 16-byte chunks of eight columns
+          if (CPC != 0) {
+            if (work) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7
-                const uint32_t word = wn == 0 ? q[c].x : (wn == 1 ? q[c].y : (wn == 2 ? q[c].z : q[c].w));
-                __half2 e[4];
-                dequant_word(word, c2, nc24, e);
+              for (int wn = 0; wn < 4; ++wn) {  // window of 32 columns
+                const uint32_t cw = CPC == 1 ? now.code : (CPC == 2 ? (now.code >> (8 * (wn >> 1))) & 0xFFu : (now.code >> (8 * wn)) & 0xFFu);
+                const __half2 c2 = __float2half2_rn((float)cw * now.cs);  // exact for k <= 24
+                const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[2 * wn + c][j] = h2_bits(e[j]);
+                for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7
+                  const uint4 x = q[2 * hh + c];
+                  const uint32_t word = wn == 0 ? x.x : (wn == 1 ? x.y : (wn == 2 ? x.z : x.w));
+                  __half2 e[4];
+                  dequant_word(word, c2, nc24, e);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) o[2 * wn + c][j] = h2_bits(e[j]);
+                }
               }
             }
+            if (hh == NH - 1 && more && !take_packed(p_ready)) ok = false;
+          } else if (work) {  // INT8 rows straight from global memory
+            const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the half block
+              const uint4 raw = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
+              const uint32_t x[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u, raw.w ^ 0x80808080u};
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                o[2 * c + (j >> 2)][j & 3] = h2_bits(bytes_to_half2(x[j >> 1], (j & 1) ? 0x4342 : 0x4140));
+            }
           }
-          if (more && !take_packed(p_ready)) {
+          if (hh == 0 && !__all_sync(0xffffffffu, w_ready) &&
+              !__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err)))
             ok = false;
-            break;
-          }
-        } else if (work) {  // INT8 rows straight from global memory
-          const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
+          if (!ok) break;
+          const uint32_t dst = w_row + slot * kWStage;
+          // where the chunk of columns 32 wn + 16 ch + 8 c lies in its 128-byte row (wn even, c = 0)
+          const uint32_t at0 = (uint32_t)((2 * ch) ^ x7) << 4;
+          if (work) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 16 columns: chunks 2c, 2c + 1 of the half block
-            const uint4 raw = v < p.h.V ? ldg_stream(src + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u, raw.w ^ 0x80808080u};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              o[2 * c + (j >> 2)][j & 3] = h2_bits(bytes_to_half2(x[j >> 1], (j & 1) ? 0x4342 : 0x4140));
-          }
-        }
-        if (!__all_sync(0xffffffffu, w_ready) &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err))) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = w_row + slot * kWStage;
-        if (work) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            // SC4: window c / 2, chunk 4 (c / 2 % 2) + 2 ch + c % 2 of its 64-column atom; INT8: the
-            // atom ch, chunk c
-            const uint32_t at = CPC != 0 ? (c >> 2) * 4096 + (at0 ^ (uint32_t)((((c >> 1) & 1) * 4 + (c & 1)) << 4))
-                                         : ch * 4096 + (uint32_t)((c ^ x7) << 4);
-            st_shared16(dst + at, o[c][0], o[c][1], o[c][2], o[c][3]);
+            for (int c = 0; c < 8; ++c) {
+              // SC4: window c / 2, chunk 4 (c / 2 % 2) + 2 ch + c % 2 of its 64-column atom; INT8: the
+              // atom ch, chunk c
+              const uint32_t at = CPC != 0 ? (c >> 2) * 4096 + (at0 ^ (uint32_t)((((c >> 1) & 1) * 4 + (c & 1)) << 4))
+                                           : ch * 4096 + (uint32_t)((c ^ x7) << 4);
+              st_shared16(dst + at, o[c][0], o[c][1], o[c][2], o[c][3]);
+            }
           }
         }
+        if (!ok) break;
         tc::fence_proxy_async_smem();  // the MMA reads the stage through the async proxy
         if (CPC != 0 && more) free_packed();
         else __syncwarp();
         if (lane == 0) tc::mbar_arrive(&w_full[slot]);
-        next_w();
+        wp ^= 1u;
+        copied = false;
       }
     }
-    if (!ok && copied >= 0) tc::mbar_wait(&w_full[copied], copied_par, p.err);  // a copy may be in flight
+    if (!ok && copied) tc::mbar_wait(&w_full[slot], wp, p.err);  // the copy may be in flight
   } else if (warp < kDequantWarps + 4) {
     // ---- epilogue: lane = token; raw sums to scratch ----
     const int e = warp - kDequantWarps;
     const uint32_t lane_off = (uint32_t)(32 * e) << 16;
     for (int64_t i = 0; grad_item<MT>(p, i, it); ++i) {
-      const int set = (int)(i % C::SETS);
-      const int64_t use = i / C::SETS;
-      if (!tc::bar_and(1, 128, mbar_wait_long(&acc_full[set], (uint32_t)use & 1u, p.err))) break;
+      if (!tc::bar_and(1, 128, mbar_wait_long(acc_full, (uint32_t)i & 1u, p.err))) break;
       tc::fence_after_sync();
       const int RR = p.h.r_c + p.h.r_r;
       const int live = it.rank ? (RR + 3) & ~3 : it.cols;  // (rows of scratch end on a multiple of 4)
@@ -666,7 +669,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 #pragma unroll 1
         for (int c0 = 0; c0 < it.cols; c0 += 16) {
           float y[16];
-          tc::tmem_ld16(tbase + (set * MT + m) * 256 + lane_off + c0, y);
+          tc::tmem_ld16(tbase + m * 256 + lane_off + c0, y);
+          if (MT == 1) {  // the odd steps' sums
+            float z[16];
+            tc::tmem_ld16(tbase + 256 + lane_off + c0, z);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) y[q] += z[q];
+          }
           if (mine) {
 #pragma unroll
             for (int q = 0; q < 16; q += 4)
@@ -676,46 +685,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
         }
       }
       tc::fence_before_sync();
-      tc::mbar_arrive(&acc_empty[set]);
+      tc::mbar_arrive(acc_empty);
     }
   } else if (warp == kDequantWarps + 4) {
     // ---- packed producer (one thread) ----
     if (lane == 0 && CPC != 0) {
+      // Each group of dequantisation warps has its own part of the ring (slots g, g + NH, ...),
+      // filled with the units that are its by their place in this CTA's sequence.
+      constexpr int NH = 3 - MT, R = C::SP / NH;
       const int64_t nkb = p.h.D >> 7;
-      int64_t np = 0;
-      int ps = 0;
-      uint32_t ph = 0;
+      int64_t np[NH] = {}, seq = 0;
       bool ok = true;
       for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
-        if (it.rank) continue;
         const uint32_t bytes = (uint32_t)it.cols * 64u;
-        for (int64_t u = it.u0; u < it.u1; ++u) {
-          if (np >= C::SP && !tc::mbar_wait(&p_empty[ps], ph ^ 1u, p.err)) {
-            ok = false;
-            break;
-          }
-          tc::fence_proxy_async_smem();  // the stage was read with generic loads
-          tc::mbar_arrive_expect_tx(&p_full[ps], bytes);
-          tc::bulk_g2s(Ps + ps * kPkStage, p.h.r_nib + ((u * nkb + 2 * it.dt) << 13), bytes, &p_full[ps]);
-          ++np;
-          if (++ps == C::SP) {
-            ps = 0;
-            ph ^= 1u;
+        for (int64_t u = it.u0; ok && !it.rank && u < it.u1; ++u) {
+          const int g = NH == 2 ? (int)((seq + (u - it.u0)) & 1) : 0;
+#pragma unroll
+          for (int k = 0; k < NH; ++k) {
+            if (k != g) continue;
+            const int ps = (int)(np[k] % R) * NH + k;
+            if (np[k] >= R && !tc::mbar_wait(&p_empty[ps], (uint32_t)(np[k] / R - 1) & 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            tc::fence_proxy_async_smem();  // the stage was read with generic loads
+            tc::mbar_arrive_expect_tx(&p_full[ps], bytes);
+            tc::bulk_g2s(Ps + ps * kPkStage, p.h.r_nib + ((u * nkb + 2 * it.dt) << 13), bytes, &p_full[ps]);
+            ++np[k];
           }
         }
+        seq += it.u1 - it.u0;
       }
       if (!ok)
-        for (int64_t q = np < C::SP ? 0 : np - C::SP; q < np; ++q)
-          tc::mbar_wait(&p_full[q % C::SP], (uint32_t)(q / C::SP) & 1u, p.err);
+        for (int k = 0; k < NH; ++k)
+          for (int64_t q = np[k] < R ? 0 : np[k] - R; q < np[k]; ++q)
+            tc::mbar_wait(&p_full[(q % R) * NH + k], (uint32_t)(q / R) & 1u, p.err);
     }
   } else if (warp == kDequantWarps + 5) {
     // ---- image producer (one thread); the image comes from the kernel before this one ----
     if (lane == 0) {
       grid_dependency_wait();
       const int64_t tile_bytes = p.nunits * 2 * C::ISTAGE;
-      int64_t ni = 0;
-      int is = 0;
-      uint32_t ph = 0;
+      // With MT = 2 each accumulator has its own half of the ring (slot 2 j + m), so that an item
+      // with one image tile leaves the other's place as it is.
+      constexpr int R = C::SI / MT;
+      int64_t ni[MT] = {};
       bool ok = true;
       for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
         const char* src = p.img + (int64_t)it.tt * MT * tile_bytes + 2 * it.u0 * C::ISTAGE;
@@ -723,89 +737,89 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (m >= it.m) break;
-            if (ni >= C::SI && !tc::mbar_wait(&i_empty[is], ph ^ 1u, p.err)) {
+            const int is = (int)(ni[m] % R) * MT + m;
+            if (ni[m] >= R && !tc::mbar_wait(&i_empty[is], (uint32_t)(ni[m] / R - 1) & 1u, p.err)) {
               ok = false;
               break;
             }
             tc::mbar_arrive_expect_tx(&i_full[is], C::ISTAGE);
             tc::bulk_g2s(Is + is * C::ISTAGE, src + m * tile_bytes, C::ISTAGE, &i_full[is]);
-            ++ni;
-            if (++is == C::SI) {
-              is = 0;
-              ph ^= 1u;
-            }
+            ++ni[m];
           }
         }
       }
       if (!ok)
-        for (int64_t q = ni < C::SI ? 0 : ni - C::SI; q < ni; ++q)
-          tc::mbar_wait(&i_full[q % C::SI], (uint32_t)(q / C::SI) & 1u, p.err);
+        for (int m = 0; m < MT; ++m)
+          for (int64_t q = ni[m] < R ? 0 : ni[m] - R; q < ni[m]; ++q)
+            tc::mbar_wait(&i_full[(q % R) * MT + m], (uint32_t)(q / R) & 1u, p.err);
     }
   } else {
-    // ---- MMA issuer: the whole warp, one elected lane issues ----
-    // A step is 64 rows: two W stages and one image stage per accumulator.  Their barriers are
-    // probed together, then one thread issues the whole step.
+    // ---- MMA issuers: two warps, one elected lane of each issues ----
+    // A step is 64 rows: two W stages and one image stage per accumulator.  Its barriers are
+    // probed together, then one thread issues the step.  With MT = 2 issuer iw takes image tile iw
+    // in every step, with MT = 1 the steps kk = iw mod 2.
+    const int iw = warp - (kDequantWarps + 6);
     const uint64_t bdesc0 = desc_mn_sw128(tc::smem_u32(Ws), 4096, 1024);
     const uint64_t adesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Is));
-    int sw = 0, si = 0;
+    constexpr int R = C::SI / 2;  // this issuer's slots of the image ring: 2 j + iw
+    const uint32_t d = tbase + 256 * iw;
+    int sw = MT == 2 ? 0 : 2 * iw, j0 = 0;
     uint32_t pw = 0, pi = 0;
     bool ok = true;
     for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
-      const int set = (int)(i % C::SETS);
-      const int64_t use = i / C::SETS;
-      if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[set], (uint32_t)(use - 1) & 1u, p.err)))
-        break;
+      if (i > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(acc_empty, (uint32_t)(i - 1) & 1u, p.err))) break;
       tc::fence_after_sync();
       const uint32_t idesc = tc::idesc_f16_m128(it.cols) | (1u << 16);  // B is MN-major
-      const uint32_t d = tbase + set * MT * 256;
+      const bool active = MT == 1 || iw < it.m;  // the second issuer of a lone image tile keeps pace
       const int64_t k1 = 2 * (it.u1 - it.u0);
-      for (int64_t kk = 0; kk < k1; ++kk) {
-        const int si1 = si + 1 == C::SI ? 0 : si + 1;
-        const uint32_t pi1 = si + 1 == C::SI ? pi ^ 1u : pi;
-        const bool two = MT == 2 && it.m == 2;
+      for (int64_t kk = MT == 2 ? 0 : iw; kk < k1; kk += 3 - MT) {
+        const int is = 2 * j0 + iw;
         const bool r0 = tc::mbar_try_wait(&w_full[sw], pw), r1 = tc::mbar_try_wait(&w_full[sw + 1], pw);
-        const bool r2 = tc::mbar_try_wait(&i_full[si], pi), r3 = !two || tc::mbar_try_wait(&i_full[si1], pi1);
-        if (!__all_sync(0xffffffffu, r0 && r1 && r2 && r3) &&
+        const bool r2 = !active || tc::mbar_try_wait(&i_full[is], pi);
+        if (!__all_sync(0xffffffffu, r0 && r1 && r2) &&
             !__all_sync(0xffffffffu, tc::mbar_wait(&w_full[sw], pw, p.err) && tc::mbar_wait(&w_full[sw + 1], pw, p.err) &&
-                                         tc::mbar_wait(&i_full[si], pi, p.err) &&
-                                         (!two || tc::mbar_wait(&i_full[si1], pi1, p.err)))) {
+                                         (!active || tc::mbar_wait(&i_full[is], pi, p.err)))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         const uint64_t bd = bdesc0 + (uint64_t)((sw * kWStage) >> 4);
-        const uint64_t ad0 = adesc0 + (uint64_t)((si * C::ISTAGE) >> 4), ad1 = adesc0 + (uint64_t)((si1 * C::ISTAGE) >> 4);
+        const uint64_t ad = adesc0 + (uint64_t)((is * C::ISTAGE) >> 4);
         if (tc::elect_one()) {
+          if (active) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // K steps of 16 rows: 32 bytes of A, two 8-row atoms of B
-            const uint64_t bj = bd + (uint64_t)(((j >> 1) * kWStage + (j & 1) * 2048) >> 4);
-            mma_f16_ss(d, ad0 + ((j * 32) >> 4), bj, idesc, (kk | j) != 0);
-            if (two) mma_f16_ss(d + 256, ad1 + ((j * 32) >> 4), bj, idesc, (kk | j) != 0);
-            if (j == 1) tc::mma_commit(&w_empty[sw]);
+            for (int j = 0; j < 4; ++j) {  // K steps of 16 rows: 32 bytes of A, two 8-row atoms of B
+              mma_f16_ss(d, ad + ((j * 32) >> 4), bd + (uint64_t)(((j >> 1) * kWStage + (j & 1) * 2048) >> 4), idesc,
+                         kk >= 3 - MT || j != 0);
+              if (j == 1) tc::mma_commit(&w_empty[sw]);
+            }
+            tc::mma_commit(&w_empty[sw + 1]);
+            tc::mma_commit(&i_empty[is]);
+          } else {
+            tc::mbar_arrive(&w_empty[sw]);
+            tc::mbar_arrive(&w_empty[sw + 1]);
           }
-          tc::mma_commit(&w_empty[sw + 1]);
-          tc::mma_commit(&i_empty[si]);
-          if (two) tc::mma_commit(&i_empty[si1]);
         }
         __syncwarp();
-        sw += 2;
-        if (sw == C::SW) {
-          sw = 0;
+        sw += MT == 2 ? 2 : 4;
+        if (sw >= C::SW) {
+          sw -= C::SW;
           pw ^= 1u;
         }
-        si = two ? si1 : si;
-        pi = two ? pi1 : pi;
-        if (++si == C::SI) {
-          si = 0;
+        if (active && ++j0 == R) {
+          j0 = 0;
           pi ^= 1u;
         }
       }
-      if (ok && tc::elect_one()) tc::mma_commit(&acc_full[set]);
+      if (ok && tc::elect_one()) {
+        if (active) tc::mma_commit(acc_full);
+        else tc::mbar_arrive(acc_full);
+      }
       __syncwarp();
     }
     if (tc::elect_one()) {
-      tc::mma_commit(mma_done);
-      tc::mbar_wait(mma_done, 0, p.err);  // every MMA issued here has retired
+      tc::mma_commit(&mma_done[iw]);
+      tc::mbar_wait(&mma_done[iw], 0, p.err);  // every MMA issued here has retired
     }
     __syncwarp();
   }
