@@ -235,31 +235,25 @@ def _optional(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-class _Call:
-    """The device and stream of one call: the tensors' device is made current around the C call
-    (the library works on the current device), the stream is the given one or that device's
-    current one, and tensors used on a stream other than that one are recorded on it."""
-
-    __slots__ = ("dev", "stream", "handle", "prev")
-
-    def __init__(self, dev: torch.device, stream):
-        self.dev, self.stream = dev, stream
-        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-    def run(self, name: str, *args, tensors=()):
-        prev = torch.cuda.current_device()
-        if prev != self.dev.index:
-            torch.cuda.set_device(self.dev)
-        try:
-            status = getattr(_lib.lib(), name)(*args, self.handle)
-        finally:
-            if prev != self.dev.index:
-                torch.cuda.set_device(prev)
+def _run(name: str, dev: torch.device, stream, tensors, *args):
+    """One call into the library for tensors on dev: that device is made current around it (the
+    library works on the current device), the stream is the given one or dev's current one, and
+    on a stream other than the current one the tensors are recorded (their memory may not be
+    handed out again before that stream is done with it)."""
+    current = torch.cuda.current_stream(dev).cuda_stream
+    handle = current if stream is None else stream.cuda_stream
+    call = getattr(_lib.lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = call(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, handle)
+    if status:
         _lib.check(status, name)
-        if self.stream is not None and self.handle != torch.cuda.current_stream(self.dev).cuda_stream:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+    if handle != current:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _head_on(dh: DeviceHead, dev: torch.device):
@@ -285,9 +279,9 @@ def nll_lse(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, stream=None)
     _int_array("targets", targets, (N,), dev)
     out = torch.empty(N, device=dev, dtype=torch.float32)
     lse = torch.empty(N, device=dev, dtype=torch.float32)
-    _Call(dev, stream).run("archead_nll_lse", H.data_ptr(), ctypes.byref(dh.struct),
-                           targets.data_ptr(), out.data_ptr(), lse.data_ptr(), N, *dh.shape_args,
-                           tensors=(H, targets, out, lse))
+    _run("archead_nll_lse", dev, stream, (H, targets, out, lse), H.data_ptr(),
+         ctypes.byref(dh.struct), targets.data_ptr(), out.data_ptr(), lse.data_ptr(), N,
+         *dh.shape_args)
     return out, lse
 
 
@@ -304,10 +298,9 @@ def nll_grad(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, nll: torch.
     _int_array("targets", targets, (N,), dev)
     _float_arrays(N, dev, nll=nll, lse=lse, dnll=dnll)
     out = _grad_out(out, N, dh, dev)
-    _Call(dev, stream).run("archead_nll_grad", H.data_ptr(), ctypes.byref(dh.struct),
-                           targets.data_ptr(), nll.data_ptr(), lse.data_ptr(), dnll.data_ptr(),
-                           out.data_ptr(), N, *dh.shape_args,
-                           tensors=(H, targets, nll, lse, dnll, out))
+    _run("archead_nll_grad", dev, stream, (H, targets, nll, lse, dnll, out), H.data_ptr(),
+         ctypes.byref(dh.struct), targets.data_ptr(), nll.data_ptr(), lse.data_ptr(),
+         dnll.data_ptr(), out.data_ptr(), N, *dh.shape_args)
     return out
 
 
@@ -321,8 +314,8 @@ def logits_grad(dY: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = 
     N, dev = dY.shape[0], dY.device
     _head_on(dh, dev)
     out = _grad_out(out, N, dh, dev)
-    _Call(dev, stream).run("archead_logits_grad", dY.data_ptr(), ctypes.byref(dh.struct),
-                           out.data_ptr(), N, *dh.shape_args, tensors=(dY, out))
+    _run("archead_logits_grad", dev, stream, (dY, out), dY.data_ptr(), ctypes.byref(dh.struct),
+         out.data_ptr(), N, *dh.shape_args)
     return out
 
 
@@ -362,12 +355,11 @@ def policy_loss(nll: torch.Tensor, nll_old: torch.Tensor, advantages: torch.Tens
     _float_arrays(B if per_sequence else N, dev, advantages=advantages)
     dnll = torch.empty(N, device=dev, dtype=torch.float32)
     stats = torch.empty(4, device=dev, dtype=torch.float32)
-    _Call(dev, stream).run(
-        "archead_policy_loss", nll.data_ptr(), nll_old.data_ptr(), _optional(nll_ref),
-        advantages.data_ptr(), _optional(weights), _optional(cu_seqlens), dnll.data_ptr(),
-        stats.data_ptr(), N, B, int(per_sequence), clip_low, clip_high, kl_coef,
-        REDUCTIONS[reduction],
-        tensors=(nll, nll_old, nll_ref, advantages, weights, cu_seqlens, dnll, stats))
+    _run("archead_policy_loss", dev, stream,
+         (nll, nll_old, nll_ref, advantages, weights, cu_seqlens, dnll, stats),
+         nll.data_ptr(), nll_old.data_ptr(), _optional(nll_ref), advantages.data_ptr(),
+         _optional(weights), _optional(cu_seqlens), dnll.data_ptr(), stats.data_ptr(), N, B,
+         per_sequence, clip_low, clip_high, kl_coef, REDUCTIONS[reduction])
     return {"stats": stats, "dnll": dnll}
 
 
@@ -395,12 +387,11 @@ def preference_loss(nll: torch.Tensor, cu_seqlens: torch.Tensor, pairs: torch.Te
     loss = torch.empty(1, device=dev, dtype=torch.float32)
     pair_loss = torch.empty(P, device=dev, dtype=torch.float32)
     rewards = torch.empty(P, 2, device=dev, dtype=torch.float32)
-    _Call(dev, stream).run(
-        "archead_preference_loss", nll.data_ptr(), _optional(nll_ref), _optional(weights),
-        cu_seqlens.data_ptr(), pairs.data_ptr(), dnll.data_ptr(), loss.data_ptr(),
-        pair_loss.data_ptr(), rewards.data_ptr(), N, B, P, PREFERENCES[kind], int(average), beta,
-        label_smoothing, margin,
-        tensors=(nll, nll_ref, weights, cu_seqlens, pairs, dnll, loss, pair_loss, rewards))
+    _run("archead_preference_loss", dev, stream,
+         (nll, nll_ref, weights, cu_seqlens, pairs, dnll, loss, pair_loss, rewards),
+         nll.data_ptr(), _optional(nll_ref), _optional(weights), cu_seqlens.data_ptr(),
+         pairs.data_ptr(), dnll.data_ptr(), loss.data_ptr(), pair_loss.data_ptr(),
+         rewards.data_ptr(), N, B, P, PREFERENCES[kind], average, beta, label_smoothing, margin)
     return {"loss": loss, "pair_loss": pair_loss, "rewards": rewards, "dnll": dnll}
 
 

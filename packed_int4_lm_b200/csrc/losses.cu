@@ -2,12 +2,15 @@
 // archead_preference_loss; formulas in archead.h).
 //
 // Both are a pass over a few floats per token plus sums over ragged sequences, so device
-// memory bounds them when the batch is large and launches when it is small.  Two forms:
-//  * small batches (kSmallTokens, kSmallSeqs): one block does everything in one launch, with
-//    the sequences' sums in shared memory;
-//  * others: the tokens are cut into fixed pieces of 256, one warp each.  A sequence inside a
-//    piece is summed by its warp; one that crosses pieces leaves one partial sum per piece
-//    (`tail` where it starts, `head` in each later piece), which its readers add in order.
+// memory bounds them when the batch is large and launches when it is small.  The tokens are cut
+// into pieces of 256, one warp each: a lane holds eight of them in registers, all loads in
+// flight, and the warp walks the sequences that lie in its pieces (adjacent ones, so that the
+// first sequence is searched for once, 32 probes a step).  A sequence inside a piece is summed by its warp;
+// one that crosses pieces leaves one partial sum per piece (`tail` where it starts, `head` in
+// each later piece), which its readers add in order.  The steps are device functions:
+//  * batches of at most 32 pieces run them in one block, in one launch, with the sequences'
+//    sums in shared memory (%SMALL%);
+//  * others in a chain of launches, each waiting for the one before (%LARGE%).
 // Sums are FP64 in an order that the sizes alone fix, so equal calls give equal bits.  A
 // sequence's slope over the pairs that hold it arrives in any order: it is added in fixed
 // point (integer adds commute exactly).
@@ -18,9 +21,11 @@
 namespace archead {
 namespace {
 
-constexpr int kPiece = 256;          // tokens per warp in the sequence sums
-constexpr int kTokBlock = 1024;      // tokens per block step in the token kernels
-constexpr int kMaxBlocks = 148 * 8;  // blocks of the token kernels (256 threads, 8 per SM)
+constexpr int kPiece = 256, kPer = kPiece / 32;  // tokens per warp, per lane
+constexpr int kMaxBlocks = 148 * 4;              // blocks of a launch: what runs at once, so that
+                                                 // a warp's pieces lie side by side
+constexpr int kSmallPieces = 32;                 // one block's warps
+constexpr int kSmallSeqs = 512, kSmallPairs = 1024;  // (30 KB of shared memory)
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
@@ -28,7 +33,7 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Sum over the block in a fixed order; thread 0 gets it.  red: one double per warp.
+// Sum over the block in a fixed order; warp 0 gets it.  red: one double per warp.
 __device__ __forceinline__ double block_sum(double v, double* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   v = warp_sum(v);
@@ -40,126 +45,167 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return v;
 }
 
-// Offset i of the sequences, taken into [0, N].
-__device__ __forceinline__ int64_t seq_at(const int32_t* cu, int64_t i, int64_t N) {
-  const int64_t c = __ldg(cu + i);
-  return c < 0 ? 0 : (c > N ? N : c);
+// ---- sequences --------------------------------------------------------------------------
+struct Seqs {
+  const int32_t* cu;  // B + 1 offsets, or nullptr: one sequence of all tokens
+  int N, B;
+};
+
+// Offset i, taken into [0, N].
+__device__ __forceinline__ int seq_at(const Seqs& q, int i) {
+  const int c = __ldg(q.cu + i);
+  return c < 0 ? 0 : (c > q.N ? q.N : c);
+}
+__device__ __forceinline__ bool seq_bad(const Seqs& q, int i) {
+  const int a = __ldg(q.cu + i), b = __ldg(q.cu + i + 1);
+  return a < 0 || b < a || b > q.N;
+}
+// Reports offsets that fall or leave [0, N], shared out over `size` threads.
+__device__ __forceinline__ void check_seqs(const Seqs& q, int64_t tid, int64_t size, unsigned* err) {
+  if (!q.cu) return;
+  bool bad = q.B == 0 && tid == 0 && (__ldg(q.cu) < 0 || __ldg(q.cu) > q.N);
+  for (int64_t i = tid; i < q.B; i += size) bad |= seq_bad(q, (int)i);
+  if (bad) atomicOr(err, kErrSegment);
 }
 
-// The sequence among [lo, hi) that holds token t (empty ones hold none), or -1.
-__device__ __forceinline__ int64_t seq_of(const int32_t* cu, int64_t lo, int64_t hi, int64_t N,
-                                          int64_t t) {
-  // largest i in [lo, hi) with cu[i] <= t
-  if (hi <= lo || seq_at(cu, lo, N) > t) return -1;
-  int64_t a = lo, b = hi;  // cu[a] <= t, cu[b] > t or b == hi
-  while (b - a > 1) {
-    const int64_t m = (a + b) >> 1;
-    if (seq_at(cu, m, N) <= t) a = m;
-    else b = m;
+// The last sequence that begins at or before token t, by a whole warp; -1 if none does.  (Where
+// the offsets are out of order it is some index in range.)
+__device__ __forceinline__ int warp_seq_of(const Seqs& q, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = q.B;  // of lo .. lo + n - 1 the first few begin at or before t
+  while (n > 32) {
+    const int step = (n + 31) >> 5;
+    const int i = (lane + 1) * step - 1;
+    const bool in = i < n && seq_at(q, lo + i) <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, in)) * step;
+    lo += c;
+    n = n - c < step ? n - c : step;
   }
-  return t < seq_at(cu, a + 1, N) ? a : -1;
+  const bool in = lane < n && seq_at(q, lo + lane) <= t;
+  return lo + __popc(__ballot_sync(0xffffffffu, in)) - 1;
 }
 
-__device__ __forceinline__ bool seq_bad(const int32_t* cu, int64_t i, int64_t N) {
-  const int64_t a = __ldg(cu + i), b = __ldg(cu + i + 1);
-  return a < 0 || b < a || b > N;
-}
+// Walks the sequences along adjacent pieces, one warp: window(i) lets each lane load what belongs
+// to sequence i (32 sequences at a time), and piece(t0, t1, f) calls f(j, s, lo, hi, b0, b1) with
+// the whole warp for the tokens [lo, hi) of sequence s = [b0, b1), whose window data lane j holds.
+template <typename W>
+struct Walker {
+  const Seqs q;
+  W window;
+  int s = 0, j = 0, b0 = 0, end = 0;  // the window's first sequence, the current one in it, its start
 
-// ---- sequence sums ----------------------------------------------------------------------
-// Per token a weight and a value; per sequence their sums.
+  __device__ __forceinline__ void load() {
+    const int i = s + (threadIdx.x & 31);
+    if (i < q.B) {
+      end = seq_at(q, i + 1);
+      window(i);
+    }
+  }
+  __device__ __forceinline__ Walker(const Seqs& seqs, int t0, W w) : q(seqs), window(w) {
+    if (q.B == 0) return;
+    s = warp_seq_of(q, t0);
+    if (s < 0) s = 0;
+    b0 = seq_at(q, s);
+    load();
+  }
+  template <typename F>
+  __device__ __forceinline__ void piece(int t0, int t1, F f) {
+    int pos = t0 < b0 ? b0 : t0;  // (tokens before the first sequence)
+    while (pos < t1 && s + j < q.B) {
+      const int b1 = __shfl_sync(0xffffffffu, end, j);
+      const int hi = b1 < t1 ? b1 : t1;
+      if (hi > pos) {
+        f(j, s + j, pos, hi, b0, b1);
+        pos = hi;
+      }
+      if (b1 > t1) break;  // goes on in the next piece
+      b0 = b1;
+      if (++j == 32) {
+        s += 32;
+        j = 0;
+        load();
+      }
+    }
+  }
+};
+
+// Per sequence the sums of a weight and a value.
 struct Pair2 {
   double w, x;
 };
-
 struct SeqSums {
   Pair2* whole;  // B: sequences inside one piece
   Pair2* head;   // per piece: the sequence that began before it
   Pair2* tail;   // per piece: the sequence that begins in it and goes on
 };
 
-// x = w (nll_ref - nll) with nll given (preference scores); nll == nullptr: weights alone.
-__device__ __forceinline__ Pair2 token_pair(const float* nll, const float* ref, const float* w,
-                                            int64_t t) {
-  Pair2 p;
-  p.w = w ? (double)__ldg(w + t) : 1.0;
-  p.x = 0.0;
-  if (nll && p.w != 0.0)
-    p.x = p.w * ((ref ? (double)__ldg(ref + t) : 0.0) - (double)__ldg(nll + t));
-  return p;
-}
-
-__global__ void __launch_bounds__(256) seq_sums_kernel(const float* __restrict__ nll,
-                                                       const float* __restrict__ ref,
-                                                       const float* __restrict__ w,
-                                                       const int32_t* __restrict__ cu, int64_t N,
-                                                       int64_t B, SeqSums out,
-                                                       unsigned long long* zero, int64_t nzero,
-                                                       unsigned* err) {
-  allow_dependent_launch();
+// The share of pieces [c, c1): x = w (ref - nll) (kValue), or the weights alone.  A token of
+// weight 0 adds nothing, whatever it holds.
+template <bool kValue>
+__device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, const float* ref,
+                                            const float* w, int c, int c1, const SeqSums& out) {
   const int lane = threadIdx.x & 31;
-  const int64_t gtid = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int64_t gsize = (int64_t)gridDim.x * blockDim.x;
-  bool bad = false;
-  for (int64_t i = gtid; i < B; i += gsize) bad |= seq_bad(cu, i, N);
-  if (bad) atomicOr(err, kErrSegment);
-  for (int64_t i = gtid; i < nzero; i += gsize) zero[i] = 0ull;
-  const int64_t c = gtid >> 5;  // this warp's piece
-  const int64_t t0 = c * kPiece;
-  if (t0 >= N) return;
-  const int64_t t1 = t0 + kPiece < N ? t0 + kPiece : N;
-  Pair2 v[kPiece / 32];
+  if (c >= c1) return;
+  auto none = [](int) {};
+  Walker<decltype(none)> walk(q, c * kPiece, none);
+  for (; c < c1; ++c) {
+    const int t0 = c * kPiece, t1 = q.N - t0 < kPiece ? q.N : t0 + kPiece;
+    float wf[kPer], a[kPer], b[kPer];
 #pragma unroll
-  for (int k = 0; k < kPiece / 32; ++k) {
-    const int64_t t = t0 + 32 * k + lane;
-    v[k] = t < t1 ? token_pair(nll, ref, w, t) : Pair2{0.0, 0.0};
-  }
-  int64_t pos = t0;
-  const int64_t first = seq_at(cu, 0, N);
-  if (pos < first) pos = first;  // tokens before the first sequence
-  int64_t s = -1;
-  while (pos < t1) {
-    // the next sequence is usually the one after; empty ones are skipped by a search
-    int64_t n = s >= 0 && s + 1 < B ? s + 1 : -1;
-    if (n >= 0 && !(seq_at(cu, n, N) <= pos && pos < seq_at(cu, n + 1, N))) n = -1;
-    s = n >= 0 ? n : seq_of(cu, 0, B, N, pos);
-    if (s < 0) break;  // behind the last sequence
-    const int64_t b0 = seq_at(cu, s, N), b1 = seq_at(cu, s + 1, N);
-    const int64_t hi = b1 < t1 ? b1 : t1;
-    Pair2 a = {0.0, 0.0};
+    for (int k = 0; k < kPer; ++k) {
+      const int t = t0 + 32 * k + lane;
+      const bool in = t < t1;
+      wf[k] = in ? (w ? __ldg(w + t) : 1.f) : 0.f;
+      a[k] = kValue && in ? __ldg(nll + t) : 0.f;
+      b[k] = kValue && in && ref ? __ldg(ref + t) : 0.f;
+    }
+    double x[kPer];
 #pragma unroll
-    for (int k = 0; k < kPiece / 32; ++k) {
-      const int64_t t = t0 + 32 * k + lane;
-      if (t >= pos && t < hi) {
-        a.w += v[k].w;
-        a.x += v[k].x;
+    for (int k = 0; k < kPer; ++k)
+      x[k] = kValue && wf[k] != 0.f ? (double)wf[k] * ((double)b[k] - (double)a[k]) : 0.0;
+    walk.piece(t0, t1, [&](int, int s, int lo, int hi, int b0, int b1) {
+      Pair2 sum = {0.0, 0.0};
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int t = t0 + 32 * k + lane;
+        if (t >= lo && t < hi) {
+          sum.w += (double)wf[k];
+          sum.x += x[k];
+        }
       }
-    }
-    a.w = warp_sum(a.w);
-    if (nll) a.x = warp_sum(a.x);
-    if (lane == 0) {
-      Pair2* dst = b0 < t0 ? out.head + c : (b1 > t1 ? out.tail + c : out.whole + s);
-      *dst = a;
-    }
-    pos = hi;
+      sum.w = warp_sum(sum.w);
+      if (kValue) sum.x = warp_sum(sum.x);
+      if (lane == 0) *(b0 < t0 ? out.head + c : (b1 > t1 ? out.tail + c : out.whole + s)) = sum;
+    });
   }
 }
 
-// The sums of sequence s, by a whole warp (every lane gets them).
-__device__ __forceinline__ Pair2 seq_total(const SeqSums& q, const int32_t* cu, int64_t s,
-                                           int64_t N) {
-  const int64_t b0 = seq_at(cu, s, N), b1 = seq_at(cu, s + 1, N);
-  if (b1 <= b0) return {0.0, 0.0};
-  const int64_t c0 = b0 / kPiece, c1 = (b1 - 1) / kPiece;
-  if (c0 == c1) return q.whole[s];
+// The pieces of this warp when all warps of the grid share `n` pieces out in order.
+__device__ __forceinline__ void my_pieces(int n, int* c0, int* c1) {
+  const int64_t w = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t all = gridDim.x * (int64_t)(blockDim.x >> 5);
+  *c0 = (int)(n * w / all);
+  *c1 = (int)(n * (w + 1) / all);
+}
+__device__ __forceinline__ int pieces_of(int64_t N) { return (int)((N + kPiece - 1) / kPiece); }
+
+// The sums of sequence s, added by `width` adjacent lanes (a power of two; `lane` counts in
+// them; all 32 lanes of the warp take part).
+__device__ __forceinline__ Pair2 seq_total(const SeqSums& q, const Seqs& sq, int s, int lane, int width) {
+  const int b0 = seq_at(sq, s), b1 = seq_at(sq, s + 1);
+  const int c0 = b0 / kPiece, c1 = b1 > b0 ? (b1 - 1) / kPiece : c0;
   Pair2 a = {0.0, 0.0};
-  for (int64_t c = c0 + 1 + (threadIdx.x & 31); c <= c1; c += 32) {
+  for (int c = c0 + 1 + lane; c <= c1; c += width) {
     const Pair2 h = q.head[c];
     a.w += h.w;
     a.x += h.x;
   }
-  a.w = warp_sum(a.w);
-  a.x = warp_sum(a.x);
-  const Pair2 t = q.tail[c0];
+  for (int o = width >> 1; o > 0; o >>= 1) {
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+  }
+  if (b1 <= b0) return {0.0, 0.0};
+  const Pair2 t = c0 == c1 ? q.whole[s] : q.tail[c0];
   return {t.w + a.w, t.x + a.x};
 }
 
@@ -171,7 +217,8 @@ struct PolicyConst {
 };
 
 struct PolicyTok {
-  double sur, kl, clipped, grad;
+  float sur, kl, grad;
+  bool clipped;
 };
 
 // exp(z) - 1 - z: its Taylor series near 0, where the difference cancels (the first term left
@@ -187,205 +234,273 @@ __device__ __forceinline__ float kl_term(float z, float em1) {
   return 0.5f * z * z * p;
 }
 
-// One token: r = exp(x), x = nll_old - nll.  Which side of the clip border it lies on is
-// decided by the exact difference of the two FP32 values against log(1 +- clip) in FP64.
+// Whether old - nll > limit exactly: rounding is monotone, so only where the rounded difference
+// equals the rounded limit does the FP64 difference (exact) decide.
+__device__ __forceinline__ bool beyond(float x, float old, float nll, double limit, bool above) {
+  const float l = (float)limit;
+  if (x != l) return above ? x > l : x < l;
+  const double d = (double)old - (double)nll;
+  return above ? d > limit : d < limit;
+}
+
 __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A, bool has_ref,
                                                   float ref, const PolicyConst& k) {
-  const double x = (double)old - (double)nll;
-  PolicyTok o = {0.0, 0.0, 0.0, 0.0};
+  const float x = old - nll;
+  PolicyTok o = {0.f, 0.f, 0.f, false};
   if (A != 0.f) {  // (0 times an infinite ratio is 0 here)
-    if ((A > 0.f && x > k.log_hi) || (A < 0.f && x < k.log_lo)) {
-      o.sur = -(A > 0.f ? k.hi : k.lo) * (double)A;
-      o.clipped = 1.0;
+    o.clipped = beyond(x, old, nll, A > 0.f ? k.log_hi : k.log_lo, A > 0.f);
+    if (o.clipped) {
+      o.sur = -(float)(A > 0.f ? k.hi : k.lo) * A;
     } else {
-      o.grad = (double)(expf((float)x) * A);
+      o.grad = expf(x) * A;
       o.sur = -o.grad;
     }
   }
   if (has_ref) {
     const float z = nll - ref, em1 = expm1f(z);
-    o.kl = (double)kl_term(z, em1);
-    o.grad += k.kl_coef * (double)em1;
+    o.kl = kl_term(z, em1);
+    o.grad = fmaf((float)k.kl_coef, em1, o.grad);
   }
   return o;
 }
 
-// Per-sequence scale 1 / sum w (0 for a sequence without weight) and how many sequences
-// have weight, one warp per sequence.  Without weights the sum is the length.
-__global__ void __launch_bounds__(256) policy_seq_kernel(SeqSums q, const float* w,
-                                                         const int32_t* __restrict__ cu,
-                                                         int64_t N, int64_t B,
-                                                         double* __restrict__ inv,
-                                                         unsigned* __restrict__ active,
-                                                         unsigned* err) {
+// Sums of the loss's parts.
+struct PolicySums {
+  double sur, kl, clipped;
+};
+
+__device__ __forceinline__ Seqs seqs_of(const PolicyArgs& a) { return {a.cu, (int)a.N, (int)a.B}; }
+
+// The tokens of pieces [c, c1): gradients, and the pieces' parts added to `sum` (per lane).  scale
+// is the common factor (1 / sum w, 1 / sequences with weight, or 1); inv the sequences' 1 / sum w.
+__device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyConst& k, int c, int c1,
+                                              double scale, const double* inv, PolicySums& sum) {
+  const Seqs q = seqs_of(a);
+  const int lane = threadIdx.x & 31;
+  if (c >= c1) return;
+  const bool by_seq = a.reduction == ARCHEAD_REDUCE_SEQUENCE, walks = by_seq || a.adv_per_seq;
+  const int first = !q.cu ? 0 : (q.B > 0 ? seq_at(q, 0) : q.N), last = q.cu ? seq_at(q, q.B) : q.N;
+  float sc = 0.f, adv = 0.f;  // of the window's sequence
+  auto window = [&](int s) {
+    sc = (float)(by_seq ? inv[s] * scale : scale);
+    if (a.adv_per_seq) adv = __ldg(a.adv + s);
+  };
+  Walker<decltype(window)> walk(walks ? q : Seqs{nullptr, 0, 0}, c * kPiece, window);
+  for (; c < c1; ++c) {
+    const int t0 = c * kPiece, t1 = q.N - t0 < kPiece ? q.N : t0 + kPiece;
+    float nll[kPer], old[kPer], ref[kPer], A[kPer], f[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + 32 * i + lane;
+      const bool in = t < t1;
+      nll[i] = in ? __ldg(a.nll + t) : 0.f;
+      old[i] = in ? __ldg(a.nll_old + t) : 0.f;
+      ref[i] = in && a.nll_ref ? __ldg(a.nll_ref + t) : 0.f;
+      A[i] = in && !a.adv_per_seq ? __ldg(a.adv + t) : 0.f;
+      f[i] = in ? (a.w ? __ldg(a.w + t) : 1.f) : 0.f;
+    }
+    if (walks) {
+      float g[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) g[i] = 0.f;  // outside every sequence
+      walk.piece(t0, t1, [&](int j, int, int lo, int hi, int, int) {
+        const float fs = __shfl_sync(0xffffffffu, sc, j), as = __shfl_sync(0xffffffffu, adv, j);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int t = t0 + 32 * i + lane;
+          if (t >= lo && t < hi) {
+            g[i] = fs;
+            if (a.adv_per_seq) A[i] = as;
+          }
+        }
+      });
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[i] *= g[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t0 + 32 * i + lane;
+        f[i] = t >= first && t < last ? f[i] * (float)scale : 0.f;
+      }
+    }
+    float sur = 0.f, kl = 0.f, clipped = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + 32 * i + lane;
+      float g = 0.f;
+      if (f[i] != 0.f) {
+        const PolicyTok o = policy_token(nll[i], old[i], A[i], a.nll_ref != nullptr, ref[i], k);
+        sur = fmaf(f[i], o.sur, sur);
+        kl = fmaf(f[i], o.kl, kl);
+        if (o.clipped) clipped += f[i];
+        g = f[i] * o.grad;
+      }
+      if (t < t1) __stcs(a.dnll + t, g);
+    }
+    sum.sur += (double)sur;
+    sum.kl += (double)kl;
+    sum.clipped += (double)clipped;
+  }
+}
+
+__device__ __forceinline__ void policy_stats(float* stats, const PolicySums& s, double kl_coef) {
+  stats[0] = (float)(kl_coef != 0.0 ? s.sur + kl_coef * s.kl : s.sur);
+  stats[1] = (float)s.sur;
+  stats[2] = (float)s.kl;
+  stats[3] = (float)s.clipped;
+}
+
+// Weight of the tokens inside sequences (of all without offsets), this thread's share.
+__device__ __forceinline__ double weight_share(const PolicyArgs& a, int64_t tid, int64_t size) {
+  const Seqs q = seqs_of(a);
+  const int lo = !q.cu ? 0 : (q.B > 0 ? seq_at(q, 0) : q.N), hi = q.cu ? seq_at(q, q.B) : q.N;
+  if (!a.w) return tid == 0 && hi > lo ? (double)(hi - lo) : 0.0;
+  double s = 0.0;
+#pragma unroll 4
+  for (int64_t t = lo + tid; t < hi; t += size) s += (double)__ldg(a.w + t);
+  return s;
+}
+
+// 1 / sum w of sequence s (0 without weight), by a group of lanes; without weights the sum is the
+// length.
+__device__ __forceinline__ double policy_seq_inv(const PolicyArgs& a, const SeqSums& q, int s, int lane, int width) {
+  const Seqs sq = seqs_of(a);
+  const double t = a.w ? seq_total(q, sq, s, lane, width).w : (double)(seq_at(sq, s + 1) - seq_at(sq, s));
+  return t > 0.0 ? 1.0 / t : 0.0;
+}
+
+template <bool kValue>
+__global__ void __launch_bounds__(256, kValue ? 4 : 5) seq_sums_kernel(const float* __restrict__ nll,
+                                                       const float* __restrict__ ref,
+                                                       const float* __restrict__ w, Seqs q,
+                                                       SeqSums out, unsigned long long* zero,
+                                                       int64_t nzero, unsigned* err) {
+  allow_dependent_launch();
+  const int64_t tid = blockIdx.x * 256ll + threadIdx.x, size = gridDim.x * 256ll;
+  int c0, c1;
+  my_pieces(pieces_of(q.N), &c0, &c1);
+  sums_pieces<kValue>(q, nll, ref, w, c0, c1, out);
+  check_seqs(q, tid, size, err);
+  for (int64_t i = tid; i < nzero; i += size) zero[i] = 0ull;
+}
+
+// Eight lanes per sequence.
+__global__ void __launch_bounds__(256) policy_seq_kernel(PolicyArgs a, SeqSums q, double* __restrict__ inv,
+                                                         double* __restrict__ active, unsigned* err) {
   allow_dependent_launch();
   grid_dependency_wait();
-  __shared__ unsigned cnt[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned n = 0;
-  bool bad = false;
-  for (int64_t s = blockIdx.x * 8ll + warp; s < B; s += gridDim.x * 8ll) {
-    double t;
-    if (w) {
-      t = seq_total(q, cu, s, N).w;
-    } else {
-      bad |= seq_bad(cu, s, N);
-      const int64_t len = seq_at(cu, s + 1, N) - seq_at(cu, s, N);
-      t = len > 0 ? (double)len : 0.0;
+  __shared__ double red[8];
+  double n = 0.0;
+  for (int64_t s0 = blockIdx.x * 32ll; s0 < a.B; s0 += gridDim.x * 32ll) {
+    const int64_t s = s0 + (threadIdx.x >> 3);
+    const double v = policy_seq_inv(a, q, (int)(s < a.B ? s : a.B - 1), threadIdx.x & 7, 8);
+    if (s < a.B && (threadIdx.x & 7) == 0) {
+      inv[s] = v;
+      n += v > 0.0;
     }
-    if (lane == 0) inv[s] = t > 0.0 ? 1.0 / t : 0.0;
-    n += t > 0.0;
   }
-  if (bad) atomicOr(err, kErrSegment);
-  if (lane == 0) cnt[warp] = n;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned a = 0;
-    for (int i = 0; i < 8; ++i) a += cnt[i];
-    active[blockIdx.x] = a;
-  }
+  if (!a.w) check_seqs(seqs_of(a), blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll, err);
+  n = block_sum(n, red);
+  if (threadIdx.x == 0) active[blockIdx.x] = n;
 }
 
-// Sum of the weights of the tokens inside sequences (of all tokens without cu): per block.
-__global__ void __launch_bounds__(256) policy_weight_kernel(const float* __restrict__ w,
-                                                            const int32_t* __restrict__ cu,
-                                                            int64_t N, int64_t B,
-                                                            double* __restrict__ part,
-                                                            unsigned* err) {
+__global__ void __launch_bounds__(256) policy_weight_kernel(PolicyArgs a, double* __restrict__ part, unsigned* err) {
   allow_dependent_launch();
   __shared__ double red[8];
-  const int64_t gtid = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int64_t gsize = (int64_t)gridDim.x * blockDim.x;
-  int64_t lo = 0, hi = N;
-  if (cu) {
-    bool bad = false;
-    for (int64_t i = gtid; i < B; i += gsize) bad |= seq_bad(cu, i, N);
-    if (bad) atomicOr(err, kErrSegment);
-    lo = B > 0 ? seq_at(cu, 0, N) : N;
-    hi = seq_at(cu, B, N);
-  }
-  double a = 0.0;
-  if (w)
-    for (int64_t t = lo + gtid; t < hi; t += gsize) a += (double)__ldg(w + t);
-  else if (gtid == 0 && hi > lo)
-    a = (double)(hi - lo);
-  a = block_sum(a, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = a;
+  const int64_t tid = blockIdx.x * 256ll + threadIdx.x, size = gridDim.x * 256ll;
+  const double s = block_sum(weight_share(a, tid, size), red);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  check_seqs(seqs_of(a), tid, size, err);
 }
 
-// The tokens: gradient, and the block's sums of surrogate, KL term and clipped weight.
-__global__ void __launch_bounds__(256) policy_token_kernel(
-    PolicyArgs a, PolicyConst k, const double* __restrict__ inv, const unsigned* active,
-    int nactive, const double* wpart, int nwpart, double* __restrict__ part, unsigned* err) {
+// total: partial sums (n of them) of what the common factor divides by; nullptr: the factor is 1.
+__global__ void __launch_bounds__(256, 4) policy_token_kernel(PolicyArgs a, PolicyConst k, const double* inv,
+                                                           const double* total, int n, PolicySums* part,
+                                                           unsigned* err) {
   allow_dependent_launch();
   grid_dependency_wait();
   __shared__ double red[8];
   __shared__ double scale_s;
-  __shared__ int64_t seq_lo, seq_hi;
-  // the common factor: 1 / sum w, 1 / (sequences with weight), or 1
-  double t = 0.0;
-  if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
-    for (int i = threadIdx.x; i < nwpart; i += 256) t += wpart[i];
-  } else if (a.reduction == ARCHEAD_REDUCE_SEQUENCE) {
-    for (int i = threadIdx.x; i < nactive; i += 256) t += (double)active[i];
-  } else if (threadIdx.x == 0) {
-    t = 1.0;
+  if (total) {
+    double t = 0.0;
+    for (int i = threadIdx.x; i < n; i += 256) t += total[i];
+    t = block_sum(t, red);
+    if (threadIdx.x == 0) scale_s = t > 0.0 ? 1.0 / t : 0.0;
+    __syncthreads();
+  } else {
+    check_seqs(seqs_of(a), blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll, err);
+  }
+  const double scale = total ? scale_s : 1.0;
+  PolicySums s = {0.0, 0.0, 0.0};
+  int c0, c1;
+  my_pieces(pieces_of(a.N), &c0, &c1);
+  policy_pieces(a, k, c0, c1, scale, inv, s);
+  s.sur = block_sum(s.sur, red);
+  s.kl = block_sum(s.kl, red);
+  s.clipped = block_sum(s.clipped, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ void __launch_bounds__(256) policy_final_kernel(const PolicySums* __restrict__ part, int n,
+                                                           double kl_coef, float* stats) {
+  grid_dependency_wait();
+  __shared__ double red[8];
+  PolicySums s = {0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += 256) {
+    s.sur += part[i].sur;
+    s.kl += part[i].kl;
+    s.clipped += part[i].clipped;
+  }
+  s.sur = block_sum(s.sur, red);
+  s.kl = block_sum(s.kl, red);
+  s.clipped = block_sum(s.clipped, red);
+  if (threadIdx.x == 0) policy_stats(stats, s, kl_coef);
+}
+
+// Everything in one block: at most kSmallPieces pieces and kSmallSeqs sequences.
+__global__ void __launch_bounds__(1024) policy_small_kernel(PolicyArgs a, PolicyConst k, unsigned* err) {
+  __shared__ double red[32], inv[kSmallSeqs], scale_s;
+  __shared__ Pair2 whole[kSmallSeqs], head[kSmallPieces], tail[kSmallPieces];
+  grid_dependency_wait();
+  const Seqs q = seqs_of(a);
+  const SeqSums sums = {whole, head, tail};
+  const int warp = threadIdx.x >> 5;
+  const bool mine = warp * kPiece < q.N;
+  double t = threadIdx.x == 0 ? 1.0 : 0.0;
+  if (a.reduction == ARCHEAD_REDUCE_SEQUENCE) {
+    if (a.w && mine) sums_pieces<false>(q, nullptr, nullptr, a.w, warp, warp + 1, sums);
+    __syncthreads();
+    t = 0.0;
+    for (int s0 = 0; s0 < q.B; s0 += 128) {
+      const int s = s0 + (threadIdx.x >> 3);
+      const double v = policy_seq_inv(a, sums, s < q.B ? s : q.B - 1, threadIdx.x & 7, 8);
+      if (s < q.B && (threadIdx.x & 7) == 0) {
+        inv[s] = v;
+        t += v > 0.0;
+      }
+    }
+  } else if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
+    t = weight_share(a, threadIdx.x, 1024);
   }
   t = block_sum(t, red);
   if (threadIdx.x == 0) scale_s = t > 0.0 ? 1.0 / t : 0.0;
   __syncthreads();
-  const double scale = scale_s;
-  if (a.cu && a.reduction == ARCHEAD_REDUCE_SUM) {  // nothing before this kernel looked
-    bool bad = false;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < a.B; i += gridDim.x * 256ll)
-      bad |= seq_bad(a.cu, i, a.N);
-    if (bad) atomicOr(err, kErrSegment);
-  }
-  double sur = 0.0, kl = 0.0, clipped = 0.0;
-  const bool need_seq = a.adv_per_seq || a.reduction == ARCHEAD_REDUCE_SEQUENCE;
-  const int64_t first = a.cu ? (a.B > 0 ? seq_at(a.cu, 0, a.N) : a.N) : 0;
-  const int64_t last = a.cu ? seq_at(a.cu, a.B, a.N) : a.N;
-  for (int64_t c0 = (int64_t)blockIdx.x * kTokBlock; c0 < a.N; c0 += (int64_t)gridDim.x * kTokBlock) {
-    if (need_seq) {  // the sequences that this step's tokens can lie in
-      __syncthreads();
-      if (threadIdx.x < 2) {
-        int64_t x = threadIdx.x ? c0 + kTokBlock - 1 : c0;
-        if (x >= last) x = last - 1;
-        if (x < first) x = first;
-        const int64_t s = last > first ? seq_of(a.cu, 0, a.B, a.N, x) : -1;
-        if (threadIdx.x) seq_hi = s < 0 ? a.B : s + 1;
-        else seq_lo = s < 0 ? 0 : s;
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < kTokBlock / 256; ++j) {
-      const int64_t n = c0 + 256 * j + threadIdx.x;
-      if (n >= a.N) break;
-      double w = n >= first && n < last ? (a.w ? (double)__ldg(a.w + n) : 1.0) : 0.0;
-      int64_t s = 0;
-      if (need_seq && w != 0.0) {
-        s = seq_of(a.cu, seq_lo, seq_hi, a.N, n);
-        if (s < 0) w = 0.0;  // only where the offsets are out of order
-      }
-      float g = 0.f;
-      if (w != 0.0) {
-        const float A = __ldg(a.adv + (a.adv_per_seq ? s : n));
-        const PolicyTok o = policy_token(__ldg(a.nll + n), __ldg(a.nll_old + n), A,
-                                         a.nll_ref != nullptr,
-                                         a.nll_ref ? __ldg(a.nll_ref + n) : 0.f, k);
-        w *= scale;
-        if (a.reduction == ARCHEAD_REDUCE_SEQUENCE) w *= inv[s];
-        sur += w * o.sur;
-        kl += w * o.kl;
-        clipped += w * o.clipped;
-        g = (float)(w * o.grad);
-      }
-      a.dnll[n] = g;
-    }
-  }
-  const double s0 = block_sum(sur, red), s1 = block_sum(kl, red), s2 = block_sum(clipped, red);
-  if (threadIdx.x == 0) {
-    part[3 * blockIdx.x] = s0;
-    part[3 * blockIdx.x + 1] = s1;
-    part[3 * blockIdx.x + 2] = s2;
-  }
-}
-
-__device__ __forceinline__ void policy_stats(float* stats, double sur, double kl,
-                                             double clipped, double kl_coef) {
-  stats[0] = (float)(kl_coef != 0.0 ? sur + kl_coef * kl : sur);
-  stats[1] = (float)sur;
-  stats[2] = (float)kl;
-  stats[3] = (float)clipped;
-}
-
-__global__ void __launch_bounds__(256) policy_final_kernel(const double* __restrict__ part, int n,
-                                                           double kl_coef, float* stats) {
-  grid_dependency_wait();
-  __shared__ double red[8];
-  double s[3] = {0.0, 0.0, 0.0};
-  for (int i = threadIdx.x; i < n; i += 256)
-#pragma unroll
-    for (int j = 0; j < 3; ++j) s[j] += part[3 * i + j];
-#pragma unroll
-  for (int j = 0; j < 3; ++j) s[j] = block_sum(s[j], red);
-  if (threadIdx.x == 0) policy_stats(stats, s[0], s[1], s[2], kl_coef);
+  PolicySums s = {0.0, 0.0, 0.0};
+  if (mine) policy_pieces(a, k, warp, warp + 1, scale_s, inv, s);
+  check_seqs(q, threadIdx.x, 1024, err);
+  s.sur = block_sum(s.sur, red);
+  s.kl = block_sum(s.kl, red);
+  s.clipped = block_sum(s.clipped, red);
+  if (threadIdx.x == 0) policy_stats(a.stats, s, k.kl_coef);
 }
 
 PolicyConst policy_const(const PolicyArgs& a) {
   return {log1p(a.clip_high), log1p(-a.clip_low), 1.0 + a.clip_high, 1.0 - a.clip_low, a.kl_coef};
 }
 
-int token_blocks(int64_t N) {
-  int64_t b = (N + kTokBlock - 1) / kTokBlock;
-  return (int)(b < 1 ? 1 : (b > kMaxBlocks ? kMaxBlocks : b));
-}
-int seq_blocks(int64_t B) {
-  int64_t b = (B + 7) / 8;
-  return (int)(b < 1 ? 1 : (b > kMaxBlocks ? kMaxBlocks : b));
-}
 int64_t piece_count(int64_t N) { return (N + kPiece - 1) / kPiece; }
+int capped(int64_t blocks) { return (int)(blocks < 1 ? 1 : (blocks > kMaxBlocks ? kMaxBlocks : blocks)); }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t seq_sum_bytes(int64_t N, int64_t B) {
@@ -399,15 +514,17 @@ SeqSums carve_seq_sums(char* b, int64_t N, int64_t B) {
                                     up256((size_t)piece_count(N) * sizeof(Pair2)));
   return q;
 }
+bool small_tokens(int64_t N, int64_t B) { return piece_count(N) <= kSmallPieces && B <= kSmallSeqs; }
 
 // A launch that may start while the previous kernel of the stream runs (its kernel waits for
 // it before reading its results).
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), int64_t grid, int threads, cudaStream_t st,
+cudaError_t launch_after(void (*kern)(P...), int64_t grid, int threads, size_t smem, cudaStream_t st,
                          A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -447,7 +564,7 @@ __device__ __forceinline__ double slope_value(const unsigned long long* acc) {
 }
 
 struct PrefConst {
-  double beta, smoothing, margin, unit;  // slopes are counted in units of `unit`
+  double beta, smoothing, margin, unit;  // slopes are counted in units of 1 / `unit`
   int kind;
 };
 
@@ -476,96 +593,133 @@ __device__ __forceinline__ double score_of(const Pair2& t, int average) {
   return average ? (t.w > 0.0 ? t.x / t.w : 0.0) : t.x;
 }
 
-// One warp per pair: its loss and rewards, its slope into both sequences' accumulators, and
-// the block's sum of losses.
+__device__ __forceinline__ Seqs seqs_of(const PreferenceArgs& a) { return {a.cu, (int)a.N, (int)a.B}; }
+
+// Pair p by 16 lanes (eight per sequence; all lanes of a warp call it): its loss and rewards, its
+// slope into both sequences' accumulators.  Its loss comes back in the first of the 16 lanes.
+__device__ __forceinline__ double pair_step(const PreferenceArgs& a, const PrefConst& k, const SeqSums& q,
+                                            int64_t p, unsigned long long* acc, unsigned* err) {
+  const int lane = threadIdx.x & 31, half = (lane >> 3) & 1;
+  const bool live = p < a.P;
+  const int mine = live ? __ldg(a.pairs + 2 * p + half) : 0;
+  const bool ok = mine >= 0 && mine < a.B;
+  const Seqs sq = seqs_of(a);
+  Pair2 t = {0.0, 0.0};
+  // (the sums' shuffles need every lane; without sequences there is nothing to read)
+  if (a.B > 0) t = seq_total(q, sq, ok ? mine : 0, lane & 7, 8);
+  const double f = ok ? score_of(t, a.average) : __longlong_as_double(0x7ff8000000000000ll);
+  const double fb = __shfl_xor_sync(0xffffffffu, f, 8);
+  const int ib = __shfl_xor_sync(0xffffffffu, mine, 8);
+  const bool okb = __shfl_xor_sync(0xffffffffu, (int)ok, 8);
+  if (!live || (lane & 15) != 0) return 0.0;
+  double loss = __longlong_as_double(0x7ff8000000000000ll), slope;
+  if (ok && okb) {
+    pref_pair(f - fb, k, &loss, &slope);
+    slope_add(acc + (int64_t)mine * kLimbs, slope * k.unit);
+    slope_add(acc + (int64_t)ib * kLimbs, -slope * k.unit);
+  } else {
+    atomicOr(err, kErrSegment);
+  }
+  a.pair_loss[p] = (float)loss;
+  a.rewards[2 * p] = (float)(ok && okb ? k.beta * f : loss);
+  a.rewards[2 * p + 1] = (float)(ok && okb ? k.beta * fb : loss);
+  return loss;
+}
+
+// dnll[t] = -w [/ sum w] slope(sequence) / P for pieces [c, c1).
+__device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefConst& k, const SeqSums& q,
+                                            const unsigned long long* acc, int c, int c1) {
+  const Seqs sq = seqs_of(a);
+  const int lane = threadIdx.x & 31;
+  if (c >= c1) return;
+  const double per_pair = a.P ? 1.0 / (k.unit * (double)a.P) : 0.0;
+  double coef = 0.0;  // of the window's sequence
+  auto window = [&](int s) { coef = -slope_value(acc + (int64_t)s * kLimbs) * per_pair; };
+  Walker<decltype(window)> walk(sq, c * kPiece, window);
+  for (; c < c1; ++c) {
+    const int t0 = c * kPiece, t1 = sq.N - t0 < kPiece ? sq.N : t0 + kPiece;
+    float w[kPer], g[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + 32 * i + lane;
+      w[i] = t < t1 ? (a.w ? __ldg(a.w + t) : 1.f) : 0.f;
+      g[i] = 0.f;
+    }
+    walk.piece(t0, t1, [&](int j, int s, int lo, int hi, int, int) {
+      double f = __shfl_sync(0xffffffffu, coef, j);
+      if (a.average) {
+        const double t = seq_total(q, sq, s, lane, 32).w;
+        f = t > 0.0 ? f / t : 0.0;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t0 + 32 * i + lane;
+        if (t >= lo && t < hi && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
+      }
+    });
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + 32 * i + lane;
+      if (t < t1) __stcs(a.dnll + t, g[i]);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) pref_pair_kernel(PreferenceArgs a, PrefConst k, SeqSums q,
                                                         unsigned long long* acc, double* part,
                                                         unsigned* err) {
   allow_dependent_launch();
   grid_dependency_wait();
   __shared__ double red[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double sum = 0.0;
-  for (int64_t p = blockIdx.x * 8ll + warp; p < a.P; p += gridDim.x * 8ll) {
-    const int64_t ia = __ldg(a.pairs + 2 * p), ib = __ldg(a.pairs + 2 * p + 1);
-    double loss, slope = 0.0, fa, fb;
-    if (ia < 0 || ia >= a.B || ib < 0 || ib >= a.B) {
-      loss = fa = fb = __longlong_as_double(0x7ff8000000000000ll);
-      if (lane == 0) atomicOr(err, kErrSegment);
-    } else {
-      fa = score_of(seq_total(q, a.cu, ia, a.N), a.average);
-      fb = score_of(seq_total(q, a.cu, ib, a.N), a.average);
-      pref_pair(fa - fb, k, &loss, &slope);
-      if (lane == 0) {
-        slope_add(acc + ia * kLimbs, slope * k.unit);
-        slope_add(acc + ib * kLimbs, -slope * k.unit);
-      }
-    }
-    if (lane == 0) {
-      a.pair_loss[p] = (float)loss;
-      a.rewards[2 * p] = (float)(k.beta * fa);
-      a.rewards[2 * p + 1] = (float)(k.beta * fb);
-      sum += loss;
-    }
-  }
+  for (int64_t p0 = blockIdx.x * 16ll; p0 < a.P; p0 += gridDim.x * 16ll)
+    sum += pair_step(a, k, q, p0 + (threadIdx.x >> 4), acc, err);
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// dnll[n] = -w [/ sum w] slope(sequence) / P, one warp per piece as in seq_sums_kernel; block
-// 0 also adds the losses.
-__global__ void __launch_bounds__(256) pref_token_kernel(PreferenceArgs a, PrefConst k, SeqSums q,
+__device__ __forceinline__ float pref_mean(const PreferenceArgs& a, double sum) {
+  return a.P ? (float)(sum / (double)a.P) : 0.f;
+}
+
+// Block 0 also adds the losses.
+__global__ void __launch_bounds__(256, 4) pref_token_kernel(PreferenceArgs a, PrefConst k, SeqSums q,
                                                          const unsigned long long* acc,
                                                          const double* part, int npart) {
   grid_dependency_wait();
   __shared__ double red[8];
-  const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {
     double s = 0.0;
     for (int i = threadIdx.x; i < npart; i += 256) s += part[i];
     s = block_sum(s, red);
-    if (threadIdx.x == 0) a.loss[0] = a.P ? (float)(s / (double)a.P) : 0.f;
+    if (threadIdx.x == 0) a.loss[0] = pref_mean(a, s);
   }
-  const int64_t c = (blockIdx.x * 256ll + threadIdx.x) >> 5;
-  const int64_t t0 = c * kPiece;
-  if (t0 >= a.N) return;
-  const int64_t t1 = t0 + kPiece < a.N ? t0 + kPiece : a.N;
-  float w[kPiece / 32], g[kPiece / 32];
-#pragma unroll
-  for (int i = 0; i < kPiece / 32; ++i) {
-    const int64_t t = t0 + 32 * i + lane;
-    w[i] = t < t1 ? (a.w ? __ldg(a.w + t) : 1.f) : 0.f;
-    g[i] = 0.f;
-  }
-  const double per_pair = a.P ? 1.0 / (k.unit * (double)a.P) : 0.0;
-  int64_t pos = t0;
-  const int64_t first = seq_at(a.cu, 0, a.N);
-  if (pos < first) pos = first;
-  int64_t s = -1;
-  while (pos < t1) {
-    int64_t n = s >= 0 && s + 1 < a.B ? s + 1 : -1;
-    if (n >= 0 && !(seq_at(a.cu, n, a.N) <= pos && pos < seq_at(a.cu, n + 1, a.N))) n = -1;
-    s = n >= 0 ? n : seq_of(a.cu, 0, a.B, a.N, pos);
-    if (s < 0) break;
-    const int64_t b1 = seq_at(a.cu, s + 1, a.N);
-    const int64_t hi = b1 < t1 ? b1 : t1;
-    double coef = -slope_value(acc + s * kLimbs) * per_pair;
-    if (a.average) {
-      const double t = seq_total(q, a.cu, s, a.N).w;
-      coef = t > 0.0 ? coef / t : 0.0;
-    }
-#pragma unroll
-    for (int i = 0; i < kPiece / 32; ++i) {
-      const int64_t t = t0 + 32 * i + lane;
-      if (t >= pos && t < hi && w[i] != 0.f) g[i] = (float)(coef * (double)w[i]);
-    }
-    pos = hi;
-  }
-#pragma unroll
-  for (int i = 0; i < kPiece / 32; ++i) {
-    const int64_t t = t0 + 32 * i + lane;
-    if (t < t1) a.dnll[t] = g[i];
-  }
+  int c0, c1;
+  my_pieces(pieces_of(a.N), &c0, &c1);
+  pref_pieces(a, k, q, acc, c0, c1);
+}
+
+// Everything in one block: at most kSmallPieces pieces, kSmallSeqs sequences, kSmallPairs pairs.
+// Dynamic shared memory: B accumulators.
+__global__ void __launch_bounds__(1024) pref_small_kernel(PreferenceArgs a, PrefConst k, unsigned* err) {
+  extern __shared__ unsigned long long acc[];
+  __shared__ double red[32];
+  __shared__ Pair2 whole[kSmallSeqs], head[kSmallPieces], tail[kSmallPieces];
+  grid_dependency_wait();
+  const Seqs sq = seqs_of(a);
+  const SeqSums sums = {whole, head, tail};
+  const int warp = threadIdx.x >> 5;
+  const bool mine = warp * kPiece < sq.N;
+  if (mine) sums_pieces<true>(sq, a.nll, a.nll_ref, a.w, warp, warp + 1, sums);
+  for (int i = threadIdx.x; i < sq.B * kLimbs; i += 1024) acc[i] = 0ull;
+  __syncthreads();
+  double sum = 0.0;
+  for (int64_t p0 = 0; p0 < a.P; p0 += 64) sum += pair_step(a, k, sums, p0 + (threadIdx.x >> 4), acc, err);
+  __syncthreads();
+  if (mine) pref_pieces(a, k, sums, acc, warp, warp + 1);
+  check_seqs(sq, threadIdx.x, 1024, err);
+  sum = block_sum(sum, red);
+  if (threadIdx.x == 0) a.loss[0] = pref_mean(a, sum);
 }
 
 PrefConst pref_const(const PreferenceArgs& a) {
@@ -575,10 +729,13 @@ PrefConst pref_const(const PreferenceArgs& a) {
   return k;
 }
 
+bool pref_small(const PreferenceArgs& a) { return small_tokens(a.N, a.B) && a.P <= kSmallPairs; }
+
 }  // namespace
 
 size_t policy_scratch_bytes(const PolicyArgs& a) {
-  size_t b = 3 * 8 * kMaxBlocks + up256(8 * kMaxBlocks) + up256(4 * kMaxBlocks);
+  if (small_tokens(a.N, a.B)) return 0;
+  size_t b = up256(kMaxBlocks * sizeof(PolicySums)) + up256(kMaxBlocks * 8);
   if (a.reduction == ARCHEAD_REDUCE_SEQUENCE)
     b += up256((size_t)a.B * 8) + (a.w ? seq_sum_bytes(a.N, a.B) : 0);
   return b;
@@ -586,69 +743,75 @@ size_t policy_scratch_bytes(const PolicyArgs& a) {
 
 cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err,
                                cudaStream_t st, int* launches) {
-  char* b = static_cast<char*>(scratch);
   const PolicyConst k = policy_const(a);
-  double* part = reinterpret_cast<double*>(b);
-  b += 3 * 8 * kMaxBlocks;
-  double* wpart = reinterpret_cast<double*>(b);
-  b += up256(8 * kMaxBlocks);
-  unsigned* active = reinterpret_cast<unsigned*>(b);
-  b += up256(4 * kMaxBlocks);
-  const int nb = token_blocks(a.N);
-  int nwp = 0, nact = 0;
-  double* inv = nullptr;
-  if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
-    nwp = nb;
-    policy_weight_kernel<<<nb, 256, 0, st>>>(a.w, a.cu, a.N, a.B, wpart, err);
+  if (small_tokens(a.N, a.B)) {
     ++*launches;
+    return launch_after(policy_small_kernel, 1, 1024, 0, st, a, k, err);
+  }
+  char* b = static_cast<char*>(scratch);
+  PolicySums* part = reinterpret_cast<PolicySums*>(b);
+  b += up256(kMaxBlocks * sizeof(PolicySums));
+  double* total = reinterpret_cast<double*>(b);
+  b += up256(kMaxBlocks * 8);
+  const int64_t pb = (piece_count(a.N) + 7) / 8;
+  const int nb = capped(pb);  // blocks of the token kernels
+  int nt = 0;
+  double* inv = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
+    nt = nb;
+    policy_weight_kernel<<<nt, 256, 0, st>>>(a, total, err);
+    ++*launches;
+    e = cudaGetLastError();
   } else if (a.reduction == ARCHEAD_REDUCE_SEQUENCE) {
     inv = reinterpret_cast<double*>(b);
     b += up256((size_t)a.B * 8);
     SeqSums q = {};
     if (a.w) {
       q = carve_seq_sums(b, a.N, a.B);
-      const int64_t blocks = (piece_count(a.N) + 7) / 8;
-      seq_sums_kernel<<<(unsigned)(blocks < 1 ? 1 : blocks), 256, 0, st>>>(
-          nullptr, nullptr, a.w, a.cu, a.N, a.B, q, nullptr, 0, err);
+      const Seqs sq = {a.cu, (int)a.N, (int)a.B};
+      seq_sums_kernel<false><<<nb, 256, 0, st>>>(nullptr, nullptr, a.w, sq, q, nullptr, 0, err);
       ++*launches;
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    nact = seq_blocks(a.B);
-    const cudaError_t e = launch_after(policy_seq_kernel, nact, 256, st, q, a.w, a.cu, a.N, a.B,
-                                       inv, active, err);
-    if (e != cudaSuccess) return e;
+    nt = capped((a.B + 31) / 32);
+    e = launch_after(policy_seq_kernel, nt, 256, 0, st, a, q, inv, total, err);
     ++*launches;
   }
-  cudaError_t e = launch_after(policy_token_kernel, nb, 256, st, a, k, inv, active, nact, wpart,
-                               nwp, part, err);
   if (e != cudaSuccess) return e;
-  e = launch_after(policy_final_kernel, 1, 256, st, part, nb, a.kl_coef, a.stats);
+  e = launch_after(policy_token_kernel, nb, 256, 0, st, a, k, inv, nt ? total : nullptr, nt, part, err);
+  if (e != cudaSuccess) return e;
   *launches += 2;
-  return e;
+  return launch_after(policy_final_kernel, 1, 256, 0, st, part, nb, a.kl_coef, a.stats);
 }
 
 size_t preference_scratch_bytes(const PreferenceArgs& a) {
+  if (pref_small(a)) return 0;
   return up256(8 * kMaxBlocks) + up256((size_t)a.B * kLimbs * 8) + seq_sum_bytes(a.N, a.B);
 }
 
 cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsigned* err,
                                    cudaStream_t st, int* launches) {
-  char* b = static_cast<char*>(scratch);
   const PrefConst k = pref_const(a);
+  if (pref_small(a)) {
+    ++*launches;
+    return launch_after(pref_small_kernel, 1, 1024, (size_t)a.B * kLimbs * 8, st, a, k, err);
+  }
+  char* b = static_cast<char*>(scratch);
   double* part = reinterpret_cast<double*>(b);
   b += up256(8 * kMaxBlocks);
   unsigned long long* acc = reinterpret_cast<unsigned long long*>(b);
   b += up256((size_t)a.B * kLimbs * 8);
   const SeqSums q = carve_seq_sums(b, a.N, a.B);
-  int64_t pb = (piece_count(a.N) + 7) / 8;
-  if (pb < 1) pb = 1;
-  seq_sums_kernel<<<(unsigned)pb, 256, 0, st>>>(a.nll, a.nll_ref, a.w, a.cu, a.N, a.B, q, acc,
-                                               a.B * kLimbs, err);
+  const Seqs sq = {a.cu, (int)a.N, (int)a.B};
+  const int pb = capped((piece_count(a.N) + 7) / 8);
+  seq_sums_kernel<true><<<pb, 256, 0, st>>>(a.nll, a.nll_ref, a.w, sq, q, acc, a.B * kLimbs, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int np = seq_blocks(a.P);
-  e = launch_after(pref_pair_kernel, np, 256, st, a, k, q, acc, part, err);
+  const int np = capped((a.P + 15) / 16);
+  e = launch_after(pref_pair_kernel, np, 256, 0, st, a, k, q, acc, part, err);
   if (e != cudaSuccess) return e;
-  e = launch_after(pref_token_kernel, pb, 256, st, a, k, q, acc, part, np);
+  e = launch_after(pref_token_kernel, pb, 256, 0, st, a, k, q, acc, part, np);
   *launches += 3;
   return e;
 }
