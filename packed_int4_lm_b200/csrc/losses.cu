@@ -3,8 +3,8 @@
 //
 // Both are a pass over a few floats per token plus sums over ragged sequences, so device
 // memory bounds them when the batch is large and launches when it is small.  The tokens are cut
-// into pieces of 256, one warp each: a lane holds eight of them in registers, all loads in
-// flight, and the warp walks the sequences that lie in its pieces (adjacent ones, so that the
+// into pieces of 256: a lane holds eight tokens of a piece, two 16-byte loads per array where
+// the arrays are aligned to it, and the warp walks the sequences that lie in its pieces (adjacent ones, so that the
 // first sequence is searched for once, 32 probes a step).  A sequence inside a piece is summed by its warp;
 // one that crosses pieces leaves one partial sum per piece (`tail` where it starts, `head` in
 // each later piece), which its readers add in order.  The steps are device functions:
@@ -21,10 +21,10 @@
 namespace archead {
 namespace {
 
-constexpr int kPiece = 256, kPer = kPiece / 32;  // tokens per warp, per lane
-constexpr int kMaxBlocks = 148 * 4;              // blocks of a launch: what runs at once, so that
-                                                 // a warp's pieces lie side by side
-constexpr int kSmallPieces = 32;                 // one block's warps
+constexpr int kPer = 8, kPiece = 32 * kPer;  // tokens per lane, per warp
+constexpr int kMaxBlocks = 148 * 4;          // blocks of a launch: what runs at once, so that a
+                                             // warp's pieces lie side by side
+constexpr int kSmallPieces = 32;             // what one block takes, one piece per warp
 constexpr int kSmallSeqs = 512, kSmallPairs = 1024;  // (30 KB of shared memory)
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -129,6 +129,47 @@ struct Walker {
   }
 };
 
+// The lane's i-th token of the piece at t0: two runs of four adjacent ones.
+__device__ __forceinline__ int token_at(int t0, int i) {
+  return t0 + 128 * (i >> 2) + 4 * (threadIdx.x & 31) + (i & 3);
+}
+// A piece's values at the lane's tokens; `other` past t1 (and, for p == nullptr, everywhere).
+// vec: p is 16-byte aligned.
+__device__ __forceinline__ void load_piece(const float* p, int t0, int t1, bool vec, float other, float (&v)[kPer]) {
+  if (p && vec && t1 - t0 == kPiece) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(p + token_at(t0, i)));
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = token_at(t0, i);
+      v[i] = p && t < t1 ? __ldg(p + t) : other;
+    }
+  }
+}
+__device__ __forceinline__ void store_piece(float* p, int t0, int t1, bool vec, const float (&v)[kPer]) {
+  if (vec && t1 - t0 == kPiece) {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4)
+      __stcs(reinterpret_cast<float4*>(p + token_at(t0, i)), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (token_at(t0, i) < t1) p[token_at(t0, i)] = v[i];
+  }
+}
+__device__ __forceinline__ bool aligned16(const void* a, const void* b = nullptr, const void* c = nullptr,
+                                          const void* d = nullptr, const void* e = nullptr, const void* f = nullptr) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+           reinterpret_cast<uintptr_t>(d) | reinterpret_cast<uintptr_t>(e) | reinterpret_cast<uintptr_t>(f)) & 15) == 0;
+}
+
 // Per sequence the sums of a weight and a value.
 struct Pair2 {
   double w, x;
@@ -144,20 +185,18 @@ struct SeqSums {
 template <bool kValue>
 __device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, const float* ref,
                                             const float* w, int c, int c1, const SeqSums& out) {
-  const int lane = threadIdx.x & 31;
   if (c >= c1) return;
+  const int lane = threadIdx.x & 31;
+  const bool vec = aligned16(nll, ref, w);
   auto none = [](int) {};
   Walker<decltype(none)> walk(q, c * kPiece, none);
   for (; c < c1; ++c) {
     const int t0 = c * kPiece, t1 = q.N - t0 < kPiece ? q.N : t0 + kPiece;
     float wf[kPer], a[kPer], b[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int t = t0 + 32 * k + lane;
-      const bool in = t < t1;
-      wf[k] = in ? (w ? __ldg(w + t) : 1.f) : 0.f;
-      a[k] = kValue && in ? __ldg(nll + t) : 0.f;
-      b[k] = kValue && in && ref ? __ldg(ref + t) : 0.f;
+    load_piece(w, t0, t1, vec, w ? 0.f : 1.f, wf);
+    if (kValue) {
+      load_piece(nll, t0, t1, vec, 0.f, a);
+      load_piece(ref, t0, t1, vec, 0.f, b);
     }
     double x[kPer];
 #pragma unroll
@@ -165,10 +204,11 @@ __device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, con
       x[k] = kValue && wf[k] != 0.f ? (double)wf[k] * ((double)b[k] - (double)a[k]) : 0.0;
     walk.piece(t0, t1, [&](int, int s, int lo, int hi, int b0, int b1) {
       Pair2 sum = {0.0, 0.0};
+      const bool whole = hi - lo == kPiece;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int t = t0 + 32 * k + lane;
-        if (t >= lo && t < hi) {
+        const int t = token_at(t0, k);
+        if (whole || (t >= lo && t < hi)) {
           sum.w += (double)wf[k];
           sum.x += x[k];
         }
@@ -211,8 +251,9 @@ __device__ __forceinline__ Pair2 seq_total(const SeqSums& q, const Seqs& sq, int
 
 // ---- policy loss ------------------------------------------------------------------------
 struct PolicyConst {
-  double log_hi, log_lo;  // log(1 + clip_high), log(1 - clip_low)
-  double hi, lo;          // 1 + clip_high, 1 - clip_low
+  double log_hi, log_lo;    // log(1 + clip_high), log(1 - clip_low)
+  float log_hi_f, log_lo_f;  // rounded
+  float hi, lo;              // 1 + clip_high, 1 - clip_low
   double kl_coef;
 };
 
@@ -221,45 +262,51 @@ struct PolicyTok {
   bool clipped;
 };
 
-// exp(z) - 1 - z: its Taylor series near 0, where the difference cancels (the first term left
-// out is below 5e-8 of the sum at |z| = 1/2).
-__device__ __forceinline__ float kl_term(float z, float em1) {
-  if (fabsf(z) >= 0.5f) return em1 - z;
-  float p = fmaf(z, 1.f / 8, 1.f);
-  p = fmaf(z * (1.f / 7), p, 1.f);
-  p = fmaf(z * (1.f / 6), p, 1.f);
-  p = fmaf(z * (1.f / 5), p, 1.f);
-  p = fmaf(z * (1.f / 4), p, 1.f);
-  p = fmaf(z * (1.f / 3), p, 1.f);
-  return 0.5f * z * z * p;
+__device__ __forceinline__ float exp_f(float x) {
+  float y;  // e^x as 2^(x log2 e): off by about 2^-22 and 2^-24 |x|
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
 }
 
-// Whether old - nll > limit exactly: rounding is monotone, so only where the rounded difference
-// equals the rounded limit does the FP64 difference (exact) decide.
-__device__ __forceinline__ bool beyond(float x, float old, float nll, double limit, bool above) {
-  const float l = (float)limit;
-  if (x != l) return above ? x > l : x < l;
-  const double d = (double)old - (double)nll;
-  return above ? d > limit : d < limit;
+// k = e^z - 1 - z.  Near 0, where the difference cancels, z^2 times its Taylor series (the first
+// term left out is below 2^-24 of the sum at |z| = 1).
+__device__ __forceinline__ float kl_term(float z) {
+  float p = 1.f / 479001600;
+  p = fmaf(p, z, 1.f / 39916800);
+  p = fmaf(p, z, 1.f / 3628800);
+  p = fmaf(p, z, 1.f / 362880);
+  p = fmaf(p, z, 1.f / 40320);
+  p = fmaf(p, z, 1.f / 5040);
+  p = fmaf(p, z, 1.f / 720);
+  p = fmaf(p, z, 1.f / 120);
+  p = fmaf(p, z, 1.f / 24);
+  p = fmaf(p, z, 1.f / 6);
+  p = fmaf(p, z, 0.5f);
+  return fabsf(z) < 1.f ? z * z * p : exp_f(z) - 1.f - z;
 }
 
 __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A, bool has_ref,
                                                   float ref, const PolicyConst& k) {
+  // The side of the clip border is that of the exact difference old - nll against log(1 +- clip).
+  // Rounding is monotone, so the rounded difference decides unless it equals the rounded border;
+  // then the FP64 difference (exact) does.
   const float x = old - nll;
-  PolicyTok o = {0.f, 0.f, 0.f, false};
-  if (A != 0.f) {  // (0 times an infinite ratio is 0 here)
-    o.clipped = beyond(x, old, nll, A > 0.f ? k.log_hi : k.log_lo, A > 0.f);
-    if (o.clipped) {
-      o.sur = -(float)(A > 0.f ? k.hi : k.lo) * A;
-    } else {
-      o.grad = expf(x) * A;
-      o.sur = -o.grad;
-    }
+  const bool up = A > 0.f;
+  const float l = up ? k.log_hi_f : k.log_lo_f;
+  PolicyTok o;
+  o.clipped = up ? x > l : A < 0.f && x < l;
+  if (x == l && A != 0.f) {
+    const double d = (double)old - (double)nll;
+    o.clipped = up ? d > k.log_hi : d < k.log_lo;
   }
+  const float r = A == 0.f ? 0.f : exp_f(x) * A;  // (0 times an infinite ratio is 0 here)
+  o.grad = o.clipped ? 0.f : r;
+  o.sur = -(o.clipped ? (up ? k.hi : k.lo) * A : r);
+  o.kl = 0.f;
   if (has_ref) {
-    const float z = nll - ref, em1 = expm1f(z);
-    o.kl = kl_term(z, em1);
-    o.grad = fmaf((float)k.kl_coef, em1, o.grad);
+    const float z = nll - ref;
+    o.kl = kl_term(z);
+    o.grad = fmaf((float)k.kl_coef, z + o.kl, o.grad);  // e^z - 1 = z + k
   }
   return o;
 }
@@ -276,9 +323,9 @@ __device__ __forceinline__ Seqs seqs_of(const PolicyArgs& a) { return {a.cu, (in
 __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyConst& k, int c, int c1,
                                               double scale, const double* inv, PolicySums& sum) {
   const Seqs q = seqs_of(a);
-  const int lane = threadIdx.x & 31;
   if (c >= c1) return;
   const bool by_seq = a.reduction == ARCHEAD_REDUCE_SEQUENCE, walks = by_seq || a.adv_per_seq;
+  const bool vec = aligned16(a.nll, a.nll_old, a.nll_ref, a.adv_per_seq ? nullptr : a.adv, a.w, a.dnll);
   const int first = !q.cu ? 0 : (q.B > 0 ? seq_at(q, 0) : q.N), last = q.cu ? seq_at(q, q.B) : q.N;
   float sc = 0.f, adv = 0.f;  // of the window's sequence
   auto window = [&](int s) {
@@ -289,29 +336,22 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
   for (; c < c1; ++c) {
     const int t0 = c * kPiece, t1 = q.N - t0 < kPiece ? q.N : t0 + kPiece;
     float nll[kPer], old[kPer], ref[kPer], A[kPer], f[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + 32 * i + lane;
-      const bool in = t < t1;
-      nll[i] = in ? __ldg(a.nll + t) : 0.f;
-      old[i] = in ? __ldg(a.nll_old + t) : 0.f;
-      ref[i] = in && a.nll_ref ? __ldg(a.nll_ref + t) : 0.f;
-      A[i] = in && !a.adv_per_seq ? __ldg(a.adv + t) : 0.f;
-      f[i] = in ? (a.w ? __ldg(a.w + t) : 1.f) : 0.f;
-    }
+    load_piece(a.nll, t0, t1, vec, 0.f, nll);
+    load_piece(a.nll_old, t0, t1, vec, 0.f, old);
+    load_piece(a.nll_ref, t0, t1, vec, 0.f, ref);
+    load_piece(a.adv_per_seq ? nullptr : a.adv, t0, t1, vec, 0.f, A);
+    load_piece(a.w, t0, t1, vec, a.w ? 0.f : 1.f, f);
     if (walks) {
-      float g[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) g[i] = 0.f;  // outside every sequence
+      float g[kPer] = {};  // outside every sequence
       walk.piece(t0, t1, [&](int j, int, int lo, int hi, int, int) {
         const float fs = __shfl_sync(0xffffffffu, sc, j), as = __shfl_sync(0xffffffffu, adv, j);
+        const bool whole = hi - lo == kPiece;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int t = t0 + 32 * i + lane;
-          if (t >= lo && t < hi) {
-            g[i] = fs;
-            if (a.adv_per_seq) A[i] = as;
-          }
+          const int t = token_at(t0, i);
+          const bool in = whole || (t >= lo && t < hi);
+          g[i] = in ? fs : g[i];
+          A[i] = in && a.adv_per_seq ? as : A[i];
         }
       });
 #pragma unroll
@@ -319,24 +359,22 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int t = t0 + 32 * i + lane;
+        const int t = token_at(t0, i);
         f[i] = t >= first && t < last ? f[i] * (float)scale : 0.f;
       }
     }
-    float sur = 0.f, kl = 0.f, clipped = 0.f;
+    float sur = 0.f, kl = 0.f, clipped = 0.f, g[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + 32 * i + lane;
-      float g = 0.f;
-      if (f[i] != 0.f) {
-        const PolicyTok o = policy_token(nll[i], old[i], A[i], a.nll_ref != nullptr, ref[i], k);
-        sur = fmaf(f[i], o.sur, sur);
-        kl = fmaf(f[i], o.kl, kl);
-        if (o.clipped) clipped += f[i];
-        g = f[i] * o.grad;
-      }
-      if (t < t1) __stcs(a.dnll + t, g);
+    for (int i = 0; i < kPer; ++i) {  // no branch on the weight: eight chains side by side
+      const bool on = f[i] != 0.f;
+      const PolicyTok o = policy_token(on ? nll[i] : 0.f, on ? old[i] : 0.f, on ? A[i] : 0.f, a.nll_ref != nullptr,
+                                       on ? ref[i] : 0.f, k);
+      sur = fmaf(f[i], o.sur, sur);
+      kl = fmaf(f[i], o.kl, kl);
+      clipped += o.clipped ? f[i] : 0.f;
+      g[i] = f[i] * o.grad;
     }
+    store_piece(a.dnll, t0, t1, vec, g);
     sum.sur += (double)sur;
     sum.kl += (double)kl;
     sum.clipped += (double)clipped;
@@ -370,7 +408,7 @@ __device__ __forceinline__ double policy_seq_inv(const PolicyArgs& a, const SeqS
 }
 
 template <bool kValue>
-__global__ void __launch_bounds__(256, kValue ? 4 : 5) seq_sums_kernel(const float* __restrict__ nll,
+__global__ void __launch_bounds__(256, 4) seq_sums_kernel(const float* __restrict__ nll,
                                                        const float* __restrict__ ref,
                                                        const float* __restrict__ w, Seqs q,
                                                        SeqSums out, unsigned long long* zero,
@@ -420,17 +458,15 @@ __global__ void __launch_bounds__(256, 4) policy_token_kernel(PolicyArgs a, Poli
   allow_dependent_launch();
   grid_dependency_wait();
   __shared__ double red[8];
-  __shared__ double scale_s;
-  if (total) {
+  double scale = 1.0;
+  if (total) {  // every warp for itself: no barrier before its loads
     double t = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) t += total[i];
-    t = block_sum(t, red);
-    if (threadIdx.x == 0) scale_s = t > 0.0 ? 1.0 / t : 0.0;
-    __syncthreads();
+    for (int i = threadIdx.x & 31; i < n; i += 32) t += total[i];
+    t = warp_sum(t);
+    scale = t > 0.0 ? 1.0 / t : 0.0;
   } else {
     check_seqs(seqs_of(a), blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll, err);
   }
-  const double scale = total ? scale_s : 1.0;
   PolicySums s = {0.0, 0.0, 0.0};
   int c0, c1;
   my_pieces(pieces_of(a.N), &c0, &c1);
@@ -465,11 +501,11 @@ __global__ void __launch_bounds__(1024) policy_small_kernel(PolicyArgs a, Policy
   grid_dependency_wait();
   const Seqs q = seqs_of(a);
   const SeqSums sums = {whole, head, tail};
-  const int warp = threadIdx.x >> 5;
-  const bool mine = warp * kPiece < q.N;
+  int c0, c1;
+  my_pieces(pieces_of(q.N), &c0, &c1);
   double t = threadIdx.x == 0 ? 1.0 : 0.0;
   if (a.reduction == ARCHEAD_REDUCE_SEQUENCE) {
-    if (a.w && mine) sums_pieces<false>(q, nullptr, nullptr, a.w, warp, warp + 1, sums);
+    if (a.w) sums_pieces<false>(q, nullptr, nullptr, a.w, c0, c1, sums);
     __syncthreads();
     t = 0.0;
     for (int s0 = 0; s0 < q.B; s0 += 128) {
@@ -487,7 +523,7 @@ __global__ void __launch_bounds__(1024) policy_small_kernel(PolicyArgs a, Policy
   if (threadIdx.x == 0) scale_s = t > 0.0 ? 1.0 / t : 0.0;
   __syncthreads();
   PolicySums s = {0.0, 0.0, 0.0};
-  if (mine) policy_pieces(a, k, warp, warp + 1, scale_s, inv, s);
+  policy_pieces(a, k, c0, c1, scale_s, inv, s);
   check_seqs(q, threadIdx.x, 1024, err);
   s.sur = block_sum(s.sur, red);
   s.kl = block_sum(s.kl, red);
@@ -496,7 +532,8 @@ __global__ void __launch_bounds__(1024) policy_small_kernel(PolicyArgs a, Policy
 }
 
 PolicyConst policy_const(const PolicyArgs& a) {
-  return {log1p(a.clip_high), log1p(-a.clip_low), 1.0 + a.clip_high, 1.0 - a.clip_low, a.kl_coef};
+  const double hi = log1p(a.clip_high), lo = log1p(-a.clip_low);
+  return {hi, lo, (float)hi, (float)lo, (float)(1.0 + a.clip_high), (float)(1.0 - a.clip_low), a.kl_coef};
 }
 
 int64_t piece_count(int64_t N) { return (N + kPiece - 1) / kPiece; }
@@ -633,18 +670,14 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
   const int lane = threadIdx.x & 31;
   if (c >= c1) return;
   const double per_pair = a.P ? 1.0 / (k.unit * (double)a.P) : 0.0;
+  const bool vec = aligned16(a.w, a.dnll);
   double coef = 0.0;  // of the window's sequence
   auto window = [&](int s) { coef = -slope_value(acc + (int64_t)s * kLimbs) * per_pair; };
   Walker<decltype(window)> walk(sq, c * kPiece, window);
   for (; c < c1; ++c) {
     const int t0 = c * kPiece, t1 = sq.N - t0 < kPiece ? sq.N : t0 + kPiece;
-    float w[kPer], g[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + 32 * i + lane;
-      w[i] = t < t1 ? (a.w ? __ldg(a.w + t) : 1.f) : 0.f;
-      g[i] = 0.f;
-    }
+    float w[kPer], g[kPer] = {};
+    load_piece(a.w, t0, t1, vec, a.w ? 0.f : 1.f, w);
     walk.piece(t0, t1, [&](int j, int s, int lo, int hi, int, int) {
       double f = __shfl_sync(0xffffffffu, coef, j);
       if (a.average) {
@@ -653,15 +686,11 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int t = t0 + 32 * i + lane;
+        const int t = token_at(t0, i);
         if (t >= lo && t < hi && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
       }
     });
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + 32 * i + lane;
-      if (t < t1) __stcs(a.dnll + t, g[i]);
-    }
+    store_piece(a.dnll, t0, t1, vec, g);
   }
 }
 
@@ -708,15 +737,15 @@ __global__ void __launch_bounds__(1024) pref_small_kernel(PreferenceArgs a, Pref
   grid_dependency_wait();
   const Seqs sq = seqs_of(a);
   const SeqSums sums = {whole, head, tail};
-  const int warp = threadIdx.x >> 5;
-  const bool mine = warp * kPiece < sq.N;
-  if (mine) sums_pieces<true>(sq, a.nll, a.nll_ref, a.w, warp, warp + 1, sums);
+  int c0, c1;
+  my_pieces(pieces_of(sq.N), &c0, &c1);
+  sums_pieces<true>(sq, a.nll, a.nll_ref, a.w, c0, c1, sums);
   for (int i = threadIdx.x; i < sq.B * kLimbs; i += 1024) acc[i] = 0ull;
   __syncthreads();
   double sum = 0.0;
   for (int64_t p0 = 0; p0 < a.P; p0 += 64) sum += pair_step(a, k, sums, p0 + (threadIdx.x >> 4), acc, err);
   __syncthreads();
-  if (mine) pref_pieces(a, k, sums, acc, warp, warp + 1);
+  pref_pieces(a, k, sums, acc, c0, c1);
   check_seqs(sq, threadIdx.x, 1024, err);
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) a.loss[0] = pref_mean(a, sum);
@@ -759,7 +788,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err
   double* inv = nullptr;
   cudaError_t e = cudaSuccess;
   if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
-    nt = nb;
+    nt = nb < 148 ? nb : 148;
     policy_weight_kernel<<<nt, 256, 0, st>>>(a, total, err);
     ++*launches;
     e = cudaGetLastError();
@@ -774,7 +803,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err
       ++*launches;
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    nt = capped((a.B + 31) / 32);
+    nt = capped((a.B + 31) / 32) < 256 ? capped((a.B + 31) / 32) : 256;
     e = launch_after(policy_seq_kernel, nt, 256, 0, st, a, q, inv, total, err);
     ++*launches;
   }
