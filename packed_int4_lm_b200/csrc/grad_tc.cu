@@ -27,10 +27,9 @@ namespace archead {
 namespace {
 
 constexpr int kDequantWarps = 16;
-constexpr int kGradThreads = 32 * (kDequantWarps + 8);  // + 4 epilogue, 2 producers, 2 MMA
+constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 1 producer, 2 MMA
 constexpr int kUnit = 128;                              // vocabulary rows per unit of K
 constexpr int kWStage = 32 * 256 * 2;                   // 32 rows x 256 columns FP16
-constexpr int kPkStage = 16384;                         // 128 rows x 256 columns of nibbles
 constexpr int kRowBlocks = 296;                         // blocks of grad_rows_kernel
 
 // ---- the image ---------------------------------------------------------------------------
@@ -38,7 +37,7 @@ struct RowsParams {
   archead_head h;
   int64_t vpad;
   float* sp;         // S'_v, vpad (0 past V)
-  float* cs;         // 2^-k per row (grad_row), vpad (0 past V)
+  uint32_t* cs;      // 2^-k per row (grad_row) as FP16x2, vpad (0 past V)
   float2* row;       // TcImage's rows without -es, or nullptr
   float* spmax;      // kRowBlocks
   unsigned* amax;    // per token, cleared here (n), or nullptr
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
       }
     }
     p.sp[v] = s;
-    p.cs[v] = c;
+    p.cs[v] = h2_bits(__float2half2_rn(c));
     if (p.row) p.row[v] = make_float2(log2f(fabsf(s)), __uint_as_float(s < 0.f ? 0x80008000u : 0u));
     m = fmaxf(m, fabsf(s));
   }
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
 struct GradParams {
   archead_head h;
   const char* img;
-  const float* cs;
+  const uint32_t* cs;
   float* part;  // [slab][n][dp]
   int64_t n, dp;
   int64_t nunits;  // units of 128 vocabulary rows
@@ -337,24 +336,25 @@ struct GradParams {
 // IT: tokens per tile of the image (at most 128); MT: image tiles (accumulators) per item.
 template <int IT, int MT>
 struct GradCfg {
-  // Shared memory (227 KB): rings of W stages (32 rows x 256 columns, 16 KB), image stages (64
-  // rows x IT tokens, one per accumulator) and packed stages (128 rows x 256 columns, 16 KB).
-  // A copy takes about 3000 cycles from the release of its slot (a commit's 700 among them), so
-  // the image ring covers four steps of 1024 cycles with two accumulators; the W ring is a
-  // multiple of the unit's four stages, so a warp always fills the same slots.  Two threads issue
-  // MMAs, each into its own accumulator of 256 columns: one alone left the tensor cores idle for
-  // about 350 cycles between steps (barrier round trips; an issue returns when the MMA before it
-  // is nearly done).  With MT = 2 an accumulator is an image tile; with MT = 1 the steps alternate
-  // between the two, which the epilogue adds.
+  // Shared memory (227 KB): rings of W stages (32 rows x 256 columns, 16 KB) and image stages (64
+  // rows x IT tokens, one per accumulator).  A copy takes about 3000 cycles from the release of its
+  // slot (a commit's 700 among them), so the image ring covers five steps of 1024 cycles with two
+  // accumulators; the W ring is a multiple of the unit's four stages, so a warp always fills the
+  // same slots.  (The packed head goes straight into the warps' registers, a unit ahead: 32 lanes
+  // read 512 adjacent bytes.  Through a ring of its own in shared memory, four units deep, the
+  // copies' latency set the pace of small batches.)  Two threads issue MMAs, each into its own
+  // accumulator of 256 columns: one alone left the tensor cores idle for about 350 cycles between
+  // steps (barrier round trips; an issue returns when the MMA before it is nearly done).  With MT =
+  // 2 an accumulator is an image tile; with MT = 1 the steps alternate between the two, which the
+  // epilogue adds.
   static constexpr int SW = MT == 2 ? 4 : 8;
-  static constexpr int SI = MT == 2 ? 8 : (IT == 128 ? 4 : 8);
-  static constexpr int SP = MT == 2 ? 2 : (IT == 128 ? 2 : (IT == 64 ? 2 : 4));
+  static constexpr int SI = MT == 2 ? 10 : (IT == 128 ? 6 : 8);
   static constexpr int ISTAGE = IT * 128;
-  static constexpr size_t SMEM = (size_t)SW * kWStage + SI * ISTAGE + SP * kPkStage + 1024 + 512;
+  static constexpr size_t SMEM = (size_t)SW * kWStage + SI * ISTAGE + 1024 + 512;
   static_assert(SMEM <= 227 * 1024, "does not fit an SM");
-  // the MMA reads 128 rows from an image stage: past a smaller one lies the packed ring (those
-  // lanes are never stored)
-  static_assert(SP * kPkStage >= 128 * 128, "reads past the last image stage stay inside");
+  // the MMA reads 128 rows from an image stage: past a smaller one lies the W ring (those lanes
+  // are never stored)
+  static_assert(SW * kWStage >= 128 * 128, "reads past the last image stage stay inside");
 };
 
 struct GradItem {
@@ -434,21 +434,28 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, u
   return true;
 }
 
-// The code bytes (CPC of them) and 2^-k of one vocabulary row, for one block of 128 columns.
-struct RowLoad {
-  uint32_t code;
-  float cs;
-};
+// The code bytes (CPC of them) of one vocabulary row for one block of 128 columns, and its word of
+// the row table.  Volatile: issued here, an iteration before their use (the compiler would move
+// plain loads down to it, where they cost a round trip to memory per unit).
 template <int CPC>
-__device__ __forceinline__ RowLoad load_grad_row(const GradParams& p, int64_t v, int64_t col) {
-  RowLoad r = {0u, 0.f};
-  if (CPC == 0) return r;
-  r.cs = __ldg(p.cs + v);  // rows past V are padded, as are their codes
-  const uint8_t* c = p.h.r_code + v * (p.h.D >> p.g_shift) + (col >> p.g_shift);
-  if (CPC == 1) r.code = __ldg(c);
-  else if (CPC == 2) r.code = __ldg(reinterpret_cast<const uint16_t*>(c));
-  else r.code = __ldg(reinterpret_cast<const uint32_t*>(c));
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* c) {
+  uint32_t r;
+  if (CPC == 1) asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(c));
+  else if (CPC == 2) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(r) : "l"(c));  // (zero-extended)
+  else asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
   return r;
+}
+__device__ __forceinline__ uint32_t load_word(const uint32_t* c) {
+  uint32_t r;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
+  return r;
+}
+// Code e of them times 2^-k, twice in FP16 (exact for k <= 24): 1024 + c is a half with the byte c
+// in its low mantissa bits.
+__device__ __forceinline__ __half2 code_half2(uint32_t codes, int e, uint32_t cs) {
+  const uint32_t r = __byte_perm(codes, 0x64646464u, 0x4040u + 0x0101u * e);
+  return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(1024.f)),
+                 *reinterpret_cast<const __half2*>(&cs));
 }
 
 template <int IT, int MT, int CPC>
@@ -456,17 +463,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
   using C = GradCfg<IT, MT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* Ws = smem;
-  unsigned char* Is = Ws + C::SW * kWStage;
-  unsigned char* Ps = Is + C::SI * C::ISTAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(Ps + C::SP * kPkStage);
+  unsigned char* Is = smem;
+  unsigned char* Ws = Is + C::SI * C::ISTAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(Ws + C::SW * kWStage);
   uint64_t* w_full = bars;
   uint64_t* w_empty = w_full + C::SW;
   uint64_t* i_full = w_empty + C::SW;
   uint64_t* i_empty = i_full + C::SI;
-  uint64_t* p_full = i_empty + C::SI;
-  uint64_t* p_empty = p_full + C::SP;
-  uint64_t* acc_full = p_empty + C::SP;
+  uint64_t* acc_full = i_empty + C::SI;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* mma_done = acc_empty + 1;  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
@@ -481,17 +485,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
       tc::mbar_init(&i_full[i], 1);
       tc::mbar_init(&i_empty[i], 1);
     }
-    for (int i = 0; i < C::SP; ++i) {
-      tc::mbar_init(&p_full[i], 1);
-      tc::mbar_init(&p_empty[i], kDequantWarps / (3 - MT));
-    }
     tc::mbar_init(acc_full, 2);
     tc::mbar_init(acc_empty, 128);
     tc::mbar_init(&mma_done[0], 1);
     tc::mbar_init(&mma_done[1], 1);
     tc::mbar_fence_init();
   }
-  if (warp == kDequantWarps + 6) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == kDequantWarps + 5) tc::tmem_alloc(tmem_slot, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -503,18 +503,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     // A warp owns rows 32 rg .. + 31 (a W stage) and one 128-column block b: with two accumulators
     // half of that block's 16-byte chunks in every unit; with one, where units follow one another
     // twice as fast, all of them in every other unit, which halves what a unit pays for barriers
-    // and fences (N = 1: %UG%).
+    // and fences (N = 1 with a dY of FP32: 148 -> 141 us).
     constexpr int NH = 3 - MT;  // halves of the chunks per warp, and groups of warps by unit
     const int rg = warp & 3, b = (warp >> 2) & 1, grp = warp >> 3;
     const int s = 32 * rg + lane;  // row in the unit
-    const uint32_t w_row = tc::smem_u32(Ws) + (uint32_t)(b * 2) * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
-    const uint32_t x7 = lane & 7;
-    const unsigned char* const p_src = Ps + b * 8192 + s * 16;
     const int slot = NH == 2 ? 4 * grp + rg : rg;  // its place in the W ring (one or two units)
-    static_assert(C::SW == 4 * NH && C::SP % NH == 0, "a slot belongs to one group of warps");
+    static_assert(C::SW == 4 * NH, "a slot belongs to one group of warps");
+    // The lane's 128-byte row of the slot, with its swizzle: chunk j of the block's first 64-column
+    // atom is stored at w_addr ^ 16 j, of the second 4096 bytes on.
+    const uint32_t w_addr = tc::smem_u32(Ws) + (uint32_t)(slot * kWStage + b * 2 * 4096 + (lane >> 3) * 1024 +
+                                                          (lane & 7) * 128 + ((lane & 7) << 4));
     uint32_t wp = 1;  // parity of the slot's last release (the first use waits for none)
-    int ps = NH == 2 ? grp : 0;
-    uint32_t pp = 0;
     int64_t seq = 0;  // units of this CTA so far
     bool copied = false;  // a copy from the factor image was the slot's last use
     bool ok = true;
@@ -548,44 +547,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
       }
       const bool work = 128 * b < it.cols;
       const int64_t col = 256ll * it.dt + (work ? 128 * b : 0);
-      // One unit ahead: its packed chunks are read into registers while this unit's entries are
-      // stored, and the barriers of the next steps are probed before their answers are needed.
-      RowLoad r = {0u, 0.f};
-      if (ua < it.u1) r = load_grad_row<CPC>(p, ua * kUnit + s, col);
-      uint4 q[2 * NH];
-      auto take_packed = [&](bool ready) -> bool {  // q = the next packed unit
-        if (!__all_sync(0xffffffffu, ready) && !__all_sync(0xffffffffu, tc::mbar_wait(&p_full[ps], pp, p.err)))
-          return false;
-        if (work) {
-#pragma unroll
-          for (int c = 0; c < 2 * NH; ++c)
-            q[c] = *reinterpret_cast<const uint4*>(p_src + ps * kPkStage + (NH == 2 ? c : 2 * grp + c) * 2048);
-        }
-        return true;
-      };
-      auto free_packed = [&]() {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_empty[ps]);
-        ps += NH;
-        if (ps >= C::SP) {
-          ps -= C::SP;
-          pp ^= 1u;
-        }
-      };
+      // One unit ahead: the next unit's packed chunks, codes and scale are on their way while this
+      // unit's entries are made, each loaded where the one before has been used up.
+      // (rows past V are padded, in cs as in the codes)
+      const int64_t G = p.h.D >> p.g_shift;
+      const uint32_t* cs_at = p.cs + ua * kUnit + s;
+      const uint8_t* code_at = p.h.r_code + (ua * kUnit + s) * G + (col >> p.g_shift);
+      uint32_t codes = 0, cs = 0;
       if (CPC != 0 && ua < it.u1) {
-        if (!take_packed(false)) {
-          ok = false;
-          break;
-        }
-        free_packed();
+        codes = load_codes<CPC>(code_at);
+        cs = load_word(cs_at);
+      }
+      const int64_t tile = (p.h.D >> 7) << 13;  // bytes of a 128-row tile
+      const uint8_t* p_at = p.h.r_nib + ua * tile + ((col >> 7) << 13) + s * 16;
+      uint4 q[2 * NH];
+      if (CPC != 0 && ua < it.u1) {
+#pragma unroll
+        for (int c = 0; c < 2 * NH; ++c) q[c] = ldg_stream(p_at + (NH == 2 ? c : 2 * grp + c) * 2048);
       }
       for (int64_t u = ua; u < it.u1; u += NH) {
         const int64_t v = u * kUnit + s;
         const bool more = u + NH < it.u1;
         const bool w_ready = tc::mbar_test(&w_empty[slot], wp);
-        const bool p_ready = CPC != 0 && more && tc::mbar_test(&p_full[ps], pp);
-        const RowLoad now = r;
-        if (CPC != 0 && more) r = load_grad_row<CPC>(p, v + NH * kUnit, col);
+        const uint32_t now = codes, now_cs = cs;
+        if (CPC != 0 && more) {
+          code_at += NH * kUnit * G;
+          cs_at += NH * kUnit;
+          p_at += NH * tile;
+          codes = load_codes<CPC>(code_at);
+          cs = load_word(cs_at);
+        }
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
           const int ch = NH == 2 ? hh : grp;  // half of the block's chunks
@@ -596,8 +587,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
             if (work) {
 #pragma unroll
               for (int wn = 0; wn < 4; ++wn) {  // window of 32 columns
-                const uint32_t cw = CPC == 1 ? now.code : (CPC == 2 ? (now.code >> (8 * (wn >> 1))) & 0xFFu : (now.code >> (8 * wn)) & 0xFFu);
-                const __half2 c2 = __float2half2_rn((float)cw * now.cs);  // exact for k <= 24
+                const __half2 c2 = code_half2(now, CPC == 1 ? 0 : (CPC == 2 ? wn >> 1 : wn), now_cs);
                 const __half2 nc24 = __hmul2(c2, __float2half2_rn(-24.f));
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {  // columns 32 wn + 16 ch + 8 c .. + 7
@@ -610,7 +600,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
                 }
               }
             }
-            if (hh == NH - 1 && more && !take_packed(p_ready)) ok = false;
+            if (more) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                q[2 * hh + c] = ldg_stream(p_at + (NH == 2 ? 2 * hh + c : 2 * grp + c) * 2048);
+            }
           } else if (work) {  // INT8 rows straight from global memory
             const uint4* src = reinterpret_cast<const uint4*>(p.h.r_nib + v * p.h.D + col) + 4 * ch;
 #pragma unroll
@@ -626,24 +620,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
               !__all_sync(0xffffffffu, tc::mbar_wait(&w_empty[slot], wp, p.err)))
             ok = false;
           if (!ok) break;
-          const uint32_t dst = w_row + slot * kWStage;
-          // where the chunk of columns 32 wn + 16 ch + 8 c lies in its 128-byte row (wn even, c = 0)
-          const uint32_t at0 = (uint32_t)((2 * ch) ^ x7) << 4;
           if (work) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              // SC4: window c / 2, chunk 4 (c / 2 % 2) + 2 ch + c % 2 of its 64-column atom; INT8: the
-              // atom ch, chunk c
-              const uint32_t at = CPC != 0 ? (c >> 2) * 4096 + (at0 ^ (uint32_t)((((c >> 1) & 1) * 4 + (c & 1)) << 4))
-                                           : ch * 4096 + (uint32_t)((c ^ x7) << 4);
-              st_shared16(dst + at, o[c][0], o[c][1], o[c][2], o[c][3]);
+              // SC4: columns 32 (c / 2) + 16 ch + 8 (c % 2), a chunk of atom c / 4; INT8: chunk c of
+              // atom ch
+              const int atom = CPC != 0 ? c >> 2 : ch;
+              const int chunk = CPC != 0 ? ((c >> 1) & 1) * 4 + 2 * ch + (c & 1) : c;
+              st_shared16((w_addr ^ (uint32_t)(chunk << 4)) + atom * 4096, o[c][0], o[c][1], o[c][2], o[c][3]);
             }
           }
         }
         if (!ok) break;
         tc::fence_proxy_async_smem();  // the MMA reads the stage through the async proxy
-        if (CPC != 0 && more) free_packed();
-        else __syncwarp();
+        __syncwarp();
         if (lane == 0) tc::mbar_arrive(&w_full[slot]);
         wp ^= 1u;
         copied = false;
@@ -688,40 +678,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
       tc::mbar_arrive(acc_empty);
     }
   } else if (warp == kDequantWarps + 4) {
-    // ---- packed producer (one thread) ----
-    if (lane == 0 && CPC != 0) {
-      // Each group of dequantisation warps has its own part of the ring (slots g, g + NH, ...),
-      // filled with the units that are its by their place in this CTA's sequence.
-      constexpr int NH = 3 - MT, R = C::SP / NH;
-      const int64_t nkb = p.h.D >> 7;
-      int64_t np[NH] = {}, seq = 0;
-      bool ok = true;
-      for (int64_t i = 0; ok && grad_item<MT>(p, i, it); ++i) {
-        const uint32_t bytes = (uint32_t)it.cols * 64u;
-        for (int64_t u = it.u0; ok && !it.rank && u < it.u1; ++u) {
-          const int g = NH == 2 ? (int)((seq + (u - it.u0)) & 1) : 0;
-#pragma unroll
-          for (int k = 0; k < NH; ++k) {
-            if (k != g) continue;
-            const int ps = (int)(np[k] % R) * NH + k;
-            if (np[k] >= R && !tc::mbar_wait(&p_empty[ps], (uint32_t)(np[k] / R - 1) & 1u, p.err)) {
-              ok = false;
-              break;
-            }
-            tc::fence_proxy_async_smem();  // the stage was read with generic loads
-            tc::mbar_arrive_expect_tx(&p_full[ps], bytes);
-            tc::bulk_g2s(Ps + ps * kPkStage, p.h.r_nib + ((u * nkb + 2 * it.dt) << 13), bytes, &p_full[ps]);
-            ++np[k];
-          }
-        }
-        seq += it.u1 - it.u0;
-      }
-      if (!ok)
-        for (int k = 0; k < NH; ++k)
-          for (int64_t q = np[k] < R ? 0 : np[k] - R; q < np[k]; ++q)
-            tc::mbar_wait(&p_full[(q % R) * NH + k], (uint32_t)(q / R) & 1u, p.err);
-    }
-  } else if (warp == kDequantWarps + 5) {
     // ---- image producer (one thread); the image comes from the kernel before this one ----
     if (lane == 0) {
       grid_dependency_wait();
@@ -758,7 +714,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     // A step is 64 rows: two W stages and one image stage per accumulator.  Its barriers are
     // probed together, then one thread issues the step.  With MT = 2 issuer iw takes image tile iw
     // in every step, with MT = 1 the steps kk = iw mod 2.
-    const int iw = warp - (kDequantWarps + 6);
+    const int iw = warp - (kDequantWarps + 5);
     const uint64_t bdesc0 = desc_mn_sw128(tc::smem_u32(Ws), 4096, 1024);
     const uint64_t adesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Is));
     constexpr int R = C::SI / 2;  // this issuer's slots of the image ring: 2 j + iw
@@ -825,7 +781,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kDequantWarps + 6) {
+  if (warp == kDequantWarps + 5) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, 512);
   }
@@ -888,7 +844,7 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n0 + t < p.n && j < RR) {
       const float* q = p.part + (n0 + t) * p.dp + p.h.D + j;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < p.slabs; ++s) {
         const float4 x = __ldcs(reinterpret_cast<const float4*>(q + s * slab));
         a.x += x.x;
@@ -914,7 +870,7 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
       for (int c = 0; c < 4; ++c) a[c] = make_float2(0.f, 0.f);
       if (n < p.n) {
         const float* src = p.part + n * p.dp + d0 + 32 * w + 2 * q;
-#pragma unroll 2
+#pragma unroll(MT == 1 ? 8 : 2)
         for (int s = 0; s < p.slabs; ++s)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1010,16 +966,17 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   g.nunits = (h.V + kUnit - 1) / kUnit;
   g.dp = (h.D + RR + 3) / 4 * 4;
   // Slabs of the vocabulary: CTAs run items of equal length side by side, so the time is that of
-  // ceil(items / CTAs) rounds of 1 / slabs each, plus the partial sums' way through memory.
-  // Measured: about 1.2 us per unit of 128 rows with two accumulators, 0.7 us with one.
+  // ceil(items / CTAs) rounds, each of 1 / slabs of a tile's units and about 6 us for filling the
+  // pipeline and storing the sums, plus the sums' way through memory.  Measured: 1.6 us per unit
+  // of 128 rows with two accumulators, 0.9 us with one.
   const int64_t tiles = (int64_t)g.ntt * g.ntiles;
   const int64_t sms = sm_count();
   double best = 1e300;
   g.slabs = 1;
   for (int s = 1; s <= 64 && s * 4 <= g.nunits + 3; ++s) {
-    const double rounds = (double)((tiles * s + sms - 1) / sms) / s;
-    const double tile_us = g.nunits * (g.mt == 2 ? 1.2 : 0.7);
-    const double cost = rounds * tile_us + 8.0 * s * n * g.dp / 4e6;
+    const int64_t rounds = (tiles * s + sms - 1) / sms;
+    const double tile_us = g.nunits * (g.mt == 2 ? 1.6 : 0.9);
+    const double cost = rounds * (tile_us / s + 6.0) + 8.0 * s * n * g.dp / 4e6 + 0.3 * s;
     if (cost < best * 0.995) {
       best = cost;
       g.slabs = s;
@@ -1081,7 +1038,8 @@ cudaError_t launch_grad_it(const GradParams& p, cudaStream_t st) {
 
 struct GradParts {
   char *img, *fimg;
-  float *sp, *cs, *spmax, *tok, *part;
+  float *sp, *spmax, *tok, *part;
+  uint32_t* cs;
   float2* row;
   unsigned* amax;
   int* texp;
@@ -1092,7 +1050,7 @@ GradParts grad_parts(const HeadGrad& a, const GradPlan& g) {
   q.img = b + g.o_img;
   q.fimg = b + g.o_fimg;
   q.sp = reinterpret_cast<float*>(b + g.o_sp);
-  q.cs = reinterpret_cast<float*>(b + g.o_cs);
+  q.cs = reinterpret_cast<uint32_t*>(b + g.o_cs);
   q.spmax = reinterpret_cast<float*>(b + g.o_spmax);
   q.tok = reinterpret_cast<float*>(b + g.o_tok);
   q.part = reinterpret_cast<float*>(b + g.o_part);
