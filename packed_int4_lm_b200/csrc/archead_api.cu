@@ -364,7 +364,10 @@ int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, c
   __half* Hh = reinterpret_cast<__half*>(b + o_hh);
   float* tsc = reinterpret_cast<float*>(b + o_tsc);
   unsigned* cnt = reinterpret_cast<unsigned*>(b + o_cnt);
-  cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches);
+  // The rank products on the tensor cores once their tiles fill the SMs (N = 4096, ranks 32 + 32:
+  // 289 -> 39 us; N = 777, ranks 64 + 64: 113 -> 34 us; below 256 tokens the CUDA cores are
+  // as fast: 8 us at N = 64).
+  cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches, s.N > 256);
   if (e == cudaSuccess) {
     prof_mark(0, st);
     e = launch_residual_tc(Hh, tsc, head, s, plan, nullptr, nullptr, nullptr, nullptr,

@@ -163,6 +163,12 @@ cudaError_t launch_lowrank_t(const uint16_t* H, const archead_head* head, const 
                              float* t, __half* img, int nt, int64_t nkbt, unsigned* err,
                              cudaStream_t st, int* launches);
 
+// The same rank blocks from the image's FP16 H by warp MMAs (csrc/lowrank_mma.cu), for batches
+// large enough to fill the SMs with tiles of 32 tokens x 32 ranks.
+struct TcPlan;
+cudaError_t launch_lowrank_mma(const archead_head* head, const Shapes& s, const TcPlan& plan, __half* img,
+                               unsigned* err, cudaStream_t st, int* launches);
+
 // tcgen05 path.  The MMA's B operand is a blocked FP16 image of the tokens: per token tile
 // of nt rows, nkb = D / 128 blocks of H followed by nrb = ceil((r_c + r_r) / 32) rank
 // blocks, each nt x 128 FP16 (see tc_image_offset).  Rank block b holds, for the factor
@@ -187,11 +193,11 @@ __host__ __device__ __forceinline__ int64_t tc_image_offset(int64_t tt, int64_t 
 }
 // Blocked image of H (zero rows up to the token tile) and its rank blocks.
 // counters: ceil(V/128) words zeroed here (the per-tile counters of a split launch, or
-// the work counter of the dynamic item order), or nullptr.
+// the work counter of the dynamic item order), or nullptr.  rank_mma: launch_lowrank_mma.
 cudaError_t launch_prologue_blocked(const uint16_t* H, const archead_head* head,
                                     const Shapes& s, const TcPlan& plan, __half* Hb, float* tsc,
                                     unsigned* counters, unsigned* err, cudaStream_t st,
-                                    int* launches);
+                                    int* launches, bool rank_mma = false);
 // Bytes of scratch for a launch whose single token tile is split evenly over the CTAs
 // (0 when the shape has more than one token tile).
 size_t tc_split_scratch_bytes(const Shapes& s, const TcPlan& plan);

@@ -50,4 +50,12 @@ __device__ __forceinline__ void pow2_pair(int e, float* a, float* b) {
   *b = __int_as_float((e - h + 127) << 23);
 }
 
+// Two signed bytes of w (its bytes sel picks, offset by 128) as exact FP16: the half 1024 + 128 + b
+// has the low mantissa byte b ^ 0x80.
+__device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w_flipped), "r"(0x64646464u), "r"(sel));
+  return __hsub2(*reinterpret_cast<__half2*>(&r), __float2half2_rn(1152.f));
+}
+
 }  // namespace archead

@@ -406,14 +406,6 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
       : "memory");
 }
 
-// Two signed bytes of w (its bytes sel picks, offset by 128) as exact FP16: the half 1024 + 128 + b
-// has the low mantissa byte b ^ 0x80.
-__device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w_flipped), "r"(0x64646464u), "r"(sel));
-  return __hsub2(*reinterpret_cast<__half2*>(&r), __float2half2_rn(1152.f));
-}
-
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");

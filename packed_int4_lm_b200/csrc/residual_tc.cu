@@ -1072,7 +1072,7 @@ size_t tc_split_scratch_bytes(const Shapes& s, const TcPlan& plan) {
 cudaError_t launch_prologue_blocked(const uint16_t* H, const archead_head* head,
                                     const Shapes& s, const TcPlan& plan, __half* Hb, float* tsc,
                                     unsigned* counters, unsigned* err, cudaStream_t st,
-                                    int* launches) {
+                                    int* launches, bool rank_mma) {
   const int nt = plan.nt;
   const int64_t Npad = (s.N + nt - 1) / nt * nt;
   const int64_t nkbt = s.D / 128 + plan.nrb;
@@ -1082,6 +1082,7 @@ cudaError_t launch_prologue_blocked(const uint16_t* H, const archead_head* head,
   ++*launches;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (rank_mma) return launch_lowrank_mma(head, s, plan, Hb, err, st, launches);
   return launch_lowrank_t(H, head, s, nullptr, Hb, nt, nkbt, err, st, launches);
 }
 
