@@ -236,16 +236,16 @@ __global__ void __launch_bounds__(256) grad_targets_kernel(const TokensParams p)
       __float2half_rn(expm1f(-p.t.nll[n]) * a * p.sp[t] * b);
 }
 
-// One warp per 64 vocabulary rows and group of up to 32 tokens (`group`; fewer for small batches,
-// which would leave most SMs idle): each lane two rows, one 128-byte image row per token, four
-// tokens' loads in flight.
-template <bool kSoftmax, bool kPairs>
+// One warp per 128 vocabulary rows and group of up to 32 tokens (`group`; fewer for small batches,
+// which would leave most SMs idle): each lane four rows, two 128-byte image rows per token, four
+// tokens' loads in flight.  A group lies in one image tile.
+template <bool kSoftmax, bool kQuads>
 __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t nhb = (p.V + kUnit - 1) / kUnit * 2;
-  const int64_t hb = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int64_t nunits = (p.V + kUnit - 1) / kUnit;
+  const int64_t u = blockIdx.x * 8ll + (threadIdx.x >> 5);
   const int64_t n0 = (int64_t)blockIdx.y * p.group;
   const int es = spmax_exp(p.spmax);
   // this lane's token of the group: its factor 2^f and, for logits, lse, target and its entry
@@ -262,35 +262,38 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
       at = expm1f(-nll);
       if ((target < 0 || target >= p.V) && p.t.dnll[mine] != 0.f) {
         lse = __int_as_float(0x7fc00000);
-        if (hb == 0) atomicOr(p.err, kErrTarget);
+        if (u == 0) atomicOr(p.err, kErrTarget);
       }
     } else {
       f = dy_exp(p.amax[mine]);
     }
-    if (hb == 0) p.texp[mine] = es - f;  // within +-240
+    if (u == 0) p.texp[mine] = es - f;  // within +-240
   }
-  if (hb >= nhb) return;
-  const int64_t v = 64 * hb + 2 * lane;
-  float s0 = p.sp[v], s1 = p.sp[v + 1], e0, e1;
+  if (u >= nunits) return;
+  const int64_t v = kUnit * u + 4 * lane;
+  const float4 sp = *reinterpret_cast<const float4*>(p.sp + v);
+  float e0, e1;
   pow2_pair(-es, &e0, &e1);
-  s0 = s0 * e0 * e1;
-  s1 = s1 * e0 * e1;
+  const float s[4] = {sp.x * e0 * e1, sp.y * e0 * e1, sp.z * e0 * e1, sp.w * e0 * e1};
+  const int64_t tt = n0 / p.nt;
+  const int nn0 = (int)(n0 - tt * p.nt), r = 4 * (lane & 15);  // row in its half unit
+  char* dst = p.img + ((tt * 2 * nunits + 2 * u + (lane >> 4)) * p.nt + nn0) * 128 + 2 * (r & 7);
+  const float* src = p.src + n0 * p.V + v;
   for (int k0 = 0; k0 < p.group && n0 + k0 < p.npad; k0 += 4) {
-    float y0[4], y1[4];
+    float y[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t n = n0 + k0 + k;
-      const float* row = p.src + n * p.V + v;
-      y0[k] = y1[k] = 0.f;
-      if (kPairs) {
-        if (n < p.n && v < p.V) {
-          const float2 q = __ldcs(reinterpret_cast<const float2*>(row));
-          y0[k] = q.x;
-          y1[k] = q.y;
-        }
-      } else if (n < p.n) {
-        if (v < p.V) y0[k] = __ldcs(row);
-        if (v + 1 < p.V) y1[k] = __ldcs(row + 1);
+      const bool in = n0 + k0 + k < p.n;
+      const float* q = src + (k0 + k) * p.V;
+      if (kQuads) {
+        const float4 x = in && v < p.V ? __ldcs(reinterpret_cast<const float4*>(q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[k][0] = x.x;
+        y[k][1] = x.y;
+        y[k][2] = x.z;
+        y[k][3] = x.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[k][e] = in && v + e < p.V ? __ldcs(q + e) : 0.f;
       }
     }
 #pragma unroll
@@ -302,15 +305,20 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
       if (kSoftmax) {
         const float l = __shfl_sync(0xffffffffu, lse, k0 + k), z = __shfl_sync(0xffffffffu, at, k0 + k);
         const int64_t t = __shfl_sync(0xffffffffu, target, k0 + k);
-        y0[k] = v < p.V ? (v == t ? z : expf(y0[k] - l)) : 0.f;
-        y1[k] = v + 1 < p.V ? (v + 1 == t ? z : expf(y1[k] - l)) : 0.f;
-        if (l != l) y0[k] = y1[k] = l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[k][e] = v + e == t ? z : expf(y[k][e] - l);
+          if (v + e >= p.V || n >= p.n) y[k][e] = 0.f;
+          if (l != l) y[k][e] = l;
+        }
       }
       if (n >= p.npad) break;
-      const int64_t tt = n / p.nt;
-      const float x0 = n < p.n ? y0[k] * a * b * s0 : 0.f, x1 = n < p.n ? y1[k] * a * b * s1 : 0.f;
-      *reinterpret_cast<__half2*>(p.img + grad_image_offset(tt, hb, nhb, p.nt, (int)(n - tt * p.nt),
-                                                            2 * lane)) = __floats2half2_rn(x0, x1);
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = y[k][e] * a * (b * s[e]);
+      const int nn = nn0 + k0 + k;
+      *reinterpret_cast<uint2*>(dst + (k0 + k) * 128 + ((((r >> 3) ^ nn) & 7) << 4)) =
+          make_uint2(h2_bits(__floats2half2_rn(x[0], x[1])), h2_bits(__floats2half2_rn(x[2], x[3])));
     }
   }
 }
@@ -1061,16 +1069,16 @@ TokensParams tokens_params(const HeadGrad& a, const SoftmaxTokens& t) {
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  const int group = g.npad <= 64 ? 4 : (g.npad <= 256 ? 8 : 32);
+  const int group = g.npad <= 64 ? 4 : (g.npad <= 512 ? 8 : 32);  // (divides the image tile)
   const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, group, b.sp, b.spmax, b.amax,
                          t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
-  const dim3 grid((unsigned)((2 * g.nunits + 7) / 8), (unsigned)((g.npad + group - 1) / group));
-  const bool pairs = a.head->V % 2 == 0 && reinterpret_cast<uintptr_t>(src) % 8 == 0;
+  const dim3 grid((unsigned)((g.nunits + 7) / 8), (unsigned)((g.npad + group - 1) / group));
+  const bool quads = a.head->V % 4 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
   ++*a.launches;
   if (t)
-    return pairs ? launch_pdl(dy_image_kernel<true, true>, grid, 256, 0, a.st, p)
+    return quads ? launch_pdl(dy_image_kernel<true, true>, grid, 256, 0, a.st, p)
                  : launch_pdl(dy_image_kernel<true, false>, grid, 256, 0, a.st, p);
-  return pairs ? launch_pdl(dy_image_kernel<false, true>, grid, 256, 0, a.st, p)
+  return quads ? launch_pdl(dy_image_kernel<false, true>, grid, 256, 0, a.st, p)
                : launch_pdl(dy_image_kernel<false, false>, grid, 256, 0, a.st, p);
 }
 
