@@ -16,6 +16,8 @@
 // point (integer adds commute exactly).
 #include <math.h>
 
+#include <type_traits>
+
 #include "tc_common.cuh"
 
 namespace archead {
@@ -204,13 +206,18 @@ __device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, con
       x[k] = kValue && wf[k] != 0.f ? (double)wf[k] * ((double)b[k] - (double)a[k]) : 0.0;
     walk.piece(t0, t1, [&](int, int s, int lo, int hi, int b0, int b1) {
       Pair2 sum = {0.0, 0.0};
-      const bool whole = hi - lo == kPiece;
+      if (hi - lo == kPiece) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int t = token_at(t0, k);
-        if (whole || (t >= lo && t < hi)) {
+        for (int k = 0; k < kPer; ++k) {
           sum.w += (double)wf[k];
-          sum.x += x[k];
+          if (kValue) sum.x += x[k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const bool in = (unsigned)(token_at(t0, k) - lo) < (unsigned)(hi - lo);
+          sum.w += in ? (double)wf[k] : 0.0;
+          if (kValue) sum.x += in ? x[k] : 0.0;
         }
       }
       sum.w = warp_sum(sum.w);
@@ -251,20 +258,20 @@ __device__ __forceinline__ Pair2 seq_total(const SeqSums& q, const Seqs& sq, int
 
 // ---- policy loss ------------------------------------------------------------------------
 struct PolicyConst {
-  double log_hi, log_lo;    // log(1 + clip_high), log(1 - clip_low)
+  double log_hi, log_lo;     // log(1 + clip_high), log(1 - clip_low)
   float log_hi_f, log_lo_f;  // rounded
   float hi, lo;              // 1 + clip_high, 1 - clip_low
-  double kl_coef;
+  float kl_coef;
 };
 
 struct PolicyTok {
-  float sur, kl, grad;
+  float sur, kl, grad;  // sur: the surrogate's negative
   bool clipped;
 };
 
 __device__ __forceinline__ float exp_f(float x) {
   float y;  // e^x as 2^(x log2 e): off by about 2^-22 and 2^-24 |x|
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
   return y;
 }
 
@@ -285,28 +292,31 @@ __device__ __forceinline__ float kl_term(float z) {
   return fabsf(z) < 1.f ? z * z * p : exp_f(z) - 1.f - z;
 }
 
+// The side of the clip border is that of the exact difference old - nll against log(1 +- clip).
+// Rounding is monotone, so the rounded difference decides unless it equals the rounded border;
+// `border` then asks for the FP64 difference, which is exact (kExact).
+template <bool kExact>
 __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A, bool has_ref,
-                                                  float ref, const PolicyConst& k) {
-  // The side of the clip border is that of the exact difference old - nll against log(1 +- clip).
-  // Rounding is monotone, so the rounded difference decides unless it equals the rounded border;
-  // then the FP64 difference (exact) does.
+                                                  float ref, const PolicyConst& k, bool& border) {
   const float x = old - nll;
   const bool up = A > 0.f;
-  const float l = up ? k.log_hi_f : k.log_lo_f;
   PolicyTok o;
-  o.clipped = up ? x > l : A < 0.f && x < l;
-  if (x == l && A != 0.f) {
+  if (kExact) {
     const double d = (double)old - (double)nll;
-    o.clipped = up ? d > k.log_hi : d < k.log_lo;
+    o.clipped = up ? d > k.log_hi : A < 0.f && d < k.log_lo;
+  } else {
+    const float l = up ? k.log_hi_f : -k.log_lo_f, y = up ? x : -x;
+    o.clipped = y > l && A != 0.f;
+    border |= y == l;
   }
   const float r = A == 0.f ? 0.f : exp_f(x) * A;  // (0 times an infinite ratio is 0 here)
   o.grad = o.clipped ? 0.f : r;
-  o.sur = -(o.clipped ? (up ? k.hi : k.lo) * A : r);
+  o.sur = o.clipped ? (up ? k.hi : k.lo) * A : r;
   o.kl = 0.f;
   if (has_ref) {
     const float z = nll - ref;
     o.kl = kl_term(z);
-    o.grad = fmaf((float)k.kl_coef, z + o.kl, o.grad);  // e^z - 1 = z + k
+    o.grad = fmaf(k.kl_coef, z + o.kl, o.grad);  // e^z - 1 = z + k
   }
   return o;
 }
@@ -345,11 +355,18 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
       float g[kPer] = {};  // outside every sequence
       walk.piece(t0, t1, [&](int j, int, int lo, int hi, int, int) {
         const float fs = __shfl_sync(0xffffffffu, sc, j), as = __shfl_sync(0xffffffffu, adv, j);
-        const bool whole = hi - lo == kPiece;
+        if (hi - lo == kPiece) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) g[i] = fs;
+          if (a.adv_per_seq) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) A[i] = as;
+          }
+          return;
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int t = token_at(t0, i);
-          const bool in = whole || (t >= lo && t < hi);
+          const bool in = (unsigned)(token_at(t0, i) - lo) < (unsigned)(hi - lo);
           g[i] = in ? fs : g[i];
           A[i] = in && a.adv_per_seq ? as : A[i];
         }
@@ -363,19 +380,24 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
         f[i] = t >= first && t < last ? f[i] * (float)scale : 0.f;
       }
     }
-    float sur = 0.f, kl = 0.f, clipped = 0.f, g[kPer];
+    float sur, kl, clipped, g[kPer];
+    bool border = false;
+    auto tokens = [&](auto exact) {  // no branch on the weight: eight chains side by side
+      sur = kl = clipped = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {  // no branch on the weight: eight chains side by side
-      const bool on = f[i] != 0.f;
-      const PolicyTok o = policy_token(on ? nll[i] : 0.f, on ? old[i] : 0.f, on ? A[i] : 0.f, a.nll_ref != nullptr,
-                                       on ? ref[i] : 0.f, k);
-      sur = fmaf(f[i], o.sur, sur);
-      kl = fmaf(f[i], o.kl, kl);
-      clipped += o.clipped ? f[i] : 0.f;
-      g[i] = f[i] * o.grad;
-    }
+      for (int i = 0; i < kPer; ++i) {
+        const PolicyTok o = policy_token<decltype(exact)::value>(nll[i], old[i], A[i], a.nll_ref != nullptr, ref[i], k, border);
+        const bool on = f[i] != 0.f;  // a masked token may hold anything
+        sur += on ? f[i] * o.sur : 0.f;
+        kl += on ? f[i] * o.kl : 0.f;
+        clipped += on && o.clipped ? f[i] : 0.f;
+        g[i] = on ? f[i] * o.grad : 0.f;
+      }
+    };
+    tokens(std::false_type());
+    if (__any_sync(0xffffffffu, border)) tokens(std::true_type());
     store_piece(a.dnll, t0, t1, vec, g);
-    sum.sur += (double)sur;
+    sum.sur -= (double)sur;
     sum.kl += (double)kl;
     sum.clipped += (double)clipped;
   }
@@ -528,12 +550,12 @@ __global__ void __launch_bounds__(1024) policy_small_kernel(PolicyArgs a, Policy
   s.sur = block_sum(s.sur, red);
   s.kl = block_sum(s.kl, red);
   s.clipped = block_sum(s.clipped, red);
-  if (threadIdx.x == 0) policy_stats(a.stats, s, k.kl_coef);
+  if (threadIdx.x == 0) policy_stats(a.stats, s, a.kl_coef);
 }
 
 PolicyConst policy_const(const PolicyArgs& a) {
   const double hi = log1p(a.clip_high), lo = log1p(-a.clip_low);
-  return {hi, lo, (float)hi, (float)lo, (float)(1.0 + a.clip_high), (float)(1.0 - a.clip_low), a.kl_coef};
+  return {hi, lo, (float)hi, (float)lo, (float)(1.0 + a.clip_high), (float)(1.0 - a.clip_low), (float)a.kl_coef};
 }
 
 int64_t piece_count(int64_t N) { return (N + kPiece - 1) / kPiece; }
@@ -686,8 +708,8 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int t = token_at(t0, i);
-        if (t >= lo && t < hi && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
+        const bool in = (unsigned)(token_at(t0, i) - lo) < (unsigned)(hi - lo);
+        if (in && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
       }
     });
     store_piece(a.dnll, t0, t1, vec, g);
@@ -788,7 +810,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err
   double* inv = nullptr;
   cudaError_t e = cudaSuccess;
   if (a.reduction == ARCHEAD_REDUCE_TOKEN) {
-    nt = nb < 148 ? nb : 148;
+    nt = nb;
     policy_weight_kernel<<<nt, 256, 0, st>>>(a, total, err);
     ++*launches;
     e = cudaGetLastError();
