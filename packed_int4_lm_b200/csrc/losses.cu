@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(256) policy_weight_kernel(PolicyArgs a, double
 }
 
 // total: partial sums (n of them) of what the common factor divides by; nullptr: the factor is 1.
-__global__ void __launch_bounds__(256, 4) policy_token_kernel(PolicyArgs a, PolicyConst k, const double* inv,
+__global__ void __launch_bounds__(256, 3) policy_token_kernel(PolicyArgs a, PolicyConst k, const double* inv,
                                                            const double* total, int n, PolicySums* part,
                                                            unsigned* err) {
   allow_dependent_launch();
@@ -805,7 +805,8 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err
   double* total = reinterpret_cast<double*>(b);
   b += up256(kMaxBlocks * 8);
   const int64_t pb = (piece_count(a.N) + 7) / 8;
-  const int nb = capped(pb);  // blocks of the token kernels
+  // blocks of the token kernels (three per SM: the tokens in flight take 80 registers)
+  const int nb = capped(pb) < 148 * 3 ? capped(pb) : 148 * 3;
   int nt = 0;
   double* inv = nullptr;
   cudaError_t e = cudaSuccess;
