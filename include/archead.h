@@ -377,7 +377,7 @@ int archead_abi_version(void);
 
 /*
  * archead_last_launches -- number of kernels the library launched during the most recent
- * successful archead_logits / archead_nll call on this host thread (for launch counting).
+ * successful call on this host thread (for launch counting).
  */
 int archead_last_launches(void);
 

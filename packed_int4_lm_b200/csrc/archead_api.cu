@@ -368,13 +368,10 @@ int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, c
   // 289 -> 39 us; N = 777, ranks 64 + 64: 113 -> 34 us; below 256 tokens the CUDA cores are
   // as fast: 8 us at N = 64).
   cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches, s.N > 256);
-  if (e == cudaSuccess) {
-    prof_mark(0, st);
+  if (e == cudaSuccess)
     e = launch_residual_tc(Hh, tsc, head, s, plan, nullptr, nullptr, nullptr, nullptr,
                            split_bytes ? reinterpret_cast<float*>(b + o_scr) : nullptr, cnt,
                            ds->err, st, launches, &image);
-    prof_mark(1, st);
-  }
   cudaFreeAsync(base, st);
   return e == cudaSuccess ? ARCHEAD_OK : ARCHEAD_ERR_CUDA;
 }

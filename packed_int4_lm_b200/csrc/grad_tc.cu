@@ -860,6 +860,16 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, gr = lane >> 2, q = lane & 3;
   float acc[MT][4][4];
+  int ex[MT][2];  // the rows' exponents and scales, needed last
+  float sc[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int hrow = 0; hrow < 2; ++hrow) {
+      const int64_t n = n0 + 16 * m + 8 * hrow + gr;
+      ex[m][hrow] = n < p.n ? p.texp[n] : 0;
+      sc[m][hrow] = n < p.n && p.rowscale ? p.rowscale[n] : 1.f;
+    }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -920,14 +930,14 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
     for (int hrow = 0; hrow < 2; ++hrow) {
       const int64_t n = n0 + 16 * m + 8 * hrow + gr;
       if (n >= p.n) continue;
-      const float sc = p.rowscale ? p.rowscale[n] : 1.f;
+      const float f = sc[m][hrow];
       float e0, e1;
-      pow2_pair(p.texp[n], &e0, &e1);
+      pow2_pair(ex[m][hrow], &e0, &e1);
       __nv_bfloat16* dst = p.dH + n * p.h.D + d0 + 32 * w + 2 * q;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float x = acc[m][c][2 * hrow] * e0 * e1 * sc, y = acc[m][c][2 * hrow + 1] * e0 * e1 * sc;
-        *reinterpret_cast<__nv_bfloat162*>(dst + 8 * c) = __floats2bfloat162_rn(sc == 0.f ? 0.f : x, sc == 0.f ? 0.f : y);
+        const float x = acc[m][c][2 * hrow] * e0 * e1 * f, y = acc[m][c][2 * hrow + 1] * e0 * e1 * f;
+        *reinterpret_cast<__nv_bfloat162*>(dst + 8 * c) = __floats2bfloat162_rn(f == 0.f ? 0.f : x, f == 0.f ? 0.f : y);
       }
     }
 }
@@ -974,6 +984,7 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   double best = 1e300;
   g.slabs = 1;
   for (int s = 1; s <= 64 && s * 4 <= g.nunits + 3; ++s) {
+    if (s > 1 && 4.0 * s * n * g.dp > 1e9) break;  // (scratch)
     const int64_t rounds = (tiles * s + sms - 1) / sms;
     const double tile_us = g.nunits * (g.mt == 2 ? 1.6 : 0.9);
     const double cost = rounds * (tile_us / s + 6.0) + 8.0 * s * n * g.dp / 4e6 + 0.3 * s;

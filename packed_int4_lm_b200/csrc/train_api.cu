@@ -14,13 +14,14 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Tokens per chunk of the gradients: about 2 GB of scratch for the FP16 image (and FP32 logits,
-// where those go through memory), whole token tiles of the product where that allows, and at
-// most 65536 (the kernels' grids).
+// where those go through memory) and the product's sums, at most 65536 (the kernels' grids), and
+// chunks of about equal size, whole token tiles of the product where that allows.
 constexpr int64_t kChunkBytes = 2ll << 30;
 
-int64_t grad_chunk(int64_t N, int64_t V, int bytes) {
-  const int64_t c = std::min<int64_t>(std::max<int64_t>(kChunkBytes / (V * bytes), 1), 65536);
-  return std::min(N, c >= 256 ? c / 256 * 256 : c);
+int64_t grad_chunk(int64_t N, int64_t V, int64_t D, int bytes) {
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(kChunkBytes / (V * bytes + 8 * D), 1), 65536);
+  const int64_t even = (N + (N + most - 1) / most - 1) / ((N + most - 1) / most);
+  return std::min(N, even >= 256 ? std::min((even + 255) / 256 * 256, most) : even);
 }
 // The last chunk is shorter and may be split otherwise.
 size_t chunk_scratch(const archead_head* head, int64_t N, int64_t chunk) {
@@ -70,20 +71,21 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
       !aligned(lse, 4) || !aligned(dnll, 4))
     return ARCHEAD_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // the tcgen05 kernel writes the image itself; the others leave logits in memory
-  Shapes s = {N, V, D, r_c, r_r, g};
-  const bool fused = tc_image_fits(head, s);
-  const int64_t chunk = grad_chunk(N, V, fused ? 2 : 6);
-  const size_t yb = fused ? 0 : (size_t)chunk * V * 4, yoff = (yb + 255) / 256 * 256;
+  // The tcgen05 kernel writes the image itself; the others leave logits in memory.  A short last
+  // chunk may run on another kernel than the ones before it.
+  auto fused = [&](int64_t n) { return tc_image_fits(head, Shapes{n, V, D, r_c, r_r, g}); };
+  const int64_t chunk = grad_chunk(N, V, D, fused(N) ? 2 : 6);
+  const int64_t yrows = std::max(fused(chunk) ? 0 : chunk, N % chunk && !fused(N % chunk) ? N % chunk : 0);
+  const size_t yoff = ((size_t)yrows * V * 4 + 255) / 256 * 256;
   return with_scratch(yoff + chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
     float* Y = reinterpret_cast<float*>(b);
     for (int64_t n0 = 0; n0 < N; n0 += chunk) {
-      s.N = std::min(chunk, N - n0);
+      const Shapes s = {std::min(chunk, N - n0), V, D, r_c, r_r, g};
       const HeadGrad a = {head, s.N, b + yoff, err, st, launches};
       const SoftmaxTokens t = {targets + n0, nll + n0, lse + n0, dnll + n0};
       if (grad_rows(a, false) != cudaSuccess) return static_cast<int>(ARCHEAD_ERR_CUDA);
-      if (fused && tc_image_fits(head, s)) {
+      if (fused(s.N)) {
         TcImage image;
         if (grad_tokens(a, t, &image) != cudaSuccess)
           return static_cast<int>(ARCHEAD_ERR_CUDA);
@@ -115,7 +117,7 @@ int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH,
   if (!dY || !dH) return ARCHEAD_ERR_NULLPTR;
   if (!aligned(dY, 4) || !aligned(dH, 16)) return ARCHEAD_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t chunk = grad_chunk(N, V, 2);
+  const int64_t chunk = grad_chunk(N, V, D, 2);
   return with_scratch(chunk_scratch(head, N, chunk), st,
                       [&](char* b, unsigned* err, int* launches) {
     for (int64_t n0 = 0; n0 < N; n0 += chunk) {

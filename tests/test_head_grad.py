@@ -349,6 +349,79 @@ def test_training_step_of_the_operators_together(cuda_ok, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("extra", [5, 40])
+def test_batches_beyond_one_chunk(cuda_ok, extra):
+    """More tokens than one pass takes (65536), with a last pass of another size, which may run on
+    another kernel: rows of the first, the middle and the last tokens against FP64."""
+    head, W, M = head_of("no ranks")
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    V, D = head["V"], head["D"]
+    N = 2 * 65536 + extra
+    rows = np.r_[0:6, 65530:65542, N - extra - 3:N]
+    H = make_hidden(N, make_channel_scales(D, 0.5, 4, 20.0, 1), 2)
+    t = make_targets(N, V, 3).cuda()
+    Hd = H.cuda()
+    nl, ls = ah.nll_lse(Hd, dh, t)
+    dn = torch.linspace(-1, 1, N, device="cuda")
+    got = ah.nll_grad(Hd, dh, t, nl, ls, dn)[torch.from_numpy(rows).cuda()]
+    ah.check()
+    Y = oracle.logits(head, bf16_bits(H[rows]))
+    m = Y.max(1)
+    lse = m + np.log(np.exp(Y - m[:, None]).sum(1))
+    P = np.exp(Y - lse[:, None])
+    at = t.cpu().numpy()[rows]
+    P[np.arange(len(rows)), at] = np.expm1(Y[np.arange(len(rows)), at] - lse)
+    d = dn.cpu().numpy()[rows]
+    want = d.astype(np.float64)[:, None] * (P @ W)
+    close(got, want, nll_tol(head, P, Y, M, d, want), "nll_grad")
+    dY = torch.randn(N, V, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    got = ah.logits_grad(dY, dh)[torch.from_numpy(rows).cuda()]
+    ah.check()
+    y = dY[torch.from_numpy(rows).cuda()].cpu().numpy()
+    want = y.astype(np.float64) @ W
+    close(got, want, BF16 * np.abs(want) + PROD * (np.abs(y).astype(np.float64) @ M) + smallest_step(head, M, y))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [3, 140])
+def test_dY_aligned_to_four_bytes_only(cuda_ok, N):
+    head, W, M = head_of("g64")
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    dY = torch.from_numpy(make_dY(N, head["V"], 8)).cuda()
+    buf = torch.empty(N * head["V"] + 1, device="cuda")
+    off = buf[1:].view(N, head["V"])
+    off.copy_(dY)
+    assert off.data_ptr() % 16 == 4
+    assert torch.equal(ah.logits_grad(off, dh), ah.logits_grad(dY, dh))
+    ah.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [5, 60, 300])
+def test_negative_super_scales_and_rows_of_zeros(cuda_ok, N):
+    """The format allows a negative super-scale; rows of nothing (no residual, zero factors)."""
+    head = make_head(700, 256, 16, 16, 64, seed=5)
+    head["r_super"][::3] |= 0x8000
+    head["r_super"][7:40] = 0
+    head["sAc"][20:30] = 0
+    head["sAw"][20:40] = 0
+    W, M = magnitudes(head)
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    dY = make_dY(N, 700, 4)
+    got = ah.logits_grad(torch.from_numpy(dY).cuda(), dh)
+    want = dY.astype(np.float64) @ W
+    pos = {**head, "r_super": head["r_super"] & np.uint16(0x7FFF)}
+    close(got, want, BF16 * np.abs(want) + PROD * (np.abs(dY).astype(np.float64) @ M) + smallest_step(pos, M, dY))
+    H, tg, Y, lse, P, dnll = nll_case(head, W, N, 9)
+    Hd, t = H.cuda(), torch.from_numpy(tg).cuda()
+    nl, ls = ah.nll_lse(Hd, dh, t)
+    got = ah.nll_grad(Hd, dh, t, nl, ls, torch.from_numpy(dnll).cuda())
+    ah.check()
+    want = dnll.astype(np.float64)[:, None] * (P @ W)
+    close(got, want, nll_tol(pos, P, Y, M, dnll, want))
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once(cuda_ok):
     """Calls in flight on two streams do not share scratch."""
     head, W, M = head_of("g128")

@@ -374,6 +374,55 @@ def test_losses_repeat_bit_for_bit_and_under_a_graph(cuda_ok, lens):
     ah.check()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", ["piece edges", "many", "one long"])
+def test_arrays_aligned_to_four_bytes_only(cuda_ok, lens):
+    """The same values at an address that is no multiple of 16 give the same bits."""
+    cu = offsets(LENS[lens])
+    N, B = int(cu[-1]), len(cu) - 1
+    nll, old, ref, w, rng = make_tokens(N, 14)
+    adv = rng.normal(size=N).astype(np.float32)
+    d = cu_dev(nll, old, adv, ref, w, cu, make_pairs(B, 40, rng))
+
+    def moved(t):
+        b = torch.empty(t.numel() + 1, device="cuda")
+        b[1:] = t
+        assert b[1:].data_ptr() % 16 == 4
+        return b[1:]
+
+    def both(nll, old, adv, ref, w):
+        a = ah.policy_loss(nll, old, adv, nll_ref=ref, weights=w, cu_seqlens=d[5], kl_coef=0.1,
+                           reduction="sequence")
+        return [*a.values(), *ah.preference_loss(nll, d[5], d[6], nll_ref=ref, weights=w).values()]
+
+    for a, b in zip(both(*d[:5]), both(*[moved(t) for t in d[:5]])):
+        assert torch.equal(a, b)
+    ah.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [600, 3000])
+def test_many_sequences_of_few_tokens(cuda_ok, B):
+    """More sequences than tokens, most of them empty, many at one place."""
+    rng = np.random.default_rng(B)
+    lens = np.where(rng.random(B) < 0.9, 0, rng.integers(1, 4, size=B))
+    lens[100:400] = 0
+    cu = offsets(lens)
+    N = int(cu[-1])
+    nll, old, ref, w, rng = make_tokens(N, 15)
+    adv = rng.normal(size=B).astype(np.float32)
+    want = policy_ref(nll, old, adv, ref, w, cu, True, reduction="sequence", beta=0.1)
+    pairs = make_pairs(B, 2000, rng)
+    wantp = preference_ref(nll, cu, pairs, ref, w, 0.3, average=True)
+    d = cu_dev(nll, old, adv, ref, w, cu, pairs)
+    got = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], weights=d[4], cu_seqlens=d[5],
+                         per_sequence=True, kl_coef=0.1, reduction="sequence")
+    gotp = ah.preference_loss(d[0], d[5], d[6], nll_ref=d[3], weights=d[4], beta=0.3, average=True)
+    ah.check()
+    close(got["dnll"], want["dnll"], U * (want["size"] + np.abs(want["dnll"])), "policy")
+    close(gotp["dnll"], wantp["dnll"], U * np.abs(wantp["dnll"]) + 1e-12 * wantp["size"], "preference")
+
+
 # ---- refusals (host) --------------------------------------------------------------------
 @pytest.fixture(scope="module")
 def L():
