@@ -337,6 +337,8 @@ int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err) {
 
 void set_last_launches(int n) { t_last_launches = n; }
 
+constexpr int64_t kWideTiles = 148;
+
 // N <= 16 runs on the decode kernel, which writes logits
 bool tc_image_fits(const archead_head* head, const Shapes& s) {
   return head->format == ARCHEAD_FMT_SC4 && s.N > 16 && tc_plan(s, 2).nt > 0;
@@ -347,12 +349,16 @@ int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, c
   DeviceState* ds;
   const int rc = current_state(&ds);
   if (rc) return rc;
-  const TcPlan plan = tc_plan(s, 2);
+  TcPlan plan = tc_plan(s, 2);
+  // Tiles of 256 x 256 once they keep every SM busy for several rounds.
+  const int64_t tiles = ((s.V + 255) / 256) * ((s.N + 255) / 256);
+  const bool wide = image.nt == 128 && s.N > 128 && tiles >= kWideTiles;
+  if (wide) plan.nt = 128;
   const int64_t Npad = (s.N + plan.nt - 1) / plan.nt * plan.nt;
   Carve cv;
   const size_t o_hh = cv.take((size_t)Npad * (s.D + 128 * plan.nrb) * 2);
   const size_t o_tsc = cv.take((size_t)s.N * 4);
-  const size_t split_bytes = tc_split_scratch_bytes(s, plan);
+  const size_t split_bytes = wide ? 0 : tc_split_scratch_bytes(s, plan);
   const size_t o_scr = split_bytes ? cv.take(split_bytes) : 0;
   const size_t o_cnt = cv.take((size_t)((s.V + 127) / 128) * 4);
   void* base = nullptr;
@@ -368,7 +374,9 @@ int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, c
   // 289 -> 39 us; N = 777, ranks 64 + 64: 113 -> 34 us; below 256 tokens the CUDA cores are
   // as fast: 8 us at N = 64).
   cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches, s.N > 256);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && wide)
+    e = launch_softmax_tc(Hh, tsc, head, s, image, ds->err, st, launches);
+  else if (e == cudaSuccess)
     e = launch_residual_tc(Hh, tsc, head, s, plan, nullptr, nullptr, nullptr, nullptr,
                            split_bytes ? reinterpret_cast<float*>(b + o_scr) : nullptr, cnt,
                            ds->err, st, launches, &image);

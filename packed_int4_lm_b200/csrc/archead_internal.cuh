@@ -209,11 +209,13 @@ size_t tc_split_scratch_bytes(const Shapes& s, const TcPlan& plan);
 // image != nullptr: the softmax gradient's FP16 image instead (see grad_common.cuh).
 struct TcImage {
   char* img;
-  // per vocabulary row (padded to 128): log2 |S'_v 2^-es| (-infinity for 0 and past V) and the
+  // per vocabulary row (padded to 128): log2 |S'_v| (-infinity for 0 and past V) and the
   // FP16x2 sign bits of S'_v
   const float2* row;
-  const float* tok;  // per token: f - lse log2 e (NaN: its target is invalid)
+  const float* tok;  // per token: f - es - lse log2 e (NaN: its target is invalid)
   int nt;            // token tile of the image
+  const float* sp;     // per row S'_v
+  const uint32_t* cs;  // per row the residual's 2^-k, FP16x2
 };
 cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead_head* head,
                                const Shapes& s, const TcPlan& plan, float* Y,
@@ -221,6 +223,12 @@ cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead
                                float2* part, float* tlogit, float* scratch, unsigned* counters,
                                unsigned* err, cudaStream_t st, int* launches,
                                const TcImage* image = nullptr);
+
+// The image of a large batch by tiles of 256 tokens x 256 rows (csrc/softmax_tc.cu; image.nt = 128,
+// himg the blocked image with token tiles of 128).
+cudaError_t launch_softmax_tc(const __half* himg, const float* tsc, const archead_head* head,
+                              const Shapes& s, const TcImage& image, unsigned* err,
+                              cudaStream_t st, int* launches);
 
 // Decode path (N <= 16): persistent bulk-copy-fed warp-MMA kernel with H resident in
 // shared memory.  nt8 = 0 when the shape does not fit (then the token-block kernel runs).

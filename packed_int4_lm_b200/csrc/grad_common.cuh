@@ -1,8 +1,8 @@
 // Shared by the kernels of the gradient product (grad_tc.cu) and those that write its operand
-// image: the per-row scale and the image's layout.
+// image: the per-row scale, the image's layout, and pieces of their tcgen05 pipelines.
 #pragma once
 
-#include "archead_internal.cuh"
+#include "tc_common.cuh"
 
 namespace archead {
 
@@ -56,6 +56,67 @@ __device__ __forceinline__ __half2 bytes_to_half2(uint32_t w_flipped, uint32_t s
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(w_flipped), "r"(0x64646464u), "r"(sel));
   return __hsub2(*reinterpret_cast<__half2*>(&r), __float2half2_rn(1152.f));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, one M=128 x N x K=16 step, issued by one thread.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// mbar_wait for a wait of many microseconds: sleeps between polls, which would otherwise take
+// issue slots and power from the warps that work.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > (1ll << 31)) {
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+    __nanosleep(200);
+  }
+  return true;
+}
+
+// The code bytes (CPC of them) of one vocabulary row for one block of 128 columns, and its word of
+// the row table.  Volatile: issued here, an iteration before their use (the compiler would move
+// plain loads down to it, where they cost a round trip to memory per unit).
+template <int CPC>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* c) {
+  uint32_t r;
+  if (CPC == 1) asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(c));
+  else if (CPC == 2) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(r) : "l"(c));  // (zero-extended)
+  else asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t load_word(const uint32_t* c) {
+  uint32_t r;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
+  return r;
+}
+// Code e of them times 2^-k, twice in FP16 (exact for k <= 24): 1024 + c is a half with the byte c
+// in its low mantissa bits.
+__device__ __forceinline__ __half2 code_half2(uint32_t codes, int e, uint32_t cs) {
+  const uint32_t r = __byte_perm(codes, 0x64646464u, 0x4040u + 0x0101u * e);
+  return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(1024.f)),
+                 *reinterpret_cast<const __half2*>(&cs));
 }
 
 }  // namespace archead

@@ -21,7 +21,6 @@
 //  * grad_finish_kernel: adds the slabs in order, adds u b, scales and rounds to BF16.
 // Nothing is accumulated in memory, so equal calls give equal bits.
 #include "grad_common.cuh"
-#include "tc_common.cuh"
 
 namespace archead {
 namespace {
@@ -401,61 +400,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead,
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, one M=128 x N x K=16 step, issued by one thread.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
-
-// mbar_wait for a wait of many microseconds: sleeps between polls, which would otherwise take
-// issue slots and power from the warps that work.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!tc::mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > (1ll << 31)) {
-      atomicOr(err, kErrTimeout);
-      return false;
-    }
-    __nanosleep(200);
-  }
-  return true;
-}
-
-// The code bytes (CPC of them) of one vocabulary row for one block of 128 columns, and its word of
-// the row table.  Volatile: issued here, an iteration before their use (the compiler would move
-// plain loads down to it, where they cost a round trip to memory per unit).
-template <int CPC>
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* c) {
-  uint32_t r;
-  if (CPC == 1) asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(c));
-  else if (CPC == 2) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(r) : "l"(c));  // (zero-extended)
-  else asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t load_word(const uint32_t* c) {
-  uint32_t r;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
-  return r;
-}
-// Code e of them times 2^-k, twice in FP16 (exact for k <= 24): 1024 + c is a half with the byte c
-// in its low mantissa bits.
-__device__ __forceinline__ __half2 code_half2(uint32_t codes, int e, uint32_t cs) {
-  const uint32_t r = __byte_perm(codes, 0x64646464u, 0x4040u + 0x0101u * e);
-  return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(1024.f)),
-                 *reinterpret_cast<const __half2*>(&cs));
 }
 
 template <int IT, int MT, int CPC>
@@ -1123,7 +1067,8 @@ cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const Sof
 
 cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image) {
   const TokensParams p = tokens_params(a, t);
-  *image = TcImage{p.img, grad_parts(a, grad_plan(*a.head, a.n)).row, p.tok, p.nt};
+  const GradParts b = grad_parts(a, grad_plan(*a.head, a.n));
+  *image = TcImage{p.img, b.row, p.tok, p.nt, p.sp, b.cs};
   ++*a.launches;
   return launch_pdl(grad_tokens_kernel, dim3((unsigned)((a.n + 255) / 256)), 256, 0, a.st, p);
 }

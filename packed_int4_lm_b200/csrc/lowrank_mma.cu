@@ -8,7 +8,6 @@
 // ranks, a warp per 16 x 16 of them; 128 columns of both operands per stage of a cp.async ring.  The
 // operands are small (H once per 32 ranks), so the ring's latency bounds it.
 #include "grad_common.cuh"
-#include "tc_common.cuh"
 
 namespace archead {
 namespace {

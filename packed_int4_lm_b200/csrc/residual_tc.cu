@@ -45,7 +45,6 @@
 // Every mbarrier wait is bounded (about a second of SM cycles); a wait that gives up sets
 // the device error word, the CTA drains what it issued and frees its tensor memory.
 #include "grad_common.cuh"
-#include "tc_common.cuh"
 
 namespace archead {
 namespace {
@@ -291,12 +290,6 @@ __device__ __forceinline__ uint32_t factor_word(const TcParams& p, int64_t v, in
     w |= (uint32_t)(uint8_t)b << (8 * u);
   }
   return w;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* ptr) {

@@ -176,6 +176,38 @@ def test_nll_grad_matches_fp64(cuda_ok, name, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,N", [("g128", 2331), ("g64", 9500), ("g32 odd", 7700), ("g256 ranks 128", 9729),
+                                    ("core only", 38000), ("wide scales", 9600)])
+def test_nll_grad_of_large_batches(cuda_ok, name, N):
+    """Batches that run in tiles of 256 tokens x 256 rows, the last ones ragged: 240 of their
+    tokens, the last tile's among them, against FP64."""
+    head, W, M = head_of(name)
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    V, D = head["V"], head["D"]
+    rng = np.random.default_rng(N)
+    rows = np.unique(np.r_[rng.integers(0, N, size=160), N - 80:N])
+    H = make_hidden(N, make_channel_scales(D, 0.5, 4, 20.0, 1), 2)
+    tg = make_targets(N, V, 3).numpy()
+    dnll = rng.normal(size=N).astype(np.float32)
+    dnll[rows[::7]] = 0
+    t = torch.from_numpy(tg).cuda()
+    Hd = H.cuda()
+    nl, ls = ah.nll_lse(Hd, dh, t)
+    dn = torch.from_numpy(dnll).cuda()
+    got = ah.nll_grad(Hd, dh, t, nl, ls, dn)
+    ah.check()
+    assert torch.equal(got, ah.nll_grad(Hd, dh, t, nl, ls, dn))
+    Y = oracle.logits(head, bf16_bits(H[rows]))
+    m = Y.max(1)
+    lse = m + np.log(np.exp(Y - m[:, None]).sum(1))
+    P = np.exp(Y - lse[:, None])
+    at = (np.arange(len(rows)), tg[rows])
+    P[at] = np.expm1(Y[at] - lse)
+    want = dnll[rows].astype(np.float64)[:, None] * (P @ W)
+    close(got[torch.from_numpy(rows).cuda()], want, nll_tol(head, P, Y, M, dnll[rows], want), name)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [9, 40, 200])
 def test_nll_grad_of_confident_tokens(cuda_ok, N):
     """Targets whose probability is close to 1: the gradient is a small difference, which must
