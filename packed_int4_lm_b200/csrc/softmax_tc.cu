@@ -12,16 +12,16 @@
 //  * warps 0-15: lane = vocabulary row of a 32-row group; packed chunks from global memory into
 //    registers a unit (128 columns) ahead, exact FP16 entries into the two W stages of the unit;
 //    then the rank columns from the INT8 factors;
-//  * warps 16-19: epilogue, lane = token: one exp2 per entry with all scales in its exponent,
-//    eight entries per 16-byte store;
-//  * warp 20: bulk copies of the H image; warps 21, 22: MMA issuers, an accumulator each.
+//  * warps 16-23: epilogue, four per accumulator, lane = token: one exp2 per entry with all scales
+//    in its exponent, eight entries per 16-byte store;
+//  * warp 24: bulk copies of the H image; warps 25, 26: MMA issuers, an accumulator each.
 // Targets' entries are set afterwards (grad_targets).  Every wait is bounded.
 #include "grad_common.cuh"
 
 namespace archead {
 namespace {
 
-constexpr int kSmThreads = 32 * 23;
+constexpr int kSmThreads = 32 * 27;
 constexpr int kStage = 256 * 128;   // W stage: 256 rows x 64 columns FP16
 constexpr int kHStage = 128 * 128;  // image stage: 128 tokens x 64 columns FP16
 constexpr int kSW = 3, kSH = 8;     // 96 KB and 128 KB
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) softmax_tc_kernel(const Softmax
     }
     tc::mbar_fence_init();
   }
-  if (warp == 21) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == 25) tc::tmem_alloc(tmem_slot, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -217,65 +217,57 @@ __global__ void __launch_bounds__(kSmThreads, 1) softmax_tc_kernel(const Softmax
         }
       }
     }
-  } else if (warp < 20) {
+  } else if (warp < 24) {
     // ---- epilogue ----
-    const int e = threadIdx.x - 512;  // 0..127, lane of the accumulator
-    const uint32_t lane_off = (uint32_t)(32 * (warp - 16)) << 16;
+    // four warps per accumulator
+    const int m = (warp - 16) >> 2, e = (threadIdx.x - 512) & 127;  // e: lane of the accumulator
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const int64_t nhb = 2 * p.nvt;
     grid_dependency_wait();
     for (int64_t i = 0; sm_item(p, i, it); ++i) {
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the previous item's rows have been read
-      for (int k = e; k < 256; k += 128) {
+      asm volatile("bar.sync 3, 256;\n" ::: "memory");  // the previous item's rows have been read
+      {
+        const int k = threadIdx.x - 512;
         const int64_t v = 256 * it.vt + k;
         rows_s[k] = v < 128 * p.nvt ? make_float2(p.sp[v], p.out.row[v].x) : make_float2(0.f, 0.f);
       }
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      bool ok = true;
+      // one outcome for all eight warps: they share barriers
+      if (!tc::bar_and(3, 256, mbar_wait_long(&acc_full[m], (uint32_t)i & 1u, p.err))) break;
+      tc::fence_after_sync();
+      const int64_t tt = 2 * it.tp + m, n = tt * 128 + e;
+      const bool mine = m < it.m && n < p.n;
+      const float a = mine ? __ldg(p.tsc + n) * 1.44269504f : 0.f, b = mine ? __ldg(p.out.tok + n) : 0.f;
+      // 64 rows of the vocabulary are one 128-byte row of the image
+      char* dst = p.out.img + ((tt * nhb + 4 * it.vt) * 128 + e) * 128;
 #pragma unroll 1
-      for (int m = 0; m < 2; ++m) {
-        if (!tc::bar_and(1, 128, mbar_wait_long(&acc_full[m], (uint32_t)i & 1u, p.err))) {
-          ok = false;
-          break;
+      for (int c0 = 0; c0 < 256; c0 += 16) {
+        uint32_t y[16];
+        tc::tmem_ld16_nowait(tbase + 256 * m + lane_off + c0, y);
+        tc::tmem_wait_ld(y);
+        if (c0 == 240) {
+          tc::fence_before_sync();
+          tc::mbar_arrive(&acc_empty[m]);
         }
-        tc::fence_after_sync();
-        const int64_t tt = 2 * it.tp + m, n = tt * 128 + e;
-        const bool mine = m < it.m && n < p.n;
-        const float a = mine ? __ldg(p.tsc + n) * 1.44269504f : 0.f, b = mine ? __ldg(p.out.tok + n) : 0.f;
-        // 64 rows of the vocabulary are one 128-byte row of the image
-        char* dst = p.out.img + ((tt * nhb + 4 * it.vt) * 128 + e) * 128;
-#pragma unroll 1
-        for (int c0 = 0; c0 < 256; c0 += 32) {
-          uint32_t y[2][16];
-          tc::tmem_ld16_nowait(tbase + 256 * m + lane_off + c0, y[0]);
-          tc::tmem_ld16_nowait(tbase + 256 * m + lane_off + c0 + 16, y[1]);
-          tc::tmem_wait_ld(y[0]);
-          tc::tmem_wait_ld(y[1]);
-          if (c0 == 224) {
-            tc::fence_before_sync();
-            tc::mbar_arrive(&acc_empty[m]);
-          }
-          if (4 * it.vt + (c0 >> 6) >= nhb || m >= it.m) continue;  // (warp-uniform)
+        if (4 * it.vt + (c0 >> 6) >= nhb || m >= it.m) continue;  // (warp-uniform)
 #pragma unroll
-          for (int k8 = 0; k8 < 4; ++k8) {  // eight rows: one chunk
-            uint32_t o[4];
+        for (int k8 = 0; k8 < 2; ++k8) {  // eight rows: one chunk
+          uint32_t o[4];
 #pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) {
-              const int c = 8 * k8 + 2 * k2;
-              const float4 f = *reinterpret_cast<const float4*>(rows_s + c0 + c);  // S', log2 |S'| of two
-              const float x0 = exp2_approx(fmaf(__uint_as_float(y[c >> 4][c & 15]) * f.x, a, b + f.y));
-              const float x1 = exp2_approx(fmaf(__uint_as_float(y[c >> 4][(c & 15) + 1]) * f.z, a, b + f.w));
-              const uint32_t sign = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.z), 0x7030) & 0x80008000u;
-              o[k2] = h2_bits(__floats2half2_rn(x0, x1)) ^ sign;
-            }
-            const int chunk = ((c0 & 63) >> 3) + k8;
-            if (mine)
-              *reinterpret_cast<uint4*>(dst + (c0 >> 6) * kHStage + (((chunk ^ e) & 7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int k2 = 0; k2 < 4; ++k2) {
+            const int c = 8 * k8 + 2 * k2;
+            const float4 f = *reinterpret_cast<const float4*>(rows_s + c0 + c);  // S', log2 |S'| of two
+            const float x0 = exp2_approx(fmaf(__uint_as_float(y[c]) * f.x, a, b + f.y));
+            const float x1 = exp2_approx(fmaf(__uint_as_float(y[c + 1]) * f.z, a, b + f.w));
+            const uint32_t sign = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.z), 0x7030) & 0x80008000u;
+            o[k2] = h2_bits(__floats2half2_rn(x0, x1)) ^ sign;
           }
+          const int chunk = ((c0 & 63) >> 3) + k8;
+          if (mine)
+            *reinterpret_cast<uint4*>(dst + (c0 >> 6) * kHStage + (((chunk ^ e) & 7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      if (!ok) break;
     }
-  } else if (warp == 20) {
+  } else if (warp == 24) {
     // ---- H image producer (one thread): each accumulator has its half of the ring ----
     if (lane == 0) {
       grid_dependency_wait();
@@ -307,7 +299,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) softmax_tc_kernel(const Softmax
     }
   } else {
     // ---- MMA issuers ----
-    const int iw = warp - 21;
+    const int iw = warp - 25;
     const uint64_t bdesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Ws));
     const uint64_t adesc0 = tc::smem_desc_kmajor_sw128(tc::smem_u32(Hs));
     const uint32_t idesc = tc::idesc_f16_m128(256), d = tbase + 256 * iw;
@@ -363,7 +355,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) softmax_tc_kernel(const Softmax
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 21) {
+  if (warp == 25) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, 512);
   }
