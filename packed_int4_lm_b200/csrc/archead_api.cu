@@ -337,7 +337,11 @@ int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err) {
 
 void set_last_launches(int n) { t_last_launches = n; }
 
-constexpr int64_t kWideTiles = 148;
+// Tiles of 256 tokens x 256 rows from which on softmax_tc.cu is faster: two rounds of the SMs.
+// Measured on the 151936 x 4096 head, the whole archead_nll_grad: N = 160 551 against 603 us, N = 512
+// 1174 against 1230 us, N = 4096 8.46 against 9.12 ms; on 32000 x 2048 the two are equal up to N = 512
+// (250 tiles), 273 against 293 us at N = 600 (375).
+constexpr int64_t kWideTiles = 296;
 
 // N <= 16 runs on the decode kernel, which writes logits
 bool tc_image_fits(const archead_head* head, const Shapes& s) {
@@ -350,7 +354,6 @@ int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, c
   const int rc = current_state(&ds);
   if (rc) return rc;
   TcPlan plan = tc_plan(s, 2);
-  // Tiles of 256 x 256 once they keep every SM busy for several rounds.
   const int64_t tiles = ((s.V + 255) / 256) * ((s.N + 255) / 256);
   const bool wide = image.nt == 128 && s.N > 128 && tiles >= kWideTiles;
   if (wide) plan.nt = 128;

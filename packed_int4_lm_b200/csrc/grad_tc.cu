@@ -7,8 +7,8 @@
 // packed head is a transposed operand: D[n, d] = sum_v A[n, v] B[v, d] with A the FP16 image of
 // dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh; 128 tokens are the lanes of an accumulator)
 // and B the dequantised head, whose vocabulary rows are K and whose columns lie side by side
-// (MN-major).  The other way round, with the head as A, an instruction takes 128 cycles to read
-// its 128 columns however few tokens there are: N = 1 took 190 us against %N1% us.
+// (MN-major).  The other way round, with the head as A, few tokens take twice the instructions
+// (128 columns each against 256): N = 1 took 190 us against 165 us when both were built.
 // u is one more tile of columns, whose B, a / S', is prepared once per call in the layout of a W
 // stage and copied (built from the INT8 rows in the product's loop it took three times as long as
 // a residual tile and set the pace of every round: N = 777, ranks 64 + 64: 3150 us against 760 us).

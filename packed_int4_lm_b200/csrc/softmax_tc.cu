@@ -5,7 +5,9 @@
 // the same sums as the logits kernel of residual_tc.cu (residual columns q c 2^-k, rank columns as
 // FP16 pieces), with tiles of 256 tokens x 256 vocabulary rows: a dequantised weight serves 256
 // tokens there against 128, so half the dequantisation, and the tensor cores read 12 KB of shared
-// memory per 128 x 256 x 16 step.  N = 4096 on the 151936 x 4096 head: %FWD%.
+// memory per 128 x 256 x 16 step (that and the stores and copies, about 160 KB per step of 64
+// columns, are what bounds it: 1300 cycles against the MMAs' 1024).  N = 4096 on the 151936 x 4096
+// head: 3.67 ms against 4.28 ms (1405 against 1204 TFLOP/s).
 //
 // Persistent, one CTA per SM.  The tokens are the accumulators' lanes (A: the blocked FP16 image of
 // H, 128 tokens each, two accumulators), the vocabulary rows their columns (B, K-major).
