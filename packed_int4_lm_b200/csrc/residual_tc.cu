@@ -715,6 +715,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) residual_tc_kernel(const TcPara
     int cur_tt = -1;
     Item it;
     bool qok = true;
+    // the token scales (and the gradient's token and row tables) come from kernels before this one
+    grid_dependency_wait();
     // one outcome for all four epilogue warps: they share named barriers below
     for (int i = 0; tc::bar_and(1, 128, next_item(p, iq, i, it, qok, false)); ++i) {
       const int ab = i % C::NACC, use = i / C::NACC;
