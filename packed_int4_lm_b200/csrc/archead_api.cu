@@ -348,43 +348,52 @@ bool tc_image_fits(const archead_head* head, const Shapes& s) {
   return head->format == ARCHEAD_FMT_SC4 && s.N > 16 && tc_plan(s, 2).nt > 0;
 }
 
-int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, const TcImage& image,
-                 cudaStream_t st, int* launches) {
+int tc_image_begin(const uint16_t* H, const archead_head* head, const Shapes& s, int nt, cudaStream_t st,
+                   int* launches, TcImageRun* r) {
   DeviceState* ds;
   const int rc = current_state(&ds);
   if (rc) return rc;
-  TcPlan plan = tc_plan(s, 2);
+  r->plan = tc_plan(s, 2);
   const int64_t tiles = ((s.V + 255) / 256) * ((s.N + 255) / 256);
-  const bool wide = image.nt == 128 && s.N > 128 && tiles >= kWideTiles;
-  if (wide) plan.nt = 128;
-  const int64_t Npad = (s.N + plan.nt - 1) / plan.nt * plan.nt;
+  r->wide = nt == 128 && s.N > 128 && tiles >= kWideTiles;
+  if (r->wide) r->plan.nt = 128;
+  const int64_t Npad = (s.N + r->plan.nt - 1) / r->plan.nt * r->plan.nt;
   Carve cv;
-  const size_t o_hh = cv.take((size_t)Npad * (s.D + 128 * plan.nrb) * 2);
+  const size_t o_hh = cv.take((size_t)Npad * (s.D + 128 * r->plan.nrb) * 2);
   const size_t o_tsc = cv.take((size_t)s.N * 4);
-  const size_t split_bytes = wide ? 0 : tc_split_scratch_bytes(s, plan);
+  const size_t split_bytes = r->wide ? 0 : tc_split_scratch_bytes(s, r->plan);
   const size_t o_scr = split_bytes ? cv.take(split_bytes) : 0;
   const size_t o_cnt = cv.take((size_t)((s.V + 127) / 128) * 4);
-  void* base = nullptr;
-  if (cudaMallocFromPoolAsync(&base, cv.off, ds->pool, st) != cudaSuccess) {
+  if (cudaMallocFromPoolAsync(&r->base, cv.off, ds->pool, st) != cudaSuccess) {
     cudaGetLastError();
     return ARCHEAD_ERR_NOMEM;
   }
-  char* b = static_cast<char*>(base);
-  __half* Hh = reinterpret_cast<__half*>(b + o_hh);
-  float* tsc = reinterpret_cast<float*>(b + o_tsc);
-  unsigned* cnt = reinterpret_cast<unsigned*>(b + o_cnt);
+  char* b = static_cast<char*>(r->base);
+  r->himg = reinterpret_cast<__half*>(b + o_hh);
+  r->tsc = reinterpret_cast<float*>(b + o_tsc);
+  r->split = split_bytes ? reinterpret_cast<float*>(b + o_scr) : nullptr;
+  r->counters = reinterpret_cast<unsigned*>(b + o_cnt);
+  r->err = ds->err;
   // The rank products on the tensor cores once their tiles fill the SMs (N = 4096, ranks 32 + 32:
   // 289 -> 39 us; N = 777, ranks 64 + 64: 113 -> 34 us; below 256 tokens the CUDA cores are
   // as fast: 8 us at N = 64).
-  cudaError_t e = launch_prologue_blocked(H, head, s, plan, Hh, tsc, cnt, ds->err, st, launches, s.N > 256);
-  if (e == cudaSuccess && wide)
-    e = launch_softmax_tc(Hh, tsc, head, s, image, ds->err, st, launches);
-  else if (e == cudaSuccess)
-    e = launch_residual_tc(Hh, tsc, head, s, plan, nullptr, nullptr, nullptr, nullptr,
-                           split_bytes ? reinterpret_cast<float*>(b + o_scr) : nullptr, cnt,
-                           ds->err, st, launches, &image);
-  cudaFreeAsync(base, st);
-  return e == cudaSuccess ? ARCHEAD_OK : ARCHEAD_ERR_CUDA;
+  if (launch_prologue_blocked(H, head, s, r->plan, r->himg, r->tsc, r->counters, r->err, st, launches,
+                              s.N > 256) == cudaSuccess)
+    return ARCHEAD_OK;
+  cudaFreeAsync(r->base, st);
+  return ARCHEAD_ERR_CUDA;
+}
+
+int tc_image_end(const archead_head* head, const Shapes& s, const TcImage& image, cudaStream_t st,
+                 int* launches, const TcImageRun& r, int rc) {
+  if (rc == ARCHEAD_OK) {
+    const cudaError_t e = r.wide ? launch_softmax_tc(r.himg, r.tsc, head, s, image, r.err, st, launches)
+                                 : launch_residual_tc(r.himg, r.tsc, head, s, r.plan, nullptr, nullptr, nullptr,
+                                                      nullptr, r.split, r.counters, r.err, st, launches, &image);
+    if (e != cudaSuccess) rc = ARCHEAD_ERR_CUDA;
+  }
+  cudaFreeAsync(r.base, st);
+  return rc;
 }
 
 // Device address of this device's error word (the device must be current).

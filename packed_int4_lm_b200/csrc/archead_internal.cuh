@@ -303,11 +303,13 @@ cudaError_t launch_repack(const uint8_t* canon, uint8_t* dev, int64_t V, int64_t
                           cudaStream_t st);
 
 // Gradient product dH = dY W through the packed head for n tokens (csrc/grad_tc.cu), in steps:
-//  1. grad_rows: the head's row scales and factor operand into the scratch;
-//  2. the FP16 image of dY: grad_image_dy from dY itself, or from the logits with dY[n, v] =
-//     exp(Y[n, v] - lse[n]) - [v = targets[n]] (the target's entry from its NLL, exp(-nll) - 1):
-//     grad_image_softmax from logits in memory, or grad_tokens, whose TcImage the tcgen05 logits
-//     kernel then fills, and grad_targets, which sets the targets' entries;
+//  1. grad_rows: the head's row scales and factor operand into the scratch.  It runs beside the
+//     kernel before it in the stream, which has to be an ordinary launch of the same call or one
+//     that ends after such a launch;
+//  2. the FP16 image of dY: from dY itself by grad_amax (before grad_rows) and grad_image_dy, or
+//     from the logits with dY[n, v] = exp(Y[n, v] - lse[n]) - [v = targets[n]] (the target's entry
+//     from its NLL, exp(-nll) - 1): grad_image_softmax from logits in memory, or grad_tokens, whose
+//     TcImage the tcgen05 logits kernel then fills, and grad_targets, which sets the targets' entries;
 //  3. grad_product: row n times dnll[n] (nullptr: 1), zero where that is 0.
 // scratch: head_grad_scratch_bytes, the same for all steps.
 struct HeadGrad {
@@ -323,7 +325,9 @@ struct SoftmaxTokens {
   const float *nll, *lse, *dnll;
 };
 size_t head_grad_scratch_bytes(const archead_head* head, int64_t n);
-cudaError_t grad_rows(const HeadGrad& a, bool dy);  // dy: grad_image_dy follows
+int head_grad_image_tile(int64_t n);  // tokens per tile of the image
+cudaError_t grad_rows(const HeadGrad& a);
+cudaError_t grad_amax(const HeadGrad& a, const float* dY);
 cudaError_t grad_image_dy(const HeadGrad& a, const float* dY);
 cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const SoftmaxTokens& t);
 cudaError_t grad_tokens(const HeadGrad& a, const SoftmaxTokens& t, TcImage* image);
@@ -359,11 +363,22 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsig
 // pool (none for 0 bytes); freed with cudaFreeAsync on the same stream.
 int take_scratch(size_t bytes, cudaStream_t st, void** base, unsigned** err);
 void set_last_launches(int n);
-// Logits of N tokens straight into the softmax gradient's image by the tcgen05 kernel.  One
-// launch sequence on st with scratch of its own; tc_image_fits says whether the shape runs there.
+// Logits of N tokens straight into the softmax gradient's image, by the tcgen05 kernels; tc_image_fits
+// says whether the shape runs there.  tc_image_begin takes scratch and prepares H (image tiles of
+// `nt` tokens), tc_image_end launches the main kernel, if rc is ARCHEAD_OK, and frees the scratch.
+struct TcImageRun {
+  TcPlan plan;
+  bool wide;  // tiles of 256 tokens x 256 rows
+  void* base;
+  __half* himg;
+  float *tsc, *split;
+  unsigned *counters, *err;
+};
 bool tc_image_fits(const archead_head* head, const Shapes& s);
-int run_tc_image(const uint16_t* H, const archead_head* head, const Shapes& s, const TcImage& image,
-                 cudaStream_t st, int* launches);
+int tc_image_begin(const uint16_t* H, const archead_head* head, const Shapes& s, int nt, cudaStream_t st,
+                   int* launches, TcImageRun* run);
+int tc_image_end(const archead_head* head, const Shapes& s, const TcImage& image, cudaStream_t st,
+                 int* launches, const TcImageRun& run, int rc);
 int validate_head_args(const archead_head* head, int64_t N, int64_t V, int64_t D, int r_c,
                        int r_r, int g);
 unsigned* error_word_address();

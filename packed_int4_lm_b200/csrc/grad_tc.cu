@@ -13,8 +13,7 @@
 // stage and copied (built from the INT8 rows in the product's loop it took three times as long as
 // a residual tile and set the pace of every round: N = 777, ranks 64 + 64: 3150 us against 760 us).
 //
-//  * grad_rows_kernel: S'_v per row and their maximum, the factor image; clears the per-token
-//    maxima.
+//  * grad_rows_kernel: S'_v per row and their maximum, the factor image.
 //  * dy_amax_kernel, dy_image_kernel: the image, from dY or from logits (softmax gradient).
 //  * grad_tc_kernel: the product.  A work item is 256 columns x up to 256 tokens (two
 //    accumulators) x a slab of the vocabulary; its FP32 sums go to scratch.
@@ -39,8 +38,6 @@ struct RowsParams {
   uint32_t* cs;      // 2^-k per row (grad_row) as FP16x2, vpad (0 past V)
   float2* row;       // TcImage's rows without -es, or nullptr
   float* spmax;      // kRowBlocks
-  unsigned* amax;    // per token, cleared here (n), or nullptr
-  int64_t n;
   char* fimg;        // factor image, or nullptr without ranks
   int fcols;         // its columns: r_c + r_r rounded up to 64
   int a_words;       // factor rows readable as aligned 32-bit words
@@ -94,8 +91,6 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
     if (p.row) p.row[v] = make_float2(log2f(fabsf(s)), __uint_as_float(s < 0.f ? 0x80008000u : 0u));
     m = fmaxf(m, fabsf(s));
   }
-  if (p.amax)
-    for (int64_t i = t0; i < p.n; i += step) p.amax[i] = 0u;
   if (p.fimg) {  // eight factor entries of a row at a time
     const unsigned per = (unsigned)p.fcols >> 3, total = (unsigned)p.vpad * per;  // < 2^31
 #pragma unroll 2
@@ -132,6 +127,9 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
     for (int i = 1; i < 32; ++i) m = fmaxf(m, red[i]);
     p.spmax[blockIdx.x] = m;
   }
+  // Nothing here depends on the kernel before, so it runs beside it; the end of this grid has to
+  // mean the end of that one for the kernels after.
+  grid_dependency_wait();
 }
 
 // Exponent of the largest S' (0 for a head of zeros), by one warp.
@@ -153,7 +151,6 @@ struct AmaxParams {
 __global__ void __launch_bounds__(256) dy_amax_kernel(const AmaxParams p) {
   const int64_t V = p.V;
   allow_dependent_launch();
-  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t per = (V + 2047) / 2048, total = per * p.n;
   for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < total; i += gridDim.x * 8ll) {
@@ -911,7 +908,7 @@ struct GradPlan {
 GradPlan grad_plan(const archead_head& h, int64_t n) {
   GradPlan g;
   const int RR = h.r_c + h.r_r;
-  g.it = n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 64 ? 64 : 128));
+  g.it = head_grad_image_tile(n);
   g.mt = n <= 128 ? 1 : 2;
   g.nimg = (int)((n + g.it - 1) / g.it);
   g.ntt = (g.nimg + g.mt - 1) / g.mt;
@@ -1039,27 +1036,32 @@ cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens*
 
 }  // namespace
 
+int head_grad_image_tile(int64_t n) { return n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 64 ? 64 : 128)); }
+
 size_t head_grad_scratch_bytes(const archead_head* head, int64_t n) { return grad_plan(*head, n).bytes; }
 
-cudaError_t grad_rows(const HeadGrad& a, bool dy) {
+cudaError_t grad_rows(const HeadGrad& a) {
   const archead_head& h = *a.head;
   const GradPlan g = grad_plan(h, a.n);
   const GradParts b = grad_parts(a, g);
-  const RowsParams p = {h, g.nunits * kUnit, b.sp, b.cs, dy ? nullptr : b.row, b.spmax, dy ? b.amax : nullptr, a.n,
+  const RowsParams p = {h, g.nunits * kUnit, b.sp, b.cs, b.row, b.spmax,
                         g.fcols ? b.fimg : nullptr, g.fcols, h.r_c % 4 == 0 && h.r_r % 4 == 0};
-  grad_rows_kernel<<<kRowBlocks, 1024, 0, a.st>>>(p);
+  ++*a.launches;
+  return launch_pdl(grad_rows_kernel, dim3(kRowBlocks), 1024, 0, a.st, p);
+}
+
+cudaError_t grad_amax(const HeadGrad& a, const float* dY) {
+  const GradParts b = grad_parts(a, grad_plan(*a.head, a.n));
+  cudaError_t e = cudaMemsetAsync(b.amax, 0, (size_t)a.n * 4, a.st);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = ((a.head->V + 2047) / 2048 * a.n + 7) / 8;
+  const AmaxParams p = {dY, a.n, a.head->V, b.amax};
+  dy_amax_kernel<<<(unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, a.st>>>(p);
   ++*a.launches;
   return cudaGetLastError();
 }
 
-cudaError_t grad_image_dy(const HeadGrad& a, const float* dY) {
-  const GradParts b = grad_parts(a, grad_plan(*a.head, a.n));
-  const int64_t blocks = ((a.head->V + 2047) / 2048 * a.n + 7) / 8;
-  const AmaxParams p = {dY, a.n, a.head->V, b.amax};
-  const cudaError_t e = launch_pdl(dy_amax_kernel, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)), 256, 0, a.st, p);
-  ++*a.launches;
-  return e == cudaSuccess ? grad_image(a, dY, nullptr) : e;
-}
+cudaError_t grad_image_dy(const HeadGrad& a, const float* dY) { return grad_image(a, dY, nullptr); }
 
 cudaError_t grad_image_softmax(const HeadGrad& a, const float* logits, const SoftmaxTokens& t) {
   return grad_image(a, logits, &t);

@@ -84,23 +84,25 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
       const Shapes s = {std::min(chunk, N - n0), V, D, r_c, r_r, g};
       const HeadGrad a = {head, s.N, b + yoff, err, st, launches};
       const SoftmaxTokens t = {targets + n0, nll + n0, lse + n0, dnll + n0};
-      if (grad_rows(a, false) != cudaSuccess) return static_cast<int>(ARCHEAD_ERR_CUDA);
+      int rc;
       if (fused(s.N)) {
-        TcImage image;
-        if (grad_tokens(a, t, &image) != cudaSuccess)
-          return static_cast<int>(ARCHEAD_ERR_CUDA);
-        const int rc = run_tc_image(H + n0 * D, head, s, image, st, launches);
+        TcImageRun run;
+        TcImage image = {};
+        rc = tc_image_begin(H + n0 * D, head, s, head_grad_image_tile(s.N), st, launches, &run);
         if (rc) return rc;
-        if (grad_targets(a, t) != cudaSuccess) return static_cast<int>(ARCHEAD_ERR_CUDA);
+        rc = cuda_status(grad_rows(a));
+        if (!rc) rc = cuda_status(grad_tokens(a, t, &image));
+        rc = tc_image_end(head, s, image, st, launches, run, rc);
+        if (!rc) rc = cuda_status(grad_targets(a, t));
       } else {
-        const int rc = archead_logits(H + n0 * D, head, Y, s.N, V, D, r_c, r_r, g, stream);
+        rc = archead_logits(H + n0 * D, head, Y, s.N, V, D, r_c, r_r, g, stream);
         if (rc) return rc;
         *launches += archead_last_launches();
-        if (grad_image_softmax(a, Y, t) != cudaSuccess)
-          return static_cast<int>(ARCHEAD_ERR_CUDA);
+        rc = cuda_status(grad_rows(a));
+        if (!rc) rc = cuda_status(grad_image_softmax(a, Y, t));
       }
-      if (grad_product(a, dnll + n0, dH + n0 * D) != cudaSuccess)
-        return static_cast<int>(ARCHEAD_ERR_CUDA);
+      if (!rc) rc = cuda_status(grad_product(a, dnll + n0, dH + n0 * D));
+      if (rc) return rc;
     }
     return static_cast<int>(ARCHEAD_OK);
   });
@@ -122,7 +124,8 @@ int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH,
                       [&](char* b, unsigned* err, int* launches) {
     for (int64_t n0 = 0; n0 < N; n0 += chunk) {
       const HeadGrad a = {head, std::min(chunk, N - n0), b, err, st, launches};
-      cudaError_t e = grad_rows(a, true);
+      cudaError_t e = grad_amax(a, dY + n0 * V);
+      if (e == cudaSuccess) e = grad_rows(a);
       if (e == cudaSuccess) e = grad_image_dy(a, dY + n0 * V);
       if (e == cudaSuccess) e = grad_product(a, nullptr, dH + n0 * D);
       if (e != cudaSuccess) return cuda_status(e);
