@@ -34,6 +34,21 @@ __host__ __device__ __forceinline__ GradRow grad_row(float S, float sac, float s
   return r;
 }
 
+// The product of up to 8 tokens through an SC4 head (grad_warp.cu): the FP32 sums of each slab of the
+// vocabulary, [slab][n][dp], columns 0 .. D - 1 and then the ranks.
+struct GradWarpParams {
+  archead_head h;
+  const char* img;  // image tiles of `it` tokens
+  const uint32_t* cs;
+  const char* fimg;  // factor image: per 32 rows, fcols x 64 bytes
+  float* part;
+  int64_t n, dp, nunits;
+  int it, fcols, slabs, g_shift;
+  unsigned* err;
+};
+constexpr int kGradWarpCtas = 2;  // per SM
+cudaError_t launch_grad_warp(const GradWarpParams& p, cudaStream_t st);
+
 // Image of dY, the product's B operand: per token tile of nt rows and 64 vocabulary rows
 // (half-unit hb) a block of nt x 128 bytes, token nn's 64 FP16 values in one 128-byte row whose
 // 16-byte chunk c is stored at c ^ (nn % 8) (the K-major 128-byte swizzle).  Byte offset of the

@@ -8,7 +8,7 @@
 // dY'[n, v] = dY[n, v] S'_v 2^e_n (grad_common.cuh; 128 tokens are the lanes of an accumulator)
 // and B the dequantised head, whose vocabulary rows are K and whose columns lie side by side
 // (MN-major).  The other way round, with the head as A, few tokens take twice the instructions
-// (128 columns each against 256): N = 1 took 190 us against 165 us when both were built.
+// (128 columns each against 256): N = 1 took 190 us against 165 us when both were built on this kernel.
 // u is one more tile of columns, whose B, a / S', is prepared once per call in the layout of a W
 // stage and copied (built from the INT8 rows in the product's loop it took three times as long as
 // a residual tile and set the pace of every round: N = 777, ranks 64 + 64: 3150 us against 760 us).
@@ -16,10 +16,13 @@
 //  * grad_rows_kernel: S'_v per row and their maximum, the factor image.
 //  * dy_amax_kernel, dy_image_kernel: the image, from dY or from logits (softmax gradient).
 //  * grad_tc_kernel: the product.  A work item is 256 columns x up to 256 tokens (two
-//    accumulators) x a slab of the vocabulary; its FP32 sums go to scratch.
+//    accumulators) x a slab of the vocabulary; its FP32 sums go to scratch.  (Up to 8 tokens of an
+//    SC4 head: grad_warp.cu.)
 //  * grad_finish_kernel: adds the slabs in order, adds u b, scales and rounds to BF16.
 // Nothing is accumulated in memory, so equal calls give equal bits.
 #include "grad_common.cuh"
+
+#include <algorithm>
 
 namespace archead {
 namespace {
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_tc_kernel(const GradPara
     // A warp owns rows 32 rg .. + 31 (a W stage) and one 128-column block b: with two accumulators
     // half of that block's 16-byte chunks in every unit; with one, where units follow one another
     // twice as fast, all of them in every other unit, which halves what a unit pays for barriers
-    // and fences (N = 1 with a dY of FP32: 148 -> 141 us).
+    // and fences (one token: 148 -> 141 us).
     constexpr int NH = 3 - MT;  // halves of the chunks per warp, and groups of warps by unit
     const int rg = warp & 3, b = (warp >> 2) & 1, grp = warp >> 3;
     const int s = 32 * rg + lane;  // row in the unit
@@ -898,6 +901,7 @@ int sm_count() {
 }
 
 struct GradPlan {
+  bool warp;   // on warp MMAs (grad_warp.cu)
   int it, mt;  // tokens per image tile, image tiles per item
   int nimg, ntt, ntiles, slabs;
   int64_t npad, nunits, dp;
@@ -922,9 +926,16 @@ GradPlan grad_plan(const archead_head& h, int64_t n) {
   // of 128 rows with two accumulators, 0.9 us with one.
   const int64_t tiles = (int64_t)g.ntt * g.ntiles;
   const int64_t sms = sm_count();
-  double best = 1e300;
   g.slabs = 1;
-  for (int s = 1; s <= 64 && s * 4 <= g.nunits + 3; ++s) {
+  // The warp MMAs win up to 8 tokens, a whole call by 143 -> 128 us at N = 1 and 146 -> 134 us at
+  // N = 8 (V = 151936, D = 4096); with 16 they need twice the registers: 155 -> 200 us.
+  g.warp = n <= 8 && h.format == ARCHEAD_FMT_SC4;
+  if (g.warp) {  // one round of CTAs, each at least four units
+    const int64_t all = (h.D + 255) / 256 + (RR + 63) / 64;
+    g.slabs = (int)std::max<int64_t>(1, std::min(sms * kGradWarpCtas / all, g.nunits / 4));
+  }
+  double best = 1e300;
+  for (int s = 1; !g.warp && s <= 64 && s * 4 <= g.nunits + 3; ++s) {
     if (s > 1 && 4.0 * s * n * g.dp > 1e9) break;  // (scratch)
     const int64_t rounds = (tiles * s + sms - 1) / sms;
     const double tile_us = g.nunits * (g.mt == 2 ? 1.6 : 0.9);
@@ -1088,7 +1099,9 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   while ((1 << gs) < h.g) ++gs;
   const GradParams p = {h, b.img, b.cs, b.part, a.n, g.dp, g.nunits, g.nimg, g.ntt, g.ntiles, g.slabs, gs, b.fimg, g.fcols, a.err};
   cudaError_t e;
-  if (g.mt == 2) {
+  if (g.warp) {
+    e = launch_grad_warp({h, b.img, b.cs, b.fimg, b.part, a.n, g.dp, g.nunits, g.it, g.fcols, g.slabs, gs, a.err}, a.st);
+  } else if (g.mt == 2) {
     e = launch_grad_it<128, 2>(p, a.st);
   } else {
     switch (g.it) {
