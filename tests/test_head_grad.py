@@ -130,6 +130,26 @@ def test_logits_grad_matches_fp64(cuda_ok, name, N):
           + smallest_step(head, M, dY), name)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,r,g", [(4096, 32, 128), (3968, 40, 32)])
+def test_few_tokens_through_a_large_head(cuda_ok, D, r, g):
+    """Slabs of the vocabulary longer than a kernel's ring of stages, in up to 8 and more tokens;
+    every row has the same bits whatever the batch beside it."""
+    head = make_head(23017, D, r, r, g)
+    W, M = magnitudes(head)
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    dY = make_dY(9, head["V"], D)
+    want = dY.astype(np.float64) @ W
+    tol = BF16 * np.abs(want) + PROD * (np.abs(dY).astype(np.float64) @ M) + smallest_step(head, M, dY)
+    t = torch.from_numpy(dY).cuda()
+    rows = {}
+    for N in (9, 8, 5, 1):
+        got = rows[N] = ah.logits_grad(t[:N], dh)
+        ah.check()
+        close(got, want[:N], tol[:N], N)
+    assert torch.equal(rows[8][:5], rows[5]) and torch.equal(rows[5][:1], rows[1])
+
+
 def nll_case(head, W, N, seed):
     D, V = head["D"], head["V"]
     H = make_hidden(N, make_channel_scales(D, 0.5, 4, 20.0, seed), seed + 1)
