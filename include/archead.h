@@ -205,8 +205,9 @@ enum archead_reduction {
  *   shares of it, and the share of the weight whose surrogate is clipped, all reduced alike.
  *   A token with weight 0, or outside every sequence, is masked: nothing else of it is used
  *   (it may hold NaN) and its dnll is 0.  Where no token counts, loss and gradient are 0.
- *   Offsets that fall or leave [0, N] set ARCHEAD_ERR_SEGMENT (each is then taken at the
- *   nearest allowed value).  0 <= clip_low < 1, clip_high >= 0, kl_coef finite; B < 2^31 - 1.
+ *   Offsets that fall or leave [0, N] set ARCHEAD_ERR_SEGMENT.  Each is then clamped into
+ *   [0, N]; where they still fall, dnll and stats are unspecified (nothing outside the arrays
+ *   is read or written).  0 <= clip_low < 1, clip_high >= 0, kl_coef finite; B < 2^31 - 1.
  *   Sums are held in FP64 and in a fixed order: equal calls give equal bits.  N = 0 writes
  *   stats alone.  Asynchronous on `stream`.
  */
