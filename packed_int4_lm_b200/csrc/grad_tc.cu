@@ -31,7 +31,7 @@ constexpr int kDequantWarps = 16;
 constexpr int kGradThreads = 32 * (kDequantWarps + 7);  // + 4 epilogue, 1 producer, 2 MMA
 constexpr int kUnit = 128;                              // vocabulary rows per unit of K
 constexpr int kWStage = 32 * 256 * 2;                   // 32 rows x 256 columns FP16
-constexpr int kRowBlocks = 296;                         // blocks of grad_rows_kernel
+constexpr int kRowBlocks = 592, kRowThreads = 512;      // of grad_rows_kernel
 
 // ---- the image ---------------------------------------------------------------------------
 struct RowsParams {
@@ -72,10 +72,10 @@ __device__ __forceinline__ GradRow head_row(const archead_head& h, int64_t v, fl
   return grad_row(bf16_bits_to_float(__ldg(h.r_super + v)), *sac, *saw);
 }
 
-__global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, 4) grad_rows_kernel(const RowsParams p) {
   allow_dependent_launch();
-  __shared__ float red[32];
-  const int64_t t0 = blockIdx.x * 1024ll + threadIdx.x, step = gridDim.x * 1024ll;
+  __shared__ float red[kRowThreads / 32];
+  const int64_t t0 = blockIdx.x * (int64_t)kRowThreads + threadIdx.x, step = gridDim.x * (int64_t)kRowThreads;
   float m = 0.f;
   for (int64_t v = t0; v < p.vpad; v += step) {
     float s = 0.f, c = 0.f;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 32; ++i) m = fmaxf(m, red[i]);
+    for (int i = 1; i < kRowThreads / 32; ++i) m = fmaxf(m, red[i]);
     p.spmax[blockIdx.x] = m;
   }
   // Nothing here depends on the kernel before, so it runs beside it; the end of this grid has to
@@ -138,7 +138,11 @@ __global__ void __launch_bounds__(1024, 2) grad_rows_kernel(const RowsParams p) 
 // Exponent of the largest S' (0 for a head of zeros), by one warp.
 __device__ __forceinline__ int spmax_exp(const float* spmax) {
   float m = 0.f;
-  for (int i = threadIdx.x & 31; i < kRowBlocks; i += 32) m = fmaxf(m, spmax[i]);
+#pragma unroll  // (all loads at once)
+  for (int i = 0; i < (kRowBlocks + 31) / 32; ++i) {
+    const int b = 32 * i + (threadIdx.x & 31);
+    m = fmaxf(m, b < kRowBlocks ? spmax[b] : 0.f);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = m > 0.f && m <= 3.402823466e38f ? ilogbf(m) : 0;
@@ -758,8 +762,11 @@ __device__ __forceinline__ uint32_t bf2_bits(__nv_bfloat162 x) { return *reinter
 // the product took three times as long, and a lone block of a small batch 40 us of dependent
 // loads.
 constexpr int kFinishPad = 4;  // floats after a row of u
+// Threads: a second half for the sums u where latency counts.
+constexpr int finish_threads(int mt) { return mt == 1 ? 256 : 128; }
 template <int MT>
-__global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const FinishParams p) {
+  constexpr int T = finish_threads(MT), U = T - 128;  // u: threads from U on
   extern __shared__ __align__(16) unsigned char fsm[];
   const int RR = p.h.r_c + p.h.r_r, rp = (RR + 15) & ~15, us_row = rp + kFinishPad;
   float* us = reinterpret_cast<float*>(fsm);                      // [16 MT][us_row]
@@ -767,7 +774,7 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
   int8_t* bs = reinterpret_cast<int8_t*>(ss + 4 * rp);            // [rp][144] entries of b
   const int64_t n0 = blockIdx.x * (16ll * MT), d0 = blockIdx.y * 128ll;
   const int64_t G = p.h.D / p.h.g;
-  for (int i = threadIdx.x; i < rp * 8; i += 128) {  // b does not depend on earlier kernels
+  for (int i = threadIdx.x; i < rp * 8; i += T) {  // b does not depend on earlier kernels
     const int j = i >> 3, c = i & 7;
     const bool core = j < p.h.r_c;
     uint4 q = make_uint4(0, 0, 0, 0);
@@ -775,7 +782,7 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
       q = __ldg(reinterpret_cast<const uint4*>((core ? p.h.Bc + j * p.h.D : p.h.Bw + (j - p.h.r_c) * p.h.D) + d0) + c);
     *reinterpret_cast<uint4*>(bs + j * 144 + 16 * c) = q;
   }
-  for (int i = threadIdx.x; i < rp * 4; i += 128) {
+  for (int i = threadIdx.x; i < rp * 4; i += T) {
     const int j = i >> 2;
     const bool core = j < p.h.r_c;
     const int64_t grp = (d0 + 32 * (i & 3)) / p.h.g;
@@ -783,24 +790,30 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
   }
   grid_dependency_wait();
   const int64_t slab = p.n * p.dp;
-  for (int i = threadIdx.x; i < 4 * MT * rp; i += 128) {
-    const int t = i / (rp >> 2), j = 4 * (i - t * (rp >> 2));
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n0 + t < p.n && j < RR) {
-      const float* q = p.part + (n0 + t) * p.dp + p.h.D + j;
+  if (threadIdx.x >= U) {
+    for (int i = threadIdx.x - U; i < 4 * MT * rp; i += 128) {
+      const int t = i / (rp >> 2), j = 4 * (i - t * (rp >> 2));
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n0 + t < p.n && j < RR) {
+        const float* q = p.part + (n0 + t) * p.dp + p.h.D + j;
 #pragma unroll 8
-      for (int s = 0; s < p.slabs; ++s) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(q + s * slab));
-        a.x += x.x;
-        a.y += x.y;
-        a.z += x.z;
-        a.w += x.w;
+        for (int s = 0; s < p.slabs; ++s) {
+          const float4 x = __ldcs(reinterpret_cast<const float4*>(q + s * slab));
+          a.x += x.x;
+          a.y += x.y;
+          a.z += x.z;
+          a.w += x.w;
+        }
+        if (j + 1 >= RR) a.y = 0.f;  // past the ranks nothing was written
+        if (j + 2 >= RR) a.z = 0.f;
+        if (j + 3 >= RR) a.w = 0.f;
       }
-      if (j + 1 >= RR) a.y = 0.f;  // past the ranks nothing was written
-      if (j + 2 >= RR) a.z = 0.f;
-      if (j + 3 >= RR) a.w = 0.f;
+      *reinterpret_cast<float4*>(us + t * us_row + j) = a;
     }
-    *reinterpret_cast<float4*>(us + t * us_row + j) = a;
+    if (U > 0) {
+      __syncthreads();
+      return;
+    }
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, gr = lane >> 2, q = lane & 3;
   float acc[MT][4][4];
@@ -815,30 +828,37 @@ __global__ void __launch_bounds__(128) grad_finish_kernel(const FinishParams p) 
       sc[m][hrow] = n < p.n && p.rowscale ? p.rowscale[n] : 1.f;
     }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m) {
+    float2 a[2][4];
+    const float* src[2];
+    bool in[2];
 #pragma unroll
     for (int hrow = 0; hrow < 2; ++hrow) {
       const int64_t n = n0 + 16 * m + 8 * hrow + gr;
-      float2 a[4];
+      in[hrow] = n < p.n;
+      src[hrow] = p.part + n * p.dp + d0 + 32 * w + 2 * q;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) a[c] = make_float2(0.f, 0.f);
-      if (n < p.n) {
-        const float* src = p.part + n * p.dp + d0 + 32 * w + 2 * q;
+      for (int c = 0; c < 4; ++c) a[hrow][c] = make_float2(0.f, 0.f);
+    }
 #pragma unroll(MT == 1 ? 8 : 2)
-        for (int s = 0; s < p.slabs; ++s)
+    for (int s = 0; s < p.slabs; ++s)
+#pragma unroll
+      for (int hrow = 0; hrow < 2; ++hrow)
+        if (in[hrow])
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float2 x = __ldcs(reinterpret_cast<const float2*>(src + s * slab + 8 * c));
-            a[c].x += x.x;
-            a[c].y += x.y;
+            const float2 x = __ldcs(reinterpret_cast<const float2*>(src[hrow] + s * slab + 8 * c));
+            a[hrow][c].x += x.x;
+            a[hrow][c].y += x.y;
           }
-      }
+#pragma unroll
+    for (int hrow = 0; hrow < 2; ++hrow)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        acc[m][c][2 * hrow] = a[c].x;
-        acc[m][c][2 * hrow + 1] = a[c].y;
+        acc[m][c][2 * hrow] = a[hrow][c].x;
+        acc[m][c][2 * hrow + 1] = a[hrow][c].y;
       }
-    }
+  }
   __syncthreads();
   for (int k0 = 0; k0 < rp; k0 += 16) {
     const int j = k0 + 2 * q;
@@ -1058,7 +1078,7 @@ cudaError_t grad_rows(const HeadGrad& a) {
   const RowsParams p = {h, g.nunits * kUnit, b.sp, b.cs, b.row, b.spmax,
                         g.fcols ? b.fimg : nullptr, g.fcols, h.r_c % 4 == 0 && h.r_r % 4 == 0};
   ++*a.launches;
-  return launch_pdl(grad_rows_kernel, dim3(kRowBlocks), 1024, 0, a.st, p);
+  return launch_pdl(grad_rows_kernel, dim3(kRowBlocks), kRowThreads, 0, a.st, p);
 }
 
 cudaError_t grad_amax(const HeadGrad& a, const float* dY) {
@@ -1119,7 +1139,7 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   const size_t smem = finish_smem(mt, h.r_c + h.r_r);
   auto kern = mt == 4 ? grad_finish_kernel<4> : grad_finish_kernel<1>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)((a.n + 16 * mt - 1) / (16 * mt)), (unsigned)(h.D / 128)), 128, smem, a.st, fp);
+  return launch_pdl(kern, dim3((unsigned)((a.n + 16 * mt - 1) / (16 * mt)), (unsigned)(h.D / 128)), finish_threads(mt), smem, a.st, fp);
 }
 
 }  // namespace archead

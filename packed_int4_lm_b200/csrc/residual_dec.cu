@@ -410,6 +410,7 @@ __device__ __forceinline__ void dec_blocks_q(const uint32_t (&wlo)[RG][2][4],
 template <int NT8, int CPC, int MODE>
 __global__ void __launch_bounds__(DecCfg<NT8>::THREADS, 1)
     residual_dec_kernel(const DecParams p) {
+  allow_dependent_launch();  // nll_grad's row scales (grad_tc.cu) are made beside this kernel
   constexpr int NTOK = DecCfg<NT8>::NTOK;
   constexpr int PAR = DecCfg<NT8>::PAR;
   constexpr int CONSUMERS = DecCfg<NT8>::CONSUMERS;
