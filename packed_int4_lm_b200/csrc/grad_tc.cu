@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
   }
   grid_dependency_wait();
   const int64_t slab = p.n * p.dp;
-  if (threadIdx.x >= U) {
+  if (U == 0 || threadIdx.x >= U) {
     for (int i = threadIdx.x - U; i < 4 * MT * rp; i += 128) {
       const int t = i / (rp >> 2), j = 4 * (i - t * (rp >> 2));
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
