@@ -14,8 +14,8 @@
 //  * Sums stay in registers for the whole slab (64 a thread); at the end the warps' sums are added
 //    through shared memory in their order and written to scratch as grad_tc_kernel does.
 // Measured, cold caches: 89 us, 3.9 TB/s; four warps per scheduler issue in 63 % of the cycles, 2.7
-// instructions per weight.  Without the dequantisation a whole call (N = 1) takes 108 of 128 us: the
-// rest is the chain of kernels around this one and the head's way through memory (52 us).
+// instructions per weight.  (A copy without the dequantisation took 20 us less: what is left then is
+// the head's way through memory, 52 us, and the ends of the pipeline.)
 // A unit of 128 rows x 256 columns (16 KB; its image: 256 bytes per token) comes by bulk copies into
 // a ring, whose second block is placed 64 bytes further, so that 8 lanes read 128 bytes of all banks.
 // The rank sums' tiles are 64 columns of the factor image, 16 KB per unit too.
