@@ -200,7 +200,8 @@ def _own(s, op):
         return ah.policy_loss(s["nll"], s["old"], s["adv"], nll_ref=s["ref"], weights=s["w"], cu_seqlens=s["cu"],
                               per_sequence=c["per_seq"], reduction=c["reduction"], **POLICY)
     return ah.preference_loss(s["nll"], s["cu"], s["pairs"], nll_ref=s["ref"], weights=s["w"], beta=0.1,
-                              kind=c["kind"], average=c["average"], label_smoothing=0.05, margin=0.1)
+                              kind=c["kind"], average=c["average"], margin=0.1,
+                              label_smoothing=0.05 if c["kind"] == "sigmoid" else 0.0)
 
 
 def _nll_grad(s):
