@@ -762,16 +762,20 @@ __device__ __forceinline__ uint32_t bf2_bits(__nv_bfloat162 x) { return *reinter
 // the product took three times as long, and a lone block of a small batch 40 us of dependent
 // loads.
 constexpr int kFinishPad = 4;  // floats after a row of u
-// Threads: a second half for the sums u where latency counts.
-constexpr int finish_threads(int mt) { return mt == 1 ? 256 : 128; }
+constexpr int kFinishRow = 132;  // floats per token of the columns' sums (MT = 1)
+// With 16 tokens per block (few tokens or columns) latency counts, so 512 threads add the slabs, one
+// float4 of the columns and one of u each, and hand them to the four warps through shared memory
+// (N = 166, D = 512, 133 ranks, 38 slabs: 57 us with 128 threads for either).
+constexpr int finish_threads(int mt) { return mt == 1 ? 512 : 128; }
 template <int MT>
 __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const FinishParams p) {
-  constexpr int T = finish_threads(MT), U = T - 128;  // u: threads from U on
+  constexpr int T = finish_threads(MT);
   extern __shared__ __align__(16) unsigned char fsm[];
   const int RR = p.h.r_c + p.h.r_r, rp = (RR + 15) & ~15, us_row = rp + kFinishPad;
   float* us = reinterpret_cast<float*>(fsm);                      // [16 MT][us_row]
   float* ss = us + 16 * MT * us_row;                              // [rp][4] scales of b
   int8_t* bs = reinterpret_cast<int8_t*>(ss + 4 * rp);            // [rp][144] entries of b
+  float* ms = reinterpret_cast<float*>(bs + 144 * rp);            // [16][kFinishRow] with MT = 1
   const int64_t n0 = blockIdx.x * (16ll * MT), d0 = blockIdx.y * 128ll;
   const int64_t G = p.h.D / p.h.g;
   for (int i = threadIdx.x; i < rp * 8; i += T) {  // b does not depend on earlier kernels
@@ -790,30 +794,54 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
   }
   grid_dependency_wait();
   const int64_t slab = p.n * p.dp;
-  if (U == 0 || threadIdx.x >= U) {
-    for (int i = threadIdx.x - U; i < 4 * MT * rp; i += 128) {
-      const int t = i / (rp >> 2), j = 4 * (i - t * (rp >> 2));
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (n0 + t < p.n && j < RR) {
-        const float* q = p.part + (n0 + t) * p.dp + p.h.D + j;
+  // u: four ranks of a token of the block
+  auto u_at = [&](int i, int* t, int* j) {
+    *t = i / (rp >> 2);
+    *j = 4 * (i - *t * (rp >> 2));
+    return i < 4 * MT * rp && n0 + *t < p.n && *j < RR ? p.part + (n0 + *t) * p.dp + p.h.D + *j : nullptr;
+  };
+  auto u_put = [&](int t, int j, float4 a) {
+    if (j + 1 >= RR) a.y = 0.f;  // past the ranks nothing was written
+    if (j + 2 >= RR) a.z = 0.f;
+    if (j + 3 >= RR) a.w = 0.f;
+    *reinterpret_cast<float4*>(us + t * us_row + j) = a;
+  };
+  auto add = [](float4& a, const float* x) {
+    const float4 y = __ldcs(reinterpret_cast<const float4*>(x));
+    a.x += y.x;
+    a.y += y.y;
+    a.z += y.z;
+    a.w += y.w;
+  };
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  int first = threadIdx.x;
+  if (MT == 1) {
+    const int mt = threadIdx.x >> 5, mc = 4 * (threadIdx.x & 31);
+    const float* msrc = n0 + mt < p.n ? p.part + (n0 + mt) * p.dp + d0 + mc : nullptr;
+    int t, j;
+    const float* usrc = u_at(threadIdx.x, &t, &j);
+    float4 m = zero, u = zero;
 #pragma unroll 8
-        for (int s = 0; s < p.slabs; ++s) {
-          const float4 x = __ldcs(reinterpret_cast<const float4*>(q + s * slab));
-          a.x += x.x;
-          a.y += x.y;
-          a.z += x.z;
-          a.w += x.w;
-        }
-        if (j + 1 >= RR) a.y = 0.f;  // past the ranks nothing was written
-        if (j + 2 >= RR) a.z = 0.f;
-        if (j + 3 >= RR) a.w = 0.f;
-      }
-      *reinterpret_cast<float4*>(us + t * us_row + j) = a;
+    for (int s = 0; s < p.slabs; ++s) {
+      if (msrc) add(m, msrc + s * slab);
+      if (usrc) add(u, usrc + s * slab);
     }
-    if (U > 0) {
-      __syncthreads();
-      return;
-    }
+    *reinterpret_cast<float4*>(ms + mt * kFinishRow + mc) = m;
+    if (first < 4 * rp) u_put(t, j, u);
+    first += T;
+  }
+  for (int i = first; i < 4 * MT * rp; i += T) {
+    int t, j;
+    const float* src = u_at(i, &t, &j);
+    float4 a = zero;
+    if (src)
+#pragma unroll 8
+      for (int s = 0; s < p.slabs; ++s) add(a, src + s * slab);
+    u_put(t, j, a);
+  }
+  if (MT == 1) {
+    __syncthreads();
+    if (threadIdx.x >= 128) return;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, gr = lane >> 2, q = lane & 3;
   float acc[MT][4][4];
@@ -827,8 +855,18 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
       ex[m][hrow] = n < p.n ? p.texp[n] : 0;
       sc[m][hrow] = n < p.n && p.rowscale ? p.rowscale[n] : 1.f;
     }
+  if (MT == 1) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+    for (int hrow = 0; hrow < 2; ++hrow)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 x = *reinterpret_cast<const float2*>(ms + (8 * hrow + gr) * kFinishRow + 32 * w + 8 * c + 2 * q);
+        acc[0][c][2 * hrow] = x.x;
+        acc[0][c][2 * hrow + 1] = x.y;
+      }
+  }
+#pragma unroll
+  for (int m = 0; MT > 1 && m < MT; ++m) {
     float2 a[2][4];
     const float* src[2];
     bool in[2];
@@ -840,7 +878,7 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
 #pragma unroll
       for (int c = 0; c < 4; ++c) a[hrow][c] = make_float2(0.f, 0.f);
     }
-#pragma unroll(MT == 1 ? 8 : 2)
+#pragma unroll 2
     for (int s = 0; s < p.slabs; ++s)
 #pragma unroll
       for (int hrow = 0; hrow < 2; ++hrow)
@@ -859,7 +897,7 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
         acc[m][c][2 * hrow + 1] = a[hrow][c].y;
       }
   }
-  __syncthreads();
+  if (MT > 1) __syncthreads();
   for (int k0 = 0; k0 < rp; k0 += 16) {
     const int j = k0 + 2 * q;
     uint32_t b[4][2];
@@ -908,7 +946,7 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
 
 size_t finish_smem(int mt, int RR) {
   const size_t rp = (RR + 15) / 16 * 16;
-  return 16 * mt * (rp + kFinishPad) * 4 + rp * 16 + rp * 144;
+  return 16 * mt * (rp + kFinishPad) * 4 + rp * 16 + rp * 144 + (mt == 1 ? 16 * kFinishRow * 4 : 0);
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -1134,8 +1172,9 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   if (e != cudaSuccess) return e;
   const FinishParams fp = {h, b.part, a.n, g.dp, g.slabs, b.texp, dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
   *a.launches += 2;
-  // 64 tokens per block share b; small batches take 16, for more blocks
-  const int mt = a.n > 512 ? 4 : 1;
+  // 64 tokens per block share b where those blocks fill the SMs twice; otherwise 16, for more blocks
+  // (V = 27766, D = 512, N = 926: 73 us in 60 blocks of 64)
+  const int mt = (a.n + 63) / 64 * (h.D / 128) >= 2 * sm_count() ? 4 : 1;
   const size_t smem = finish_smem(mt, h.r_c + h.r_r);
   auto kern = mt == 4 ? grad_finish_kernel<4> : grad_finish_kernel<1>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
