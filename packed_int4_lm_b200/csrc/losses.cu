@@ -93,6 +93,9 @@ __device__ __forceinline__ int warp_seq_of(const Seqs& q, int t) {
 // Walks the sequences along adjacent pieces, one warp: window(i) lets each lane load what belongs
 // to sequence i (32 sequences at a time), and piece(t0, t1, f) calls f(j, s, lo, hi, b0, b1) with
 // the whole warp for the tokens [lo, hi) of sequence s = [b0, b1), whose window data lane j holds.
+// Where a window's 32 sequences lie inside the piece and are short, many(s, lo, hi, b0, b1) takes
+// them at once: lane j has sequence s + j = [b0, b1), and [lo, hi) are the tokens of all (6500
+// sequences of one token, preference: 144 -> 58 us).
 template <typename W>
 struct Walker {
   const Seqs q;
@@ -113,10 +116,21 @@ struct Walker {
     b0 = seq_at(q, s);
     load();
   }
-  template <typename F>
-  __device__ __forceinline__ void piece(int t0, int t1, F f) {
+  template <typename F, typename M>
+  __device__ __forceinline__ void piece(int t0, int t1, F f, M many) {
     int pos = t0 < b0 ? b0 : t0;  // (tokens before the first sequence)
     while (pos < t1 && s + j < q.B) {
+      if (j == 0 && pos == b0 && s + 32 <= q.B) {
+        const int last = __shfl_sync(0xffffffffu, end, 31), before = __shfl_up_sync(0xffffffffu, end, 1);
+        const int begin = (threadIdx.x & 31) == 0 ? b0 : before;
+        if (last <= t1 && __all_sync(0xffffffffu, end >= begin && end - begin <= 32)) {
+          many(s, b0, last, begin, end);
+          pos = b0 = last;
+          s += 32;
+          load();
+          continue;
+        }
+      }
       const int b1 = __shfl_sync(0xffffffffu, end, j);
       const int hi = b1 < t1 ? b1 : t1;
       if (hi > pos) {
@@ -133,6 +147,15 @@ struct Walker {
     }
   }
 };
+
+// The lane whose sequence of a window holds token t (b1: the lanes' ends, in order).
+__device__ __forceinline__ int lane_of(int b1, int t) {
+  int j = 0;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1)
+    if (__shfl_sync(0xffffffffu, b1, j + step - 1) <= t) j += step;
+  return j;
+}
 
 // The lane's i-th token of the piece at t0: two runs of four adjacent ones.
 __device__ __forceinline__ int token_at(int t0, int i) {
@@ -226,6 +249,14 @@ __device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, con
       sum.w = warp_sum(sum.w);
       if (kValue) sum.x = warp_sum(sum.x);
       if (lane == 0) *(b0 < t0 ? out.head + c : (b1 > t1 ? out.tail + c : out.whole + s)) = sum;
+    }, [&](int s, int, int, int b0, int b1) {
+      Pair2 sum = {0.0, 0.0};
+      for (int t = b0; t < b1; ++t) {
+        const float f = w ? __ldg(w + t) : 1.f;
+        sum.w += (double)f;
+        if (kValue && f != 0.f) sum.x += (double)f * ((ref ? (double)__ldg(ref + t) : 0.0) - (double)__ldg(nll + t));
+      }
+      out.whole[s + lane] = sum;
     });
   }
 }
@@ -370,6 +401,15 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const bool in = (unsigned)(token_at(t0, i) - lo) < (unsigned)(hi - lo);
+          g[i] = in ? fs : g[i];
+          A[i] = in && a.adv_per_seq ? as : A[i];
+        }
+      }, [&](int, int lo, int hi, int, int b1) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int t = token_at(t0, i), j = lane_of(b1, t);
+          const float fs = __shfl_sync(0xffffffffu, sc, j), as = __shfl_sync(0xffffffffu, adv, j);
+          const bool in = (unsigned)(t - lo) < (unsigned)(hi - lo);
           g[i] = in ? fs : g[i];
           A[i] = in && a.adv_per_seq ? as : A[i];
         }
@@ -714,22 +754,45 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
         const bool in = (unsigned)(token_at(t0, i) - lo) < (unsigned)(hi - lo);
         if (in && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
       }
+    }, [&](int s, int lo, int hi, int b0, int b1) {
+      double own = coef;
+      if (a.average) {
+        const double t = b1 > b0 ? q.whole[s + lane].w : 0.0;
+        own = t > 0.0 ? own / t : 0.0;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = token_at(t0, i);
+        const double f = __shfl_sync(0xffffffffu, own, lane_of(b1, t));
+        const bool in = (unsigned)(t - lo) < (unsigned)(hi - lo);
+        if (in && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
+      }
     });
     store_piece(a.dnll, t0, t1, vec, g);
   }
 }
 
+// With few sequences (kFew) many pairs add to one slope: a block's are added in shared memory first
+// (12000 pairs of 2 sequences: a call 41 -> 22 us).
+constexpr int kLocalSeqs = 256;
+template <bool kFew>
 __global__ void __launch_bounds__(256) pref_pair_kernel(PreferenceArgs a, PrefConst k, SeqSums q,
                                                         unsigned long long* acc, double* part,
                                                         unsigned* err) {
   allow_dependent_launch();
-  grid_dependency_wait();
   __shared__ double red[8];
+  __shared__ unsigned long long local[kFew ? kLocalSeqs * kLimbs : 1];
+  const int words = kFew ? (int)a.B * kLimbs : 0;
+  for (int i = threadIdx.x; i < words; i += 256) local[i] = 0ull;
+  if (kFew) __syncthreads();
+  grid_dependency_wait();
   double sum = 0.0;
   for (int64_t p0 = blockIdx.x * 16ll; p0 < a.P; p0 += gridDim.x * 16ll)
-    sum += pair_step(a, k, q, p0 + (threadIdx.x >> 4), acc, err);
+    sum += pair_step(a, k, q, p0 + (threadIdx.x >> 4), kFew ? local : acc, err);
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  for (int i = threadIdx.x; i < words; i += 256)
+    if (local[i]) atomicAdd(acc + i, local[i]);
 }
 
 __device__ __forceinline__ float pref_mean(const PreferenceArgs& a, double sum) {
@@ -864,7 +927,7 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsig
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int np = capped((a.P + 15) / 16);
-  e = launch_after(pref_pair_kernel, np, 256, 0, st, a, k, q, acc, part, err);
+  e = launch_after(a.B <= kLocalSeqs ? pref_pair_kernel<true> : pref_pair_kernel<false>, np, 256, 0, st, a, k, q, acc, part, err);
   if (e != cudaSuccess) return e;
   e = launch_after(pref_token_kernel, pb, 256, 0, st, a, k, q, acc, part, np);
   *launches += 3;

@@ -107,6 +107,7 @@ LENS = {
     "empty ones": [0, 0, 5, 0, 1, 0, 700, 0],
     "piece edges": [256, 255, 257, 1, 1024, 0, 512],
     "many short": [3, 0, 1, 2] * 300,
+    "short in one block": [1] * 100 + [1, 2, 0, 3, 33, 1] * 20 + [0] * 70 + [2] * 100,
     "one long": [2, 20011, 1],
     "many": list(np.random.default_rng(5).integers(0, 40, size=1500)),
 }
