@@ -30,7 +30,8 @@ constexpr int kPer = 8, kPiece = 32 * kPer;  // tokens per lane, per warp
 constexpr int kMaxBlocks = 148 * 4;          // blocks of a launch: what runs at once, so that a
                                              // warp's pieces lie side by side
 constexpr int kSmallPieces = 32;             // what one block takes, one piece per warp
-constexpr int kSmallSeqs = 512, kSmallPairs = 1024;  // (30 KB of shared memory)
+constexpr int kSmallSeqs = 256, kSmallPairs = 192;  // (more of them take longer in one block than the
+                                                    // chain: 256 sequences, 256 pairs 30 against 24 us)
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
@@ -93,9 +94,9 @@ __device__ __forceinline__ int warp_seq_of(const Seqs& q, int t) {
 // Walks the sequences along adjacent pieces, one warp: window(i) lets each lane load what belongs
 // to sequence i (32 sequences at a time), and piece(t0, t1, f) calls f(j, s, lo, hi, b0, b1) with
 // the whole warp for the tokens [lo, hi) of sequence s = [b0, b1), whose window data lane j holds.
-// Where a window's 32 sequences lie inside the piece and are short, many(s, lo, hi, b0, b1) takes
-// them at once: lane j has sequence s + j = [b0, b1), and [lo, hi) are the tokens of all (6500
-// sequences of one token, preference: 144 -> 58 us).
+// Short sequences inside the piece are taken several at once, by many(s, lo, hi, b0, b1, mine): lane
+// j has sequence s + j = [b0, b1) if it is one of them (mine), and [lo, hi) are the tokens of all (6500
+// sequences of one token, preference: 144 -> 34 us; 8192 of 512 tokens 31 -> 32 us).
 template <typename W>
 struct Walker {
   const Seqs q;
@@ -104,6 +105,7 @@ struct Walker {
 
   __device__ __forceinline__ void load() {
     const int i = s + (threadIdx.x & 31);
+    end = 0x7fffffff;
     if (i < q.B) {
       end = seq_at(q, i + 1);
       window(i);
@@ -120,18 +122,26 @@ struct Walker {
   __device__ __forceinline__ void piece(int t0, int t1, F f, M many) {
     int pos = t0 < b0 ? b0 : t0;  // (tokens before the first sequence)
     while (pos < t1 && s + j < q.B) {
-      if (j == 0 && pos == b0 && s + 32 <= q.B) {
-        const int last = __shfl_sync(0xffffffffu, end, 31), before = __shfl_up_sync(0xffffffffu, end, 1);
-        const int begin = (threadIdx.x & 31) == 0 ? b0 : before;
-        if (last <= t1 && __all_sync(0xffffffffu, end >= begin && end - begin <= 32)) {
-          many(s, b0, last, begin, end);
+      const int b1 = __shfl_sync(0xffffffffu, end, j);
+      if (pos == b0 && b1 <= t1 && b1 - b0 <= 32) {
+        const int before = __shfl_up_sync(0xffffffffu, end, 1), lane = threadIdx.x & 31;
+        const int begin = lane == 0 ? b0 : before;
+        const unsigned run = __ballot_sync(0xffffffffu, end <= t1 && end >= begin && end - begin <= 32) >> j;
+        const int n = run == 0xffffffffu ? 32 : __ffs(~run) - 1;  // sequences j .. j + n - 1 of the window
+        if (n >= 4) {  // (8: 36 against 34 us)
+          const int last = __shfl_sync(0xffffffffu, end, j + n - 1);
+          const bool mine = lane >= j && lane < j + n;
+          many(s, b0, last, mine ? begin : 0, end, mine);
           pos = b0 = last;
-          s += 32;
-          load();
+          j += n;
+          if (j == 32) {
+            s += 32;
+            j = 0;
+            load();
+          }
           continue;
         }
       }
-      const int b1 = __shfl_sync(0xffffffffu, end, j);
       const int hi = b1 < t1 ? b1 : t1;
       if (hi > pos) {
         f(j, s + j, pos, hi, b0, b1);
@@ -249,14 +259,14 @@ __device__ __forceinline__ void sums_pieces(const Seqs& q, const float* nll, con
       sum.w = warp_sum(sum.w);
       if (kValue) sum.x = warp_sum(sum.x);
       if (lane == 0) *(b0 < t0 ? out.head + c : (b1 > t1 ? out.tail + c : out.whole + s)) = sum;
-    }, [&](int s, int, int, int b0, int b1) {
+    }, [&](int s, int, int, int b0, int b1, bool mine) {
       Pair2 sum = {0.0, 0.0};
-      for (int t = b0; t < b1; ++t) {
+      for (int t = b0; mine && t < b1; ++t) {
         const float f = w ? __ldg(w + t) : 1.f;
         sum.w += (double)f;
         if (kValue && f != 0.f) sum.x += (double)f * ((ref ? (double)__ldg(ref + t) : 0.0) - (double)__ldg(nll + t));
       }
-      out.whole[s + lane] = sum;
+      if (mine) out.whole[s + lane] = sum;
     });
   }
 }
@@ -404,7 +414,7 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
           g[i] = in ? fs : g[i];
           A[i] = in && a.adv_per_seq ? as : A[i];
         }
-      }, [&](int, int lo, int hi, int, int b1) {
+      }, [&](int, int lo, int hi, int, int b1, bool) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int t = token_at(t0, i), j = lane_of(b1, t);
@@ -754,10 +764,10 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
         const bool in = (unsigned)(token_at(t0, i) - lo) < (unsigned)(hi - lo);
         if (in && w[i] != 0.f) g[i] = (float)(f * (double)w[i]);
       }
-    }, [&](int s, int lo, int hi, int b0, int b1) {
+    }, [&](int s, int lo, int hi, int b0, int b1, bool mine) {
       double own = coef;
       if (a.average) {
-        const double t = b1 > b0 ? q.whole[s + lane].w : 0.0;
+        const double t = mine && b1 > b0 ? q.whole[s + lane].w : 0.0;
         own = t > 0.0 ? own / t : 0.0;
       }
 #pragma unroll
