@@ -5,10 +5,10 @@
 // into pieces of 256: a lane holds eight tokens of a piece, two 16-byte loads per array where the
 // arrays are aligned to it, and a warp walks the sequences that lie in its pieces (adjacent ones, so
 // that the first sequence is searched for once, 32 probes a step).  A sequence inside a piece is
-// summed by its warp; one that crosses pieces leaves one partial sum per piece (`tail` where it
+// summed by its warp, a short one among others by a lane; one that crosses pieces leaves one partial sum per piece (`tail` where it
 // starts, `head` in each later piece), which its readers add in order.  The steps are device
 // functions:
-//  * batches of at most 32 pieces run them in one block, in one launch, with the sequences' sums in
+//  * small batches (at most 32 pieces) run them in one block, in one launch, with the sequences' sums in
 //    shared memory (7 sequences of 40 tokens: 13 us a call against 22 us for the chain, most of it
 //    the host's);
 //  * others in a chain of launches, each waiting for the one before (8192 sequences, 4.2 M tokens:
