@@ -126,7 +126,9 @@ struct Walker {
       if (pos == b0 && b1 <= t1 && b1 - b0 <= 32) {
         const int before = __shfl_up_sync(0xffffffffu, end, 1), lane = threadIdx.x & 31;
         const int begin = lane == 0 ? b0 : before;
-        const unsigned run = __ballot_sync(0xffffffffu, end <= t1 && end >= begin && end - begin <= 32) >> j;
+        // (a lane past the last sequence holds no end: t1 may be 0x7fffffff too)
+        const bool is_short = s + lane < q.B && end <= t1 && end >= begin && end - begin <= 32;
+        const unsigned run = __ballot_sync(0xffffffffu, is_short) >> j;
         const int n = run == 0xffffffffu ? 32 : __ffs(~run) - 1;  // sequences j .. j + n - 1 of the window
         if (n >= 4) {  // (8: 36 against 34 us)
           const int last = __shfl_sync(0xffffffffu, end, j + n - 1);

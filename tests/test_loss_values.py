@@ -1,0 +1,65 @@
+"""The losses on per-token NLLs at the ends of their range: infinities and NaN, slopes of very
+different size, cancelling sums, both ends of the one-block form, the largest sizes and other
+streams.  Formulas and tolerances as in test_losses.py."""
+import numpy as np
+import pytest
+import torch
+
+import packed_int4_lm_b200 as ah
+from test_losses import U, close, cu_dev, make_pairs, make_tokens, offsets, policy_ref, preference_ref
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def _largest(fill):
+    """A float array of the largest size, filled a slice at a time."""
+    N = 2 ** 31 - 1
+    x = torch.empty(N, device="cuda")
+    for n0 in range(0, N, 1 << 28):
+        n1 = min(N, n0 + (1 << 28))
+        x[n0:n1] = fill(torch.arange(n0, n1, device="cuda", dtype=torch.int64))
+    return x, N
+
+
+@pytest.mark.parametrize("average", [False])
+def test_losses_of_the_most_tokens(cuda_ok, average):
+    """2^31 - 1 tokens: one long sequence and five of one token behind it, whose last offsets are the
+    largest 32-bit number.  The values are multiples of 2^-10, so every sum is exact."""
+    nll, N = _largest(lambda i: ((i * 40503) & 1023).float() / 1024)
+    cu = torch.tensor([0] + [N - 5 + k for k in range(6)], dtype=torch.int64).to(torch.int32).cuda()
+    w = torch.ones(N, device="cuda")
+    parts = [slice(n0, min(N, n0 + (1 << 28))) for n0 in range(0, N, 1 << 28)]
+    last = nll[-5:].double().cpu().numpy()
+    total = sum(nll[p].double().sum().item() for p in parts) - last.sum()
+    pairs = torch.tensor([[0, 1], [2, 3], [4, 5], [5, 0]], dtype=torch.int32, device="cuda")
+    f = np.concatenate([[-total / (N - 5) if average else -total], -last])
+    beta = 1.0 if average else 2.0 ** -30
+    a, b = pairs.cpu().numpy().T
+    m = beta * (f[a] - f[b])
+    back = np.zeros(6)
+    np.add.at(back, a, -beta / (1 + np.exp(m)) / 4)
+    np.add.at(back, b, beta / (1 + np.exp(m)) / 4)
+    first = -back[0] / (N - 5 if average else 1)
+    for weights in (None, w):
+        got = ah.preference_loss(nll, cu, pairs, weights=weights, beta=beta, average=average)
+        ah.check()
+        for k, want in (("pair_loss", np.logaddexp(0, -m)), ("rewards", beta * np.stack([f[a], f[b]], 1))):
+            close(got[k], want, 1.001 * U * np.abs(want) + 1e-12, k)
+        g = got["dnll"]
+        close(g[-5:], -back[1:], 1.001 * U * np.abs(back[1:]) + 1e-12 * beta, "dnll")
+        for p in parts:
+            part = g[p.start:min(p.stop, N - 5)]
+            assert max(abs(part.min().item() - first), abs(part.max().item() - first)) <= 1.001 * U * abs(first)
+        del got, g, part
+    adv = torch.tensor([0.5, 1, -1, 2, -2, 3], device="cuda")
+    got = ah.policy_loss(nll, nll, adv, weights=w, cu_seqlens=cu, per_sequence=True, reduction="sequence")
+    ah.check()
+    g = got["dnll"]
+    close(g[-5:], np.array([1, -1, 2, -2, 3]) / 6, 4 * U, "policy dnll")
+    want = 0.5 / 6 / (N - 5)
+    assert abs(g[0].item() - want) <= 4 * U * want and abs(g[N - 6].item() - want) <= 4 * U * want
+    close(got["stats"], np.array([-3.5 / 6, -3.5 / 6, 0, 0]), 1e-6, "stats")
+    del got, g, nll, w
+    torch.cuda.empty_cache()
