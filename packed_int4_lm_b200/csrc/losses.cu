@@ -58,7 +58,7 @@ struct Seqs {
 };
 
 // Offset i, taken into [0, N].
-__device__ __forceinline__ int seq_at(const Seqs& q, int i) {
+__device__ __forceinline__ int seq_at(const Seqs& q, int64_t i) {
   const int c = __ldg(q.cu + i);
   return c < 0 ? 0 : (c > q.N ? q.N : c);
 }
@@ -80,8 +80,8 @@ __device__ __forceinline__ int warp_seq_of(const Seqs& q, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = q.B;  // of lo .. lo + n - 1 the first few begin at or before t
   while (n > 32) {
-    const int step = (n + 31) >> 5;
-    const int i = (lane + 1) * step - 1;
+    const int step = ((n - 1) >> 5) + 1;
+    const int64_t i = (lane + 1ll) * step - 1;  // (passes 2^31 with the most sequences)
     const bool in = i < n && seq_at(q, lo + i) <= t;
     const int c = __popc(__ballot_sync(0xffffffffu, in)) * step;
     lo += c;
@@ -101,33 +101,34 @@ template <typename W>
 struct Walker {
   const Seqs q;
   W window;
-  int s = 0, j = 0, b0 = 0, end = 0;  // the window's first sequence, the current one in it, its start
+  unsigned s = 0;  // the window's first sequence (unsigned: windows pass the last sequence, which may be 2^31 - 3)
+  int j = 0, b0 = 0, end = 0;  // the current one in it, its start
 
   __device__ __forceinline__ void load() {
-    const int i = s + (threadIdx.x & 31);
+    const unsigned i = s + (threadIdx.x & 31);
     end = 0x7fffffff;
-    if (i < q.B) {
-      end = seq_at(q, i + 1);
+    if (i < (unsigned)q.B) {
+      end = seq_at(q, i + 1ll);
       window(i);
     }
   }
   __device__ __forceinline__ Walker(const Seqs& seqs, int t0, W w) : q(seqs), window(w) {
     if (q.B == 0) return;
-    s = warp_seq_of(q, t0);
-    if (s < 0) s = 0;
+    const int first = warp_seq_of(q, t0);
+    s = first < 0 ? 0 : first;
     b0 = seq_at(q, s);
     load();
   }
   template <typename F, typename M>
   __device__ __forceinline__ void piece(int t0, int t1, F f, M many) {
     int pos = t0 < b0 ? b0 : t0;  // (tokens before the first sequence)
-    while (pos < t1 && s + j < q.B) {
+    while (pos < t1 && s + j < (unsigned)q.B) {
       const int b1 = __shfl_sync(0xffffffffu, end, j);
       if (pos == b0 && b1 <= t1 && b1 - b0 <= 32) {
         const int before = __shfl_up_sync(0xffffffffu, end, 1), lane = threadIdx.x & 31;
         const int begin = lane == 0 ? b0 : before;
         // (a lane past the last sequence holds no end: t1 may be 0x7fffffff too)
-        const bool is_short = s + lane < q.B && end <= t1 && end >= begin && end - begin <= 32;
+        const bool is_short = s + lane < (unsigned)q.B && end <= t1 && end >= begin && end - begin <= 32;
         const unsigned run = __ballot_sync(0xffffffffu, is_short) >> j;
         const int n = run == 0xffffffffu ? 32 : __ffs(~run) - 1;  // sequences j .. j + n - 1 of the window
         if (n >= 4) {  // (8: 36 against 34 us)

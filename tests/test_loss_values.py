@@ -63,3 +63,21 @@ def test_losses_of_the_most_tokens(cuda_ok, average):
     close(got["stats"], np.array([-3.5 / 6, -3.5 / 6, 0, 0]), 1e-6, "stats")
     del got, g, nll, w
     torch.cuda.empty_cache()
+
+
+def test_policy_of_the_most_sequences(cuda_ok):
+    """2^31 - 2 sequences, all empty but the last ones: what those ten alone give."""
+    B, N = 2 ** 31 - 2, 1000
+    nll, old, ref, w, rng = make_tokens(N, 51)
+    lens = [100] * 8 + [1, 199]
+    adv = rng.normal(size=N).astype(np.float32)
+    d = cu_dev(nll, old, adv, ref, offsets(lens))
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[-11:] = d[4]
+    want = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], cu_seqlens=d[4], kl_coef=0.1, reduction="sequence")
+    got = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], cu_seqlens=cu, kl_coef=0.1, reduction="sequence")
+    ah.check()
+    assert torch.equal(got["dnll"], want["dnll"])
+    close(got["stats"], want["stats"].cpu().double().numpy(), 2 * U * np.abs(want["stats"].cpu().double().numpy()) + 1e-9, "stats")
+    del cu
+    torch.cuda.empty_cache()
