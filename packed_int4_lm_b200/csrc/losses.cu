@@ -752,6 +752,10 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
   double coef = 0.0;  // of the window's sequence
   auto window = [&](int s) { coef = -slope_value(acc + (int64_t)s * kLimbs) * per_pair; };
   Walker<decltype(window)> walk(sq, c * kPiece, window);
+  // With `average`: the last sequence's weight.  A long one comes back in every piece of the warp; added
+  // up from its pieces each time, 2^31 tokens of one sequence took 100 s a call.
+  int weighed = -1;
+  double weight = 0.0;
   for (; c < c1; ++c) {
     const int t0 = c * kPiece, t1 = sq.N - t0 < kPiece ? sq.N : t0 + kPiece;
     float w[kPer], g[kPer] = {};
@@ -759,8 +763,11 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
     walk.piece(t0, t1, [&](int j, int s, int lo, int hi, int, int) {
       double f = __shfl_sync(0xffffffffu, coef, j);
       if (a.average) {
-        const double t = seq_total(q, sq, s, lane, 32).w;
-        f = t > 0.0 ? f / t : 0.0;
+        if (s != weighed) {
+          weight = seq_total(q, sq, s, lane, 32).w;
+          weighed = s;
+        }
+        f = weight > 0.0 ? f / weight : 0.0;
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {

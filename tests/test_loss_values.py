@@ -13,6 +13,24 @@ pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
 
 
+def test_preference_average_of_long_sequences(cuda_ok):
+    """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
+    piece of it."""
+    lens = [3, 5_000_000, 40, 3_000_001, 0, 2]
+    cu = offsets(lens)
+    N = int(cu[-1])
+    rng = np.random.default_rng(7)
+    nll = np.abs(rng.normal(size=N)).astype(np.float32)
+    w = rng.choice([0.0, 1.0, 0.5], size=N).astype(np.float32)
+    pairs = np.array([[1, 3], [0, 1], [3, 5], [2, 4]], dtype=np.int32)
+    want = preference_ref(nll, cu, pairs, None, w, 0.7, average=True)
+    d = cu_dev(nll, cu, pairs, w)
+    got = ah.preference_loss(d[0], d[1], d[2], weights=d[3], beta=0.7, average=True)
+    ah.check()
+    close(got["dnll"], want["dnll"], U * np.abs(want["dnll"]) + 1e-12 * want["size"], "dnll")
+    close(got["rewards"], want["rewards"], 1.001 * U * np.abs(want["rewards"]) + 1e-12, "rewards")
+
+
 def _largest(fill):
     """A float array of the largest size, filled a slice at a time."""
     N = 2 ** 31 - 1
@@ -23,7 +41,7 @@ def _largest(fill):
     return x, N
 
 
-@pytest.mark.parametrize("average", [False])
+@pytest.mark.parametrize("average", [False, True])
 def test_losses_of_the_most_tokens(cuda_ok, average):
     """2^31 - 1 tokens: one long sequence and five of one token behind it, whose last offsets are the
     largest 32-bit number.  The values are multiples of 2^-10, so every sum is exact."""
