@@ -15,6 +15,10 @@ and, to train what feeds the (frozen) head:
     nlls, lse = nll_lse(H_bf16, dh, targets)                    # forward
     out = policy_loss(nlls, nlls_old, advantages)               # or preference_loss(...)
     dH  = nll_grad(H_bf16, dh, targets, nlls, lse, out["dnll"]) # N x D bf16: H.backward(dH)
+
+These take a `stream` to run on instead of the current one.  The caller then orders the two: the
+inputs (and an `out` that is given) have to be ready on that stream, e.g. by stream.wait_stream,
+and the results are ready there.
 """
 from __future__ import annotations
 
@@ -257,14 +261,28 @@ def _run(name: str, dev: torch.device, stream, tensors, *args):
                 t.record_stream(stream)
 
 
+def _outputs(dev: torch.device, stream, make):
+    """The tensors that make() allocates for the results of a call on `stream`.  Where that is not
+    the current stream they are memory of its own pool: memory of the current stream's may still be
+    in use by work queued there.  The current stream is recorded as a user of them."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev.index):
+        return make()
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        out = make()
+    for t in out:
+        t.record_stream(current)
+    return out
+
+
 def _head_on(dh: DeviceHead, dev: torch.device):
     if dh.tensors["r_nib"].device != dev:
         raise ValueError(f"the head is on {dh.tensors['r_nib'].device}, the inputs are on {dev}")
 
 
-def _grad_out(out: Optional[torch.Tensor], N: int, dh: DeviceHead, dev) -> torch.Tensor:
+def _grad_out(out: Optional[torch.Tensor], N: int, dh: DeviceHead, dev, stream) -> torch.Tensor:
     if out is None:
-        return torch.empty((N, dh.D), device=dev, dtype=torch.bfloat16)
+        return _outputs(dev, stream, lambda: [torch.empty((N, dh.D), device=dev, dtype=torch.bfloat16)])[0]
     if (out.dtype != torch.bfloat16 or tuple(out.shape) != (N, dh.D) or out.device != dev
             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous bf16 tensor of shape ({N}, {dh.D}) on {dev}")
@@ -278,8 +296,7 @@ def nll_lse(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, stream=None)
     N, dev = H.shape[0], H.device
     _head_on(dh, dev)
     _int_array("targets", targets, (N,), dev)
-    out = torch.empty(N, device=dev, dtype=torch.float32)
-    lse = torch.empty(N, device=dev, dtype=torch.float32)
+    out, lse = _outputs(dev, stream, lambda: [torch.empty(N, device=dev, dtype=torch.float32) for _ in range(2)])
     _run("archead_nll_lse", dev, stream, (H, targets, out, lse), H.data_ptr(),
          ctypes.byref(dh.struct), targets.data_ptr(), out.data_ptr(), lse.data_ptr(), N,
          *dh.shape_args)
@@ -298,7 +315,7 @@ def nll_grad(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, nll: torch.
     _head_on(dh, dev)
     _int_array("targets", targets, (N,), dev)
     _float_arrays(N, dev, nll=nll, lse=lse, dnll=dnll)
-    out = _grad_out(out, N, dh, dev)
+    out = _grad_out(out, N, dh, dev, stream)
     _run("archead_nll_grad", dev, stream, (H, targets, nll, lse, dnll, out), H.data_ptr(),
          ctypes.byref(dh.struct), targets.data_ptr(), nll.data_ptr(), lse.data_ptr(),
          dnll.data_ptr(), out.data_ptr(), N, *dh.shape_args)
@@ -314,7 +331,7 @@ def logits_grad(dY: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = 
         raise ValueError(f"dY must be a contiguous float32 CUDA tensor of shape (N, {dh.V})")
     N, dev = dY.shape[0], dY.device
     _head_on(dh, dev)
-    out = _grad_out(out, N, dh, dev)
+    out = _grad_out(out, N, dh, dev, stream)
     _run("archead_logits_grad", dev, stream, (dY, out), dY.data_ptr(), ctypes.byref(dh.struct),
          out.data_ptr(), N, *dh.shape_args)
     return out
@@ -354,7 +371,7 @@ def policy_loss(nll: torch.Tensor, nll_old: torch.Tensor, advantages: torch.Tens
         raise ValueError("per_sequence advantages and the sequence reduction need cu_seqlens")
     _float_arrays(N, dev, nll=nll, nll_old=nll_old, nll_ref=nll_ref, weights=weights)
     _float_arrays(B if per_sequence else N, dev, advantages=advantages)
-    dnll, stats = nll.new_empty(N), nll.new_empty(4)
+    dnll, stats = _outputs(dev, stream, lambda: [nll.new_empty(N), nll.new_empty(4)])
     _run("archead_policy_loss", dev, stream,
          (nll, nll_old, nll_ref, advantages, weights, cu_seqlens, dnll, stats),
          nll.data_ptr(), nll_old.data_ptr(), _optional(nll_ref), advantages.data_ptr(),
@@ -383,8 +400,8 @@ def preference_loss(nll: torch.Tensor, cu_seqlens: torch.Tensor, pairs: torch.Te
         raise ValueError("pairs must be an int32 tensor of shape (P, 2)")
     P = pairs.shape[0]
     _int_array("pairs", pairs, (P, 2), dev)
-    dnll, loss = nll.new_empty(N), nll.new_empty(1)
-    pair_loss, rewards = nll.new_empty(P), nll.new_empty(P, 2)
+    dnll, loss, pair_loss, rewards = _outputs(
+        dev, stream, lambda: [nll.new_empty(N), nll.new_empty(1), nll.new_empty(P), nll.new_empty(P, 2)])
     _run("archead_preference_loss", dev, stream,
          (nll, nll_ref, weights, cu_seqlens, pairs, dnll, loss, pair_loss, rewards),
          nll.data_ptr(), _optional(nll_ref), _optional(weights), cu_seqlens.data_ptr(),

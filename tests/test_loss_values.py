@@ -99,3 +99,48 @@ def test_policy_of_the_most_sequences(cuda_ok):
     close(got["stats"], want["stats"].cpu().double().numpy(), 2 * U * np.abs(want["stats"].cpu().double().numpy()) + 1e-9, "stats")
     del cu
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("which", ["policy", "preference", "nll_lse", "nll_grad", "logits_grad"])
+def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, which):
+    """A call on another stream while the current one still has work that writes a freed tensor of
+    the outputs' size: the outputs do not lie there."""
+    from test_head_grad import head_of, make_dY
+    head, W, M = head_of("g64")
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    N = 200
+    nll, old, ref, w, rng = make_tokens(N, 61)
+    d = cu_dev(nll, old, rng.normal(size=N).astype(np.float32), offsets([100, 100]), np.array([[0, 1]], dtype=np.int32))
+    H = torch.from_numpy(rng.normal(size=(N, head["D"]))).to(torch.bfloat16).cuda()
+    t = torch.from_numpy(rng.integers(0, head["V"], size=N).astype(np.int32)).cuda()
+    nl, ls = ah.nll_lse(H, dh, t)
+    dY = torch.from_numpy(make_dY(N, head["V"], 3)).cuda()
+    side = torch.cuda.Stream()
+
+    def call(stream=None):
+        if which == "policy":
+            return list(ah.policy_loss(d[0], d[1], d[2], stream=stream).values())
+        if which == "preference":
+            return list(ah.preference_loss(d[0], d[3], d[4], stream=stream).values())
+        if which == "nll_lse":
+            return list(ah.nll_lse(H, dh, t, stream=stream))
+        if which == "nll_grad":
+            return [ah.nll_grad(H, dh, t, nl, ls, d[2], stream=stream)]
+        return [ah.logits_grad(dY, dh, stream=stream)]
+
+    want = [o.clone() for o in call()]
+    call(side)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    old_memory = [torch.empty_like(o) for o in want]
+    for o in old_memory:
+        o.fill_(NAN)
+    addresses = {o.data_ptr() for o in old_memory}
+    del o, old_memory
+    got = call(side)
+    assert addresses.isdisjoint(o.data_ptr() for o in got)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    ah.check()
