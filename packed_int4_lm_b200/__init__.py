@@ -243,7 +243,7 @@ def _run(name: str, dev: torch.device, stream, tensors, *args):
     """One call into the library for tensors on dev: that device is made current around it (the
     library works on the current device), the stream is the given one or dev's current one, and
     on a stream other than the current one the tensors are recorded (their memory may not be
-    handed out again before that stream is done with it)."""
+    handed out again before that stream is done with it).  A call through a head lists the head's."""
     # (torch.cuda.current_stream builds a Stream object first: 2 us, a fifth of a small call)
     current = torch._C._cuda_getCurrentRawStream(dev.index)
     handle = current if stream is None else stream.cuda_stream
@@ -297,7 +297,7 @@ def nll_lse(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, stream=None)
     _head_on(dh, dev)
     _int_array("targets", targets, (N,), dev)
     out, lse = _outputs(dev, stream, lambda: [torch.empty(N, device=dev, dtype=torch.float32) for _ in range(2)])
-    _run("archead_nll_lse", dev, stream, (H, targets, out, lse), H.data_ptr(),
+    _run("archead_nll_lse", dev, stream, (H, targets, out, lse, *dh.tensors.values()), H.data_ptr(),
          ctypes.byref(dh.struct), targets.data_ptr(), out.data_ptr(), lse.data_ptr(), N,
          *dh.shape_args)
     return out, lse
@@ -316,8 +316,8 @@ def nll_grad(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, nll: torch.
     _int_array("targets", targets, (N,), dev)
     _float_arrays(N, dev, nll=nll, lse=lse, dnll=dnll)
     out = _grad_out(out, N, dh, dev, stream)
-    _run("archead_nll_grad", dev, stream, (H, targets, nll, lse, dnll, out), H.data_ptr(),
-         ctypes.byref(dh.struct), targets.data_ptr(), nll.data_ptr(), lse.data_ptr(),
+    _run("archead_nll_grad", dev, stream, (H, targets, nll, lse, dnll, out, *dh.tensors.values()),
+         H.data_ptr(), ctypes.byref(dh.struct), targets.data_ptr(), nll.data_ptr(), lse.data_ptr(),
          dnll.data_ptr(), out.data_ptr(), N, *dh.shape_args)
     return out
 
@@ -332,8 +332,8 @@ def logits_grad(dY: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = 
     N, dev = dY.shape[0], dY.device
     _head_on(dh, dev)
     out = _grad_out(out, N, dh, dev, stream)
-    _run("archead_logits_grad", dev, stream, (dY, out), dY.data_ptr(), ctypes.byref(dh.struct),
-         out.data_ptr(), N, *dh.shape_args)
+    _run("archead_logits_grad", dev, stream, (dY, out, *dh.tensors.values()), dY.data_ptr(),
+         ctypes.byref(dh.struct), out.data_ptr(), N, *dh.shape_args)
     return out
 
 

@@ -144,3 +144,42 @@ def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, w
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     ah.check()
+
+
+@pytest.mark.parametrize("which", ["nll_lse", "nll_grad", "logits_grad"])
+def test_a_head_that_is_dropped_after_a_call_on_another_stream(cuda_ok, which):
+    """The head's memory is not handed out again while a stream that was given still reads it."""
+    from test_head_grad import HEADS, make_dY
+    head = HEADS["g64"]()
+    N, V, D = 40, head["V"], head["D"]
+    rng = np.random.default_rng(3)
+    H = torch.from_numpy(rng.normal(size=(N, D))).to(torch.bfloat16).cuda()
+    t = torch.from_numpy(rng.integers(0, V, size=N).astype(np.int32)).cuda()
+    dn = torch.from_numpy(rng.normal(size=N).astype(np.float32)).cuda()
+    dY = torch.from_numpy(make_dY(N, V, 3)).cuda()
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    nl, ls = ah.nll_lse(H, dh, t)
+    side = torch.cuda.Stream()
+
+    def call(dh, stream=None):
+        if which == "nll_lse":
+            return list(ah.nll_lse(H, dh, t, stream=stream))
+        if which == "nll_grad":
+            return [ah.nll_grad(H, dh, t, nl, ls, dn, stream=stream)]
+        return [ah.logits_grad(dY, dh, stream=stream)]
+
+    want = [o.clone() for o in call(dh)]
+    call(dh, side)
+    torch.cuda.synchronize()
+    shapes = [(x.shape, x.dtype) for x in dh.tensors.values()]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    got = call(dh, side)
+    used = {x.data_ptr() for x in dh.tensors.values()}
+    del dh
+    again = [torch.full(s, 1, dtype=d, device="cuda") for s, d in shapes]
+    assert used.isdisjoint(x.data_ptr() for x in again)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    ah.check()
