@@ -16,7 +16,7 @@ and, to train what feeds the (frozen) head:
     out = policy_loss(nlls, nlls_old, advantages)               # or preference_loss(...)
     dH  = nll_grad(H_bf16, dh, targets, nlls, lse, out["dnll"]) # N x D bf16: H.backward(dH)
 
-These take a `stream` to run on instead of the current one.  The caller then orders the two: the
+All of them take a `stream` to run on instead of the current one.  The caller then orders the two: the
 inputs (and an `out` that is given) have to be ready on that stream, e.g. by stream.wait_stream,
 and the results are ready there.
 """
@@ -115,126 +115,6 @@ def _check_H(H: torch.Tensor, dh: DeviceHead):
         raise ValueError("H must be a contiguous CUDA tensor")
 
 
-def logits(H: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = None,
-           stream=None) -> torch.Tensor:
-    """Y = H W_d^T + (H B_w^T) A_w^T (N x V float32), asynchronous on the stream."""
-    _check_H(H, dh)
-    N = H.shape[0]
-    if out is None:
-        out = torch.empty(N, dh.V, device=H.device, dtype=torch.float32)
-    _lib.check(_lib.lib().archead_logits(H.data_ptr(), ctypes.byref(dh.struct),
-                                         out.data_ptr() if N else None, N, *dh.shape_args,
-                                         _stream_handle(stream)), "archead_logits")
-    return out
-
-
-def nll(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor,
-        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Per-token NLL (nats) = logsumexp(Y[n]) - Y[n, target[n]], without writing Y."""
-    _check_H(H, dh)
-    N = H.shape[0]
-    if targets.dtype != torch.int32 or targets.shape != (N,) or not targets.is_cuda:
-        raise ValueError("targets must be an int32 CUDA tensor of shape (N,)")
-    if out is None:
-        out = torch.empty(N, device=H.device, dtype=torch.float32)
-    _lib.check(_lib.lib().archead_nll(H.data_ptr(), ctypes.byref(dh.struct),
-                                      targets.contiguous().data_ptr(),
-                                      out.data_ptr() if N else None, N, *dh.shape_args,
-                                      _stream_handle(stream)), "archead_nll")
-    return out
-
-
-def nll_partials(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, v_begin: int,
-                 v_total: int, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """archead_nll_partials: this vocabulary shard's (max, sum exp, target logit) per token
-    (N x 3 float32).  dh holds rows [v_begin, v_begin + dh.V) of a v_total-row head."""
-    _check_H(H, dh)
-    N = H.shape[0]
-    if targets.dtype != torch.int32 or targets.shape != (N,) or not targets.is_cuda:
-        raise ValueError("targets must be an int32 CUDA tensor of shape (N,)")
-    if out is None:
-        out = torch.empty(N, 3, device=H.device, dtype=torch.float32)
-    _lib.check(_lib.lib().archead_nll_partials(H.data_ptr(), ctypes.byref(dh.struct),
-                                               targets.contiguous().data_ptr(), int(v_begin),
-                                               int(v_total), out.data_ptr() if N else None, N,
-                                               *dh.shape_args, _stream_handle(stream)),
-               "archead_nll_partials")
-    return out
-
-
-def nll_merge(partials: torch.Tensor, out: Optional[torch.Tensor] = None,
-              stream=None) -> torch.Tensor:
-    """archead_nll_merge: per-token NLL from G shards' partials (G x N x 3 float32 CUDA)."""
-    if (partials.dtype != torch.float32 or partials.dim() != 3 or partials.shape[2] != 3
-            or not partials.is_cuda):
-        raise ValueError("partials must be a float32 CUDA tensor of shape (G, N, 3)")
-    G, N = int(partials.shape[0]), int(partials.shape[1])
-    p = partials.contiguous()
-    if out is None:
-        out = torch.empty(N, device=partials.device, dtype=torch.float32)
-    _lib.check(_lib.lib().archead_nll_merge(p.data_ptr(), G, N, out.data_ptr() if N else None,
-                                            _stream_handle(stream)), "archead_nll_merge")
-    return out
-
-
-def vocab_parallel_nll(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, v_begin: int,
-                       v_total: int, group=None) -> torch.Tensor:
-    """Per-token NLL of a head whose vocabulary rows are sharded over the ranks of `group`
-    (rank k holds dh = rows [v_begin, v_begin + dh.V)): each rank reduces its shard to
-    (max, sum exp, target logit) per token, one all-gather exchanges the N x 3 partials,
-    and every rank merges them in rank order.  H and targets are the same on every rank."""
-    import torch.distributed as dist
-    part = nll_partials(H, dh, targets, v_begin, v_total)
-    if not (dist.is_available() and dist.is_initialized()):  # one process holds the head
-        return nll_merge(part[None])
-    G = dist.get_world_size(group)
-    if dist.get_backend(group) == "gloo":  # host collectives (tests without NCCL)
-        host = part.cpu()
-        gathered = [torch.empty_like(host) for _ in range(G)]
-        dist.all_gather(gathered, host, group=group)
-        return nll_merge(torch.stack(gathered).to(part.device))
-    gathered = [torch.empty_like(part) for _ in range(G)]
-    dist.all_gather(gathered, part, group=group)
-    return nll_merge(torch.stack(gathered))
-
-
-def agreement(H: torch.Tensor, dh: DeviceHead, Y_dense: torch.Tensor, k: int = 10,
-              stream=None) -> dict:
-    """archead_agreement: per token the ids of the k largest packed logits ("topk", N x k
-    int32, decreasing, equal logits by smaller id), the dense argmax ("top1_dense", N),
-    KL(P_dense || P_packed) in nats ("kl", N) and the packed log-sum-exp ("lse", N), all
-    on the device.  Y_dense: N x V float32 reference logits on the same device."""
-    _check_H(H, dh)
-    N = H.shape[0]
-    if (Y_dense.dtype != torch.float32 or tuple(Y_dense.shape) != (N, dh.V)
-            or not Y_dense.is_cuda or not Y_dense.is_contiguous()):
-        raise ValueError(f"Y_dense must be a contiguous float32 CUDA tensor of shape ({N}, {dh.V})")
-    dev = H.device
-    out = {"topk": torch.empty(N, k, dtype=torch.int32, device=dev),
-           "top1_dense": torch.empty(N, dtype=torch.int32, device=dev),
-           "kl": torch.empty(N, dtype=torch.float32, device=dev),
-           "lse": torch.empty(N, dtype=torch.float32, device=dev)}
-    _lib.check(_lib.lib().archead_agreement(
-        H.data_ptr(), ctypes.byref(dh.struct), Y_dense.data_ptr(), int(k),
-        *[out[x].data_ptr() if N else None for x in ("topk", "top1_dense", "kl", "lse")],
-        N, *dh.shape_args, _stream_handle(stream)), "archead_agreement")
-    return out
-
-
-def _float_arrays(N: int, dev, **arrays):
-    """Checks that each given array is a contiguous float32 CUDA tensor of shape (N,) on dev."""
-    for name, t in arrays.items():
-        if t is not None and (t.dtype is not torch.float32 or t.shape != (N,) or t.device != dev
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({N},) on {dev}")
-
-
-def _int_array(name: str, t: torch.Tensor, shape, dev):
-    if (t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != dev
-            or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
-
-
 def _optional(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -273,6 +153,123 @@ def _outputs(dev: torch.device, stream, make):
     for t in out:
         t.record_stream(current)
     return out
+
+
+def logits(H: torch.Tensor, dh: DeviceHead, out: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """Y = H W_d^T + (H B_w^T) A_w^T (N x V float32), asynchronous on the stream."""
+    _check_H(H, dh)
+    N, dev = H.shape[0], H.device
+    if out is None:
+        out, = _outputs(dev, stream, lambda: [torch.empty(N, dh.V, device=dev, dtype=torch.float32)])
+    _run("archead_logits", dev, stream, (H, out, *dh.tensors.values()), H.data_ptr(),
+         ctypes.byref(dh.struct), out.data_ptr() if N else None, N, *dh.shape_args)
+    return out
+
+
+def nll(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor,
+        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Per-token NLL (nats) = logsumexp(Y[n]) - Y[n, target[n]], without writing Y."""
+    _check_H(H, dh)
+    N = H.shape[0]
+    if targets.dtype != torch.int32 or targets.shape != (N,) or not targets.is_cuda:
+        raise ValueError("targets must be an int32 CUDA tensor of shape (N,)")
+    if out is None:
+        out, = _outputs(H.device, stream, lambda: [torch.empty(N, device=H.device, dtype=torch.float32)])
+    targets, = _outputs(H.device, stream, lambda: [targets.contiguous()])
+    _run("archead_nll", H.device, stream, (H, targets, out, *dh.tensors.values()), H.data_ptr(),
+         ctypes.byref(dh.struct), targets.data_ptr(), out.data_ptr() if N else None, N,
+         *dh.shape_args)
+    return out
+
+
+def nll_partials(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, v_begin: int,
+                 v_total: int, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """archead_nll_partials: this vocabulary shard's (max, sum exp, target logit) per token
+    (N x 3 float32).  dh holds rows [v_begin, v_begin + dh.V) of a v_total-row head."""
+    _check_H(H, dh)
+    N = H.shape[0]
+    if targets.dtype != torch.int32 or targets.shape != (N,) or not targets.is_cuda:
+        raise ValueError("targets must be an int32 CUDA tensor of shape (N,)")
+    if out is None:
+        out, = _outputs(H.device, stream, lambda: [torch.empty(N, 3, device=H.device, dtype=torch.float32)])
+    targets, = _outputs(H.device, stream, lambda: [targets.contiguous()])
+    _run("archead_nll_partials", H.device, stream, (H, targets, out, *dh.tensors.values()),
+         H.data_ptr(), ctypes.byref(dh.struct), targets.data_ptr(), int(v_begin), int(v_total),
+         out.data_ptr() if N else None, N, *dh.shape_args)
+    return out
+
+
+def nll_merge(partials: torch.Tensor, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """archead_nll_merge: per-token NLL from G shards' partials (G x N x 3 float32 CUDA)."""
+    if (partials.dtype != torch.float32 or partials.dim() != 3 or partials.shape[2] != 3
+            or not partials.is_cuda):
+        raise ValueError("partials must be a float32 CUDA tensor of shape (G, N, 3)")
+    G, N = int(partials.shape[0]), int(partials.shape[1])
+    dev = partials.device
+    p, = _outputs(dev, stream, lambda: [partials.contiguous()])
+    if out is None:
+        out, = _outputs(dev, stream, lambda: [torch.empty(N, device=dev, dtype=torch.float32)])
+    _run("archead_nll_merge", dev, stream, (p, out), p.data_ptr(), G, N, out.data_ptr() if N else None)
+    return out
+
+
+def vocab_parallel_nll(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, v_begin: int,
+                       v_total: int, group=None) -> torch.Tensor:
+    """Per-token NLL of a head whose vocabulary rows are sharded over the ranks of `group`
+    (rank k holds dh = rows [v_begin, v_begin + dh.V)): each rank reduces its shard to
+    (max, sum exp, target logit) per token, one all-gather exchanges the N x 3 partials,
+    and every rank merges them in rank order.  H and targets are the same on every rank."""
+    import torch.distributed as dist
+    part = nll_partials(H, dh, targets, v_begin, v_total)
+    if not (dist.is_available() and dist.is_initialized()):  # one process holds the head
+        return nll_merge(part[None])
+    G = dist.get_world_size(group)
+    if dist.get_backend(group) == "gloo":  # host collectives (tests without NCCL)
+        host = part.cpu()
+        gathered = [torch.empty_like(host) for _ in range(G)]
+        dist.all_gather(gathered, host, group=group)
+        return nll_merge(torch.stack(gathered).to(part.device))
+    gathered = [torch.empty_like(part) for _ in range(G)]
+    dist.all_gather(gathered, part, group=group)
+    return nll_merge(torch.stack(gathered))
+
+
+def agreement(H: torch.Tensor, dh: DeviceHead, Y_dense: torch.Tensor, k: int = 10,
+              stream=None) -> dict:
+    """archead_agreement: per token the ids of the k largest packed logits ("topk", N x k
+    int32, decreasing, equal logits by smaller id), the dense argmax ("top1_dense", N),
+    KL(P_dense || P_packed) in nats ("kl", N) and the packed log-sum-exp ("lse", N), all
+    on the device.  Y_dense: N x V float32 reference logits on the same device."""
+    _check_H(H, dh)
+    N = H.shape[0]
+    if (Y_dense.dtype != torch.float32 or tuple(Y_dense.shape) != (N, dh.V)
+            or not Y_dense.is_cuda or not Y_dense.is_contiguous()):
+        raise ValueError(f"Y_dense must be a contiguous float32 CUDA tensor of shape ({N}, {dh.V})")
+    dev = H.device
+    names = ("topk", "top1_dense", "kl", "lse")
+    out = dict(zip(names, _outputs(dev, stream, lambda: [
+        torch.empty(N, k, dtype=torch.int32, device=dev), torch.empty(N, dtype=torch.int32, device=dev),
+        torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev)])))
+    _run("archead_agreement", dev, stream, (H, Y_dense, *out.values(), *dh.tensors.values()),
+         H.data_ptr(), ctypes.byref(dh.struct), Y_dense.data_ptr(), int(k),
+         *[out[x].data_ptr() if N else None for x in names], N, *dh.shape_args)
+    return out
+
+
+def _float_arrays(N: int, dev, **arrays):
+    """Checks that each given array is a contiguous float32 CUDA tensor of shape (N,) on dev."""
+    for name, t in arrays.items():
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (N,) or t.device != dev
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({N},) on {dev}")
+
+
+def _int_array(name: str, t: torch.Tensor, shape, dev):
+    if (t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != dev
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
 
 
 def _head_on(dh: DeviceHead, dev: torch.device):

@@ -101,7 +101,8 @@ def test_policy_of_the_most_sequences(cuda_ok):
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("which", ["policy", "preference", "nll_lse", "nll_grad", "logits_grad"])
+@pytest.mark.parametrize("which", ["policy", "preference", "nll_lse", "nll_grad", "logits_grad", "logits", "nll",
+                                   "nll_partials", "nll_merge", "agreement"])
 def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, which):
     """A call on another stream while the current one still has work that writes a freed tensor of
     the outputs' size: the outputs do not lie there."""
@@ -115,6 +116,7 @@ def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, w
     t = torch.from_numpy(rng.integers(0, head["V"], size=N).astype(np.int32)).cuda()
     nl, ls = ah.nll_lse(H, dh, t)
     dY = torch.from_numpy(make_dY(N, head["V"], 3)).cuda()
+    t2, part = torch.stack([t, t], 1), ah.nll_partials(H, dh, t, 0, head["V"])
     side = torch.cuda.Stream()
 
     def call(stream=None):
@@ -126,7 +128,17 @@ def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, w
             return list(ah.nll_lse(H, dh, t, stream=stream))
         if which == "nll_grad":
             return [ah.nll_grad(H, dh, t, nl, ls, d[2], stream=stream)]
-        return [ah.logits_grad(dY, dh, stream=stream)]
+        if which == "logits_grad":
+            return [ah.logits_grad(dY, dh, stream=stream)]
+        if which == "logits":
+            return [ah.logits(H, dh, stream=stream)]
+        if which == "nll":  # (a copy of the targets is made on the way)
+            return [ah.nll(H, dh, t2[:, 0], stream=stream)]
+        if which == "nll_partials":
+            return [ah.nll_partials(H, dh, t2[:, 0], 0, head["V"], stream=stream)]
+        if which == "nll_merge":
+            return [ah.nll_merge(part[None], stream=stream)]
+        return list(ah.agreement(H, dh, dY, stream=stream).values())
 
     want = [o.clone() for o in call()]
     call(side)
@@ -134,7 +146,7 @@ def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, w
     torch.cuda._sleep(100_000_000)  # some 50 ms
     old_memory = [torch.empty_like(o) for o in want]
     for o in old_memory:
-        o.fill_(NAN)
+        o.fill_(-7)
     addresses = {o.data_ptr() for o in old_memory}
     del o, old_memory
     got = call(side)
