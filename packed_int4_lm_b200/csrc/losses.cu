@@ -353,7 +353,7 @@ __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A,
     o.clipped = up ? d > k.log_hi : A < 0.f && d < k.log_lo;
   } else {
     const float l = up ? k.log_hi_f : -k.log_lo_f, y = up ? x : -x;
-    o.clipped = y > l && A != 0.f;
+    o.clipped = y > l && (up || A < 0.f);  // (not for a NaN)
     border |= y == l;
   }
   const float r = A == 0.f ? 0.f : exp_f(x) * A;  // (0 times an infinite ratio is 0 here)

@@ -13,6 +13,29 @@ pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
 
 
+@pytest.mark.parametrize("border", [False, True])
+def test_policy_nan_advantage_is_nan_on_every_side_of_the_border(cuda_ok, border):
+    """A token whose advantage is NaN gets NaN wherever its ratio lies, and is not clipped, whether
+    or not a token beside it lies on the clip border; no other token changes."""
+    nll, old, ref, w, rng = make_tokens(300, 31)
+    x = rng.choice([-2.0, -0.1, 0.1, 2.0], size=300)
+    old = (nll + x).astype(np.float32)
+    adv = rng.normal(size=300).astype(np.float32)
+    if border:
+        nll[::64], old[::64], adv[::64] = 0, np.float32(np.log1p(0.2)), 1
+    bad = np.arange(300) % 7 == 3
+    assert (x[bad] == -2.0).any() and (x[bad] == 2.0).any()
+    d = cu_dev(nll, old, adv, np.where(bad, np.float32(np.nan), adv), (~bad).astype(np.float32))
+    kw = dict(clip_low=0.2, clip_high=0.2, reduction="sum")
+    want = ah.policy_loss(d[0], d[1], d[2], weights=d[4], **kw)
+    got = ah.policy_loss(d[0], d[1], d[3], **kw)
+    ah.check()
+    g, b = got["dnll"].cpu().numpy(), want["dnll"].cpu().numpy()
+    assert np.isnan(g[bad]).all()
+    assert (g[~bad] == b[~bad]).all()
+    assert torch.isnan(got["stats"][:2]).all() and got["stats"][3] == want["stats"][3]
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
