@@ -201,6 +201,7 @@ enum archead_reduction {
  *   (which needs cu_seqlens, as ARCHEAD_REDUCE_SEQUENCE does).  All on the device.
  *   dnll float N (device): the loss's derivative by each token's NLL; where the clipped side
  *   is the smaller one the surrogate's derivative is 0 (at the border itself it is not).
+ *   A token with A = 0 adds nothing to the surrogate, also where r is infinite.
  *   stats float 4 (device): the loss, the surrogate's and the KL term's (before kl_coef)
  *   shares of it, and the share of the weight whose surrogate is clipped, all reduced alike.
  *   A token with weight 0, or outside every sequence, is masked: nothing else of it is used

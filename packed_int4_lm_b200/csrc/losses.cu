@@ -356,7 +356,8 @@ __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A,
     o.clipped = y > l && (up || A < 0.f);  // (not for a NaN)
     border |= y == l;
   }
-  const float r = A == 0.f ? 0.f : exp_f(x) * A;  // (0 times an infinite ratio is 0 here)
+  // (0 times an infinite ratio is 0 here; a NaN stays one)
+  const float r = A == 0.f ? (x != x ? x : 0.f) : exp_f(x) * A;
   o.grad = o.clipped ? 0.f : r;
   o.sur = o.clipped ? (up ? k.hi : k.lo) * A : r;
   o.kl = 0.f;

@@ -36,6 +36,21 @@ def test_policy_nan_advantage_is_nan_on_every_side_of_the_border(cuda_ok, border
     assert torch.isnan(got["stats"][:2]).all() and got["stats"][3] == want["stats"][3]
 
 
+def test_policy_advantage_zero_keeps_a_nan(cuda_ok):
+    """Advantage 0 times an infinite ratio is 0; a NaN log-probability stays NaN."""
+    nll = np.array([NAN, 1, 0, -np.inf, 2], dtype=np.float32)
+    old = np.array([1, NAN, 500, 1, 2], dtype=np.float32)
+    d = cu_dev(nll, old, np.zeros(5, dtype=np.float32))
+    got = ah.policy_loss(*d, reduction="sum")
+    ah.check()
+    g = got["dnll"].cpu().numpy()
+    assert np.isnan(g[:2]).all() and not g[2:].any()
+    assert torch.isnan(got["stats"][:2]).all()
+    good = ah.policy_loss(*[t[2:].contiguous() for t in d], reduction="sum")
+    ah.check()
+    assert good["stats"].tolist() == [0] * 4
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
