@@ -364,7 +364,8 @@ __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A,
   if (has_ref) {
     const float z = nll - ref;
     o.kl = kl_term(z);
-    o.grad = fmaf(k.kl_coef, z + o.kl, o.grad);  // e^z - 1 = z + k
+    // e^z - 1 = z + k (without a coefficient the term is only reported, and may be infinite)
+    if (k.kl_coef != 0.f) o.grad = fmaf(k.kl_coef, z + o.kl, o.grad);
   }
   return o;
 }

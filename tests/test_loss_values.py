@@ -51,6 +51,22 @@ def test_policy_advantage_zero_keeps_a_nan(cuda_ok):
     assert good["stats"].tolist() == [0] * 4
 
 
+def test_policy_reference_without_a_coefficient_leaves_the_gradient(cuda_ok):
+    """With kl_coef = 0 the reference is only reported: the loss and its gradient are the
+    surrogate's, whatever the KL term is."""
+    nll, old, ref, w, rng = make_tokens(600, 33)
+    adv = rng.normal(size=600).astype(np.float32)
+    ref[::3] = (nll - rng.choice([100, 89, 1e30], size=600).astype(np.float32))[::3]
+    ref[1::7] = rng.choice([np.nan, np.inf, -np.inf], size=600)[1::7]
+    d = cu_dev(nll, old, adv, ref)
+    for reduction in ("sum", "token"):
+        want = ah.policy_loss(d[0], d[1], d[2], reduction=reduction)
+        got = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], kl_coef=0.0, reduction=reduction)
+        ah.check()
+        assert torch.equal(got["dnll"], want["dnll"])
+        assert torch.equal(got["stats"][[0, 1, 3]], want["stats"][[0, 1, 3]])
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
