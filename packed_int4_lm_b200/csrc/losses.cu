@@ -322,9 +322,9 @@ __device__ __forceinline__ float exp_f(float x) {
   return y;
 }
 
-// k = e^z - 1 - z.  Near 0, where the difference cancels, z^2 times its Taylor series (the first
-// term left out is below 2^-24 of the sum at |z| = 1).
-__device__ __forceinline__ float kl_term(float z) {
+// k = e^z - 1 - z and its derivative d = e^z - 1.  Near 0, where the differences cancel, k is z^2 times
+// its Taylor series (the first term left out is below 2^-24 of the sum at |z| = 1) and d = z + k.
+__device__ __forceinline__ void kl_term(float z, float* k, float* d) {
   float p = 1.f / 479001600;
   p = fmaf(p, z, 1.f / 39916800);
   p = fmaf(p, z, 1.f / 3628800);
@@ -336,7 +336,10 @@ __device__ __forceinline__ float kl_term(float z) {
   p = fmaf(p, z, 1.f / 24);
   p = fmaf(p, z, 1.f / 6);
   p = fmaf(p, z, 0.5f);
-  return fabsf(z) < 1.f ? z * z * p : exp_f(z) - 1.f - z;
+  const bool near = fabsf(z) < 1.f;
+  const float up = exp_f(z) - 1.f, small = z * z * p;
+  *k = near ? small : up - z;
+  *d = near ? z + small : up;
 }
 
 // The side of the clip border is that of the exact difference old - nll against log(1 +- clip).
@@ -362,10 +365,10 @@ __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A,
   o.sur = o.clipped ? (up ? k.hi : k.lo) * A : r;
   o.kl = 0.f;
   if (has_ref) {
-    const float z = nll - ref;
-    o.kl = kl_term(z);
-    // e^z - 1 = z + k (without a coefficient the term is only reported, and may be infinite)
-    if (k.kl_coef != 0.f) o.grad = fmaf(k.kl_coef, z + o.kl, o.grad);
+    float d;
+    kl_term(nll - ref, &o.kl, &d);
+    // (without a coefficient the term is only reported, and may be infinite)
+    if (k.kl_coef != 0.f) o.grad = fmaf(k.kl_coef, d, o.grad);
   }
   return o;
 }

@@ -51,6 +51,26 @@ def test_policy_advantage_zero_keeps_a_nan(cuda_ok):
     assert good["stats"].tolist() == [0] * 4
 
 
+def test_policy_infinite_reference(cuda_ok):
+    """nll_ref = +inf: z = -inf, the KL term e^z - z - 1 is infinite and its derivative e^z - 1 is -1.
+    Far below 0 the derivative keeps its precision."""
+    nll, old, ref, w, rng = make_tokens(40, 32)
+    adv = rng.normal(size=40).astype(np.float32)
+    ref[5] = np.inf
+    ref[6:12] = nll[6:12] + np.array([1.5, 4, 20, 90, 1e4, 3e38], dtype=np.float32)
+    d = cu_dev(nll, old, adv, ref)
+    got = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], kl_coef=0.5, reduction="sum", clip_low=0.9, clip_high=9)
+    ah.check()
+    r = np.exp(old.astype(np.float64) - nll)
+    z = nll.astype(np.float64) - ref
+    want = r * adv + 0.5 * np.expm1(z)
+    # half steps: |z| of the difference inside exp times e^z, a few of exp and the products
+    size = (np.abs(old.astype(np.float64) - nll) + 8) * r * np.abs(adv) + 0.5 * ((np.minimum(np.abs(z), 1e3) + 8) * np.exp(z) + 4)
+    close(got["dnll"], want, U * (size + np.abs(want)), "dnll")
+    s = got["stats"].cpu().numpy()
+    assert s[0] == np.inf and s[2] == np.inf and np.isfinite(s[1])
+
+
 def test_policy_reference_without_a_coefficient_leaves_the_gradient(cuda_ok):
     """With kl_coef = 0 the reference is only reported: the loss and its gradient are the
     surrogate's, whatever the KL term is."""
