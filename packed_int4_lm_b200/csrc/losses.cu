@@ -343,11 +343,11 @@ __device__ __forceinline__ void kl_term(float z, float* k, float* d) {
 }
 
 // The side of the clip border is that of the exact difference old - nll against log(1 +- clip).
-// Rounding is monotone, so the rounded difference decides unless it equals the rounded border;
-// `border` then asks for the FP64 difference, which is exact (kExact).
+// Rounding is monotone, so the rounded difference decides unless it equals the rounded border; a piece
+// with such a token takes the FP64 difference, which is exact (kExact).
 template <bool kExact>
 __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A, bool has_ref,
-                                                  float ref, const PolicyConst& k, bool& border) {
+                                                  float ref, const PolicyConst& k) {
   const float x = old - nll;
   const bool up = A > 0.f;
   PolicyTok o;
@@ -355,9 +355,7 @@ __device__ __forceinline__ PolicyTok policy_token(float nll, float old, float A,
     const double d = (double)old - (double)nll;
     o.clipped = up ? d > k.log_hi : A < 0.f && d < k.log_lo;
   } else {
-    const float l = up ? k.log_hi_f : -k.log_lo_f, y = up ? x : -x;
-    o.clipped = y > l && (up || A < 0.f);  // (not for a NaN)
-    border |= y == l;
+    o.clipped = up ? x > k.log_hi_f : A < 0.f && x < k.log_lo_f;
   }
   // (0 times an infinite ratio is 0 here; a NaN stays one)
   const float r = A == 0.f ? (x != x ? x : 0.f) : exp_f(x) * A;
@@ -441,26 +439,25 @@ __device__ __forceinline__ void policy_pieces(const PolicyArgs& a, const PolicyC
         f[i] = t >= first && t < last ? f[i] * (float)scale : 0.f;
       }
     }
-    float sur, kl, clipped, g[kPer];
+    float g[kPer];
     bool border = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) border |= old[i] - nll[i] == (A[i] > 0.f ? k.log_hi_f : k.log_lo_f);
     auto tokens = [&](auto exact) {  // no branch on the weight: eight chains side by side
-      sur = kl = clipped = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const PolicyTok o = policy_token<decltype(exact)::value>(nll[i], old[i], A[i], a.nll_ref != nullptr, ref[i], k, border);
+        const PolicyTok o = policy_token<decltype(exact)::value>(nll[i], old[i], A[i], a.nll_ref != nullptr, ref[i], k);
         const bool on = f[i] != 0.f;  // a masked token may hold anything
-        sur += on ? f[i] * o.sur : 0.f;
-        kl += on ? f[i] * o.kl : 0.f;
-        clipped += on && o.clipped ? f[i] : 0.f;
+        const double share = (double)f[i];
+        sum.sur = fma(share, on ? -(double)o.sur : 0.0, sum.sur);
+        sum.kl = fma(share, on ? (double)o.kl : 0.0, sum.kl);
+        sum.clipped += on && o.clipped ? share : 0.0;
         g[i] = on ? f[i] * o.grad : 0.f;
       }
     };
-    tokens(std::false_type());
     if (__any_sync(0xffffffffu, border)) tokens(std::true_type());
+    else tokens(std::false_type());
     store_piece(a.dnll, t0, t1, vec, g);
-    sum.sur -= (double)sur;
-    sum.kl += (double)kl;
-    sum.clipped += (double)clipped;
   }
 }
 

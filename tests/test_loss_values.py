@@ -87,6 +87,27 @@ def test_policy_reference_without_a_coefficient_leaves_the_gradient(cuda_ok):
         assert torch.equal(got["stats"][[0, 1, 3]], want["stats"][[0, 1, 3]])
 
 
+@pytest.mark.parametrize("N", [512, 40000])
+def test_policy_sums_of_cancelling_tokens(cuda_ok, N):
+    """Equal log-probabilities make every share -A: large ones that cancel leave the small ones,
+    exactly, as these sums are exact in FP64."""
+    rng = np.random.default_rng(N)
+    at = np.arange(0, N, 4)
+    for big in (2.0 ** 31, 3e38):
+        adv = rng.integers(-9, 10, size=N).astype(np.float32)
+        if big < 1e38:  # big, small, -big, small
+            adv[at], adv[at + 2] = big, -big
+            small = -(adv[at + 1].astype(np.float64).sum() + adv[at + 3].sum())
+        else:  # what four tokens add up to passes FP32 in between
+            adv[at], adv[at + 1], adv[at + 2], adv[at + 3] = big, big, -big, -big
+            small = 0.0
+        x = torch.ones(N, device="cuda")
+        got = ah.policy_loss(x, x, torch.from_numpy(adv).cuda(), reduction="sum")
+        ah.check()
+        assert got["stats"].tolist() == [small, small, 0, 0]
+        assert torch.equal(got["dnll"], torch.from_numpy(adv).cuda())
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
