@@ -71,6 +71,22 @@ def test_policy_infinite_reference(cuda_ok):
     assert s[0] == np.inf and s[2] == np.inf and np.isfinite(s[1])
 
 
+def test_policy_far_ratios_keep_their_precision(cuda_ok):
+    """Ratios and KL terms of large and tiny differences, which are exact here."""
+    x = np.array([-100, -87, -60, -31.5, -8, -1, 1, 8, 31.5, 60, 87], dtype=np.float32)
+    adv = np.where(x > 0, -1, 1).astype(np.float32)  # (the clipped side is never the smaller one)
+    zero = np.zeros_like(x)
+    d = cu_dev(zero, x, adv, -x)
+    got = ah.policy_loss(d[0], d[1], d[2], reduction="sum")
+    kl = ah.policy_loss(d[0], d[0], torch.zeros_like(d[0]), nll_ref=d[3], kl_coef=1.0, reduction="sum")
+    ah.check()
+    r = np.exp(x.astype(np.float64)) * adv
+    # an exponential within two units in the last place (four half steps), a product
+    close(got["dnll"], r, 6 * U * np.abs(r) + 2.0 ** -149, "dnll")
+    want = np.expm1(x.astype(np.float64))
+    close(kl["dnll"], want, 6 * U * (np.abs(want) + 1), "kl")
+
+
 def test_policy_reference_without_a_coefficient_leaves_the_gradient(cuda_ok):
     """With kl_coef = 0 the reference is only reported: the loss and its gradient are the
     surrogate's, whatever the KL term is."""
