@@ -689,7 +689,8 @@ __device__ __forceinline__ void pref_pair(double gap, const PrefConst& k, double
     // -log sigma(m) = log(1 + e^-|m|) + max(-m, 0), and one of the two sigmas is 1 / (1 + e)
     const double e = exp(-fabs(m)), l = log1p(e), big = 1.0 / (1.0 + e), small = e / (1.0 + e);
     const double up = m >= 0 ? big : small, down = m >= 0 ? small : big;  // sigma(m), sigma(-m)
-    *loss = l + (m >= 0 ? k.smoothing * m : -(1.0 - k.smoothing) * m);
+    // (without smoothing an infinite margin costs nothing)
+    *loss = l + (m >= 0 ? (k.smoothing > 0.0 ? k.smoothing * m : 0.0) : -(1.0 - k.smoothing) * m);
     *slope = k.beta * (k.smoothing * up - (1.0 - k.smoothing) * down);
     if (m != m) *loss = *slope = m;
   } else if (k.kind == ARCHEAD_PREF_HINGE) {

@@ -124,6 +124,25 @@ def test_policy_sums_of_cancelling_tokens(cuda_ok, N):
         assert torch.equal(got["dnll"], torch.from_numpy(adv).cuda())
 
 
+def test_preference_infinite_margin(cuda_ok):
+    """A preferred answer that the reference gives probability 0: the loss without smoothing is 0
+    and flat; with smoothing it is infinite."""
+    nll = np.array([1, 2, 3], dtype=np.float32)
+    ref = np.array([np.inf, 2, 1], dtype=np.float32)
+    pairs = np.array([[0, 1], [2, 1]], dtype=np.int32)
+    d = cu_dev(nll, offsets([1, 1, 1]), pairs, ref)
+    got = ah.preference_loss(d[0], d[1], d[2], nll_ref=d[3], beta=0.5)
+    other = ah.preference_loss(d[0], d[1], d[2], nll_ref=d[3], beta=0.5, label_smoothing=0.1)
+    back = ah.preference_loss(d[0], d[1], d[2].flip(1).contiguous(), nll_ref=d[3], beta=0.5)
+    ah.check()
+    m = 0.5 * (-2.0 - 0.0)
+    close(got["pair_loss"], np.array([0.0, np.log1p(np.exp(-m))]), 4 * U, "pair_loss")
+    close(got["dnll"], np.array([0.0, -0.25, 0.25]) / (1 + np.exp(m)), 4 * U, "dnll")
+    assert torch.isfinite(got["loss"]).all()
+    assert other["pair_loss"][0] == INF and torch.isfinite(other["dnll"]).all()
+    assert back["pair_loss"][0] == INF and back["dnll"][0] == -0.25
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
