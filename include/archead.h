@@ -239,6 +239,8 @@ enum archead_preference {
  *   float P x 2: beta f_a, beta f_b.  All pointers on the device.
  *   A pair index outside [0, B) sets ARCHEAD_ERR_SEGMENT; that pair's loss and rewards and
  *   the mean loss are NaN and it adds nothing to dnll.  Offsets as in archead_policy_loss.
+ *   A sequence whose pairs have a slope dl/df that is not finite, or 2^127 or more (in units of beta;
+ *   for ipo of max(1, 1 / beta)), gets NaN in dnll.
  *   label_smoothing in [0, 1) (0 unless the kind is sigmoid), beta > 0, margin finite.
  *   Sums are held in FP64 and in a fixed order: equal calls give equal bits.
  *   Asynchronous on `stream`.

@@ -648,31 +648,38 @@ cudaError_t launch_after(void (*kern)(P...), int64_t grid, int threads, size_t s
 }
 
 // ---- preference loss --------------------------------------------------------------------
-// A sequence's slope dL/df over its pairs, in fixed point: four signed 64-bit limbs, limb k
-// of weight 2^(32 k - 96), so sums up to 2^31 pairs keep every bit above 2^-96 (of the unit
-// that the host chooses, about the largest slope of an ordinary pair) and integer adds make
-// the result independent of their order.  A slope that is not finite, or above 2^31 units,
-// counts in a fifth word and makes the sequence's slope NaN.
-constexpr int kLimbs = 5;
+// A sequence's slope dL/df over its pairs, in fixed point: signed 64-bit limbs, limb k of weight
+// 2^(32 k - 192), so sums up to 2^31 pairs keep every bit from 2^-192 to 2^127 (of the unit that the host
+// chooses, about the largest slope of an ordinary pair: slopes of decided pairs fade as e^-m, and
+// their FP32 gradients keep their precision down to the smallest) and integer adds make the
+// result independent of their order.  A slope that is not finite, or 2^127 units or more, counts
+// in one more word and makes the sequence's slope NaN.
+constexpr int kLimbs = 10, kSlopeWords = kLimbs + 1;
+
+__device__ __forceinline__ double pow2_double(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
 
 __device__ __forceinline__ void slope_add(unsigned long long* acc, double v) {
-  if (!(fabs(v) < 2147483648.0)) {
-    atomicAdd(acc + 4, 1ull);
+  if (!(fabs(v) < 1.7014118346046923e38)) {
+    atomicAdd(acc + kLimbs, 1ull);
     return;
   }
+  const int e = ((__double2hiint(v) >> 20) & 0x7ff) - 1023;
+  if (e < -192) return;
+  const int k = (e + 192) >> 5;  // the limb of the leading bit; the 53 bits reach into two more
+  v *= pow2_double(192 - 32 * k);  // exact, as are the steps below: powers of two and the fraction's bits
 #pragma unroll
-  for (int k = 3; k >= 0; --k) {
+  for (int j = 0; j < 3; ++j) {
     const long long d = (long long)v;  // toward zero
-    if (d) atomicAdd(acc + k, (unsigned long long)d);
-    v = (v - (double)d) * 4294967296.0;  // exact: a power of two and the fraction's bits
+    if (d && k >= j) atomicAdd(acc + (k - j), (unsigned long long)d);
+    v = (v - (double)d) * 4294967296.0;
   }
 }
 
 __device__ __forceinline__ double slope_value(const unsigned long long* acc) {
-  if (acc[4]) return __longlong_as_double(0x7ff8000000000000ll);
-  double v = 0.0, unit = 1.0 / 4294967296.0 / 4294967296.0 / 4294967296.0;
+  if (acc[kLimbs]) return __longlong_as_double(0x7ff8000000000000ll);
+  double v = 0.0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k, unit *= 4294967296.0) v += (double)(long long)acc[k] * unit;
+  for (int k = 0; k < kLimbs; ++k) v = fma((double)(long long)acc[k], pow2_double(32 * k - 192), v);
   return v;
 }
 
@@ -729,8 +736,8 @@ __device__ __forceinline__ double pair_step(const PreferenceArgs& a, const PrefC
   double loss = __longlong_as_double(0x7ff8000000000000ll), slope;
   if (ok && okb) {
     pref_pair(f - fb, k, &loss, &slope);
-    slope_add(acc + (int64_t)mine * kLimbs, slope * k.unit);
-    slope_add(acc + (int64_t)ib * kLimbs, -slope * k.unit);
+    slope_add(acc + (int64_t)mine * kSlopeWords, slope * k.unit);
+    slope_add(acc + (int64_t)ib * kSlopeWords, -slope * k.unit);
   } else {
     atomicOr(err, kErrSegment);
   }
@@ -749,7 +756,7 @@ __device__ __forceinline__ void pref_pieces(const PreferenceArgs& a, const PrefC
   const double per_pair = a.P ? 1.0 / (k.unit * (double)a.P) : 0.0;
   const bool vec = aligned16(a.w, a.dnll);
   double coef = 0.0;  // of the window's sequence
-  auto window = [&](int s) { coef = -slope_value(acc + (int64_t)s * kLimbs) * per_pair; };
+  auto window = [&](int s) { coef = -slope_value(acc + (int64_t)s * kSlopeWords) * per_pair; };
   Walker<decltype(window)> walk(sq, c * kPiece, window);
   // With `average`: the last sequence's weight.  A long one comes back in every piece of the warp; added
   // up from its pieces each time, 2^31 tokens of one sequence took 100 s a call.
@@ -800,8 +807,8 @@ __global__ void __launch_bounds__(256) pref_pair_kernel(PreferenceArgs a, PrefCo
                                                         unsigned* err) {
   allow_dependent_launch();
   __shared__ double red[8];
-  __shared__ unsigned long long local[kFew ? kLocalSeqs * kLimbs : 1];
-  const int words = kFew ? (int)a.B * kLimbs : 0;
+  __shared__ unsigned long long local[kFew ? kLocalSeqs * kSlopeWords : 1];
+  const int words = kFew ? (int)a.B * kSlopeWords : 0;
   for (int i = threadIdx.x; i < words; i += 256) local[i] = 0ull;
   if (kFew) __syncthreads();
   grid_dependency_wait();
@@ -847,7 +854,7 @@ __global__ void __launch_bounds__(1024) pref_small_kernel(PreferenceArgs a, Pref
   int c0, c1;
   my_pieces(pieces_of(sq.N), &c0, &c1);
   sums_pieces<true>(sq, a.nll, a.nll_ref, a.w, c0, c1, sums);
-  for (int i = threadIdx.x; i < sq.B * kLimbs; i += 1024) acc[i] = 0ull;
+  for (int i = threadIdx.x; i < sq.B * kSlopeWords; i += 1024) acc[i] = 0ull;
   __syncthreads();
   double sum = 0.0;
   for (int64_t p0 = 0; p0 < a.P; p0 += 64) sum += pair_step(a, k, sums, p0 + (threadIdx.x >> 4), acc, err);
@@ -924,7 +931,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, void* scratch, unsigned* err
 
 size_t preference_scratch_bytes(const PreferenceArgs& a) {
   if (pref_small(a)) return 0;
-  return up256(8 * kMaxBlocks) + up256((size_t)a.B * kLimbs * 8) + seq_sum_bytes(a.N, a.B);
+  return up256(8 * kMaxBlocks) + up256((size_t)a.B * kSlopeWords * 8) + seq_sum_bytes(a.N, a.B);
 }
 
 cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsigned* err,
@@ -932,17 +939,17 @@ cudaError_t launch_preference_loss(const PreferenceArgs& a, void* scratch, unsig
   const PrefConst k = pref_const(a);
   if (pref_small(a)) {
     ++*launches;
-    return launch_after(pref_small_kernel, 1, 1024, (size_t)a.B * kLimbs * 8, st, a, k, err);
+    return launch_after(pref_small_kernel, 1, 1024, (size_t)a.B * kSlopeWords * 8, st, a, k, err);
   }
   char* b = static_cast<char*>(scratch);
   double* part = reinterpret_cast<double*>(b);
   b += up256(8 * kMaxBlocks);
   unsigned long long* acc = reinterpret_cast<unsigned long long*>(b);
-  b += up256((size_t)a.B * kLimbs * 8);
+  b += up256((size_t)a.B * kSlopeWords * 8);
   const SeqSums q = carve_seq_sums(b, a.N, a.B);
   const Seqs sq = {a.cu, (int)a.N, (int)a.B};
   const int pb = capped((piece_count(a.N) + 7) / 8);
-  seq_sums_kernel<true><<<pb, 256, 0, st>>>(a.nll, a.nll_ref, a.w, sq, q, acc, a.B * kLimbs, err);
+  seq_sums_kernel<true><<<pb, 256, 0, st>>>(a.nll, a.nll_ref, a.w, sq, q, acc, a.B * kSlopeWords, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int np = capped((a.P + 15) / 16);

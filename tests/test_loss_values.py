@@ -143,6 +143,47 @@ def test_preference_infinite_margin(cuda_ok):
     assert back["pair_loss"][0] == INF and back["dnll"][0] == -0.25
 
 
+@pytest.mark.parametrize("copies", [1, 40])
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "ipo"])
+def test_preference_slopes_of_every_size(cuda_ok, kind, copies):
+    """Pairs that are long decided, whose slopes fade as e^-m, beside fresh ones, and squared gaps of
+    any size: every slope is right to its last bit, in one block and in the chain."""
+    gaps = np.array([0.0, 1, 20, 50, 55, 60, 70, 80, 87, 100, 103, -30, -1000])
+    if kind == "ipo":
+        gaps = np.concatenate([gaps, [2e9, 3e9, 5e15, -7e20, 1e30, -1e37]])
+    nll = np.zeros(2 * len(gaps), dtype=np.float32)
+    nll[1::2] = gaps
+    gaps = nll[1::2].astype(np.float64)
+    nll, gaps = np.tile(nll, copies), np.tile(gaps, copies)
+    P = len(gaps)
+    pairs = np.arange(2 * P, dtype=np.int32).reshape(P, 2)
+    d = cu_dev(nll, offsets([1] * (2 * P)), pairs)
+    got = ah.preference_loss(*d, beta=1.0, kind=kind)
+    assert (ah.last_launches() == 1) == (copies == 1)
+    ah.check()
+    if kind == "sigmoid":
+        slope = -1 / (1 + np.exp(gaps))
+    elif kind == "hinge":
+        slope = np.where(gaps < 1, -1.0, 0.0)
+    else:
+        slope = 2 * (gaps - 0.5)
+    want = np.stack([-slope, slope], 1).ravel() / P
+    # FP64 rounded once: half a step, of the smallest FP32 number at least
+    close(got["dnll"], want, 1.001 * U * np.abs(want) + 1.001 * 2.0 ** -150, kind)
+
+
+def test_preference_slopes_past_every_size_are_nan(cuda_ok):
+    """An infinite gap under the squared loss, and one whose slope passes what sums can hold, make
+    the two answers' gradients NaN and no other's."""
+    nll = np.array([0, np.inf, 0, 3e38, 0, 5], dtype=np.float32)
+    w = np.array([1, 1, 1, 3e38, 1, 1], dtype=np.float32)
+    d = cu_dev(nll, offsets([1] * 6), np.arange(6, dtype=np.int32).reshape(3, 2), w)
+    got = ah.preference_loss(d[0], d[1], d[2], weights=d[3], kind="ipo", beta=1.0)
+    ah.check()
+    g = got["dnll"].cpu().numpy()
+    assert np.isnan(g[:4]).all() and list(g[4:]) == [-3.0, 3.0]
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
