@@ -184,6 +184,54 @@ def test_preference_slopes_past_every_size_are_nan(cuda_ok):
     assert np.isnan(g[:4]).all() and list(g[4:]) == [-3.0, 3.0]
 
 
+@pytest.mark.parametrize("B", [33, 129, 255, 256, 257])
+@pytest.mark.parametrize("reduction", ["token", "sequence", "sum"])
+@pytest.mark.parametrize("per_seq", [False, True])
+def test_policy_of_many_sequences_in_one_block(cuda_ok, B, reduction, per_seq):
+    """Up to 256 sequences run in one launch, whose walk reloads its window of 32 and whose sums
+    take two rounds of 128."""
+    rng = np.random.default_rng(B)
+    lens = rng.choice([0, 1, 2, 5, 33, 70], size=B)
+    lens[B // 2:B // 2 + 20] = rng.integers(33, 60, size=20 if B > 50 else B - B // 2)[:20]
+    cu = offsets(lens)
+    N = int(cu[-1])
+    assert N <= 32 * 256
+    nll, old, ref, w, rng = make_tokens(N, 41)
+    w[cu[3]:cu[9]] = 0
+    adv = rng.normal(size=B if per_seq else N).astype(np.float32)
+    kw = dict(lo=0.2, hi=0.3, beta=0.1, reduction=reduction)
+    for weights in (w, None):
+        want = policy_ref(nll, old, adv, ref, weights, cu, per_seq, **kw)
+        d = cu_dev(nll, old, adv, ref, weights, cu)
+        got = ah.policy_loss(d[0], d[1], d[2], nll_ref=d[3], weights=d[4], cu_seqlens=d[5], per_sequence=per_seq,
+                             clip_low=0.2, clip_high=0.3, kl_coef=0.1, reduction=reduction)
+        assert (ah.last_launches() == 1) == (B <= 256)
+        ah.check()
+        close(got["dnll"], want["dnll"], U * (want["size"] + np.abs(want["dnll"])), "dnll")
+        close(got["stats"], want["stats"], 2 * U * (want["mag"] + np.abs(want["stats"])), "stats")
+
+
+@pytest.mark.parametrize("B,P", [(33, 64), (129, 65), (255, 192), (256, 192), (256, 193), (257, 65)])
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_of_many_sequences_in_one_block(cuda_ok, B, P, average):
+    """Up to 256 sequences and 192 pairs run in one launch, 64 pairs a round."""
+    rng = np.random.default_rng(B + P)
+    cu = offsets(rng.choice([0, 1, 2, 5, 33, 70], size=B))
+    N = int(cu[-1])
+    nll, _, ref, w, rng = make_tokens(N, 42, spread=0.1)
+    pairs = make_pairs(B, P, rng)
+    want = preference_ref(nll, cu, pairs, ref, w, 0.2, "sigmoid", 0.1, 0.05, average)
+    d = cu_dev(nll, cu, pairs, ref, w)
+    got = ah.preference_loss(d[0], d[1], d[2], nll_ref=d[3], weights=d[4], beta=0.2, label_smoothing=0.1, margin=0.05,
+                             average=average)
+    assert (ah.last_launches() == 1) == (B <= 256 and P <= 192)
+    ah.check()
+    slip = 1e-12
+    close(got["dnll"], want["dnll"], U * np.abs(want["dnll"]) + slip * (want["size"] + 1e-30), "dnll")
+    for k in ("pair_loss", "rewards", "loss"):
+        close(got[k], want[k], 1.001 * U * np.abs(want[k]) + slip * (1 + np.abs(want[k])), k)
+
+
 def test_preference_average_of_long_sequences(cuda_ok):
     """Sequences of millions of tokens beside short ones: a sequence's weight is the same in every
     piece of it."""
