@@ -814,9 +814,10 @@ __global__ void __launch_bounds__(finish_threads(MT)) grad_finish_kernel(const F
   grid_dependency_wait();
   const int64_t slab = p.n * p.dp;
   // u: four ranks of a token of the block
+  const int uq = rp > 0 ? rp >> 2 : 1;  // quads of a token
   auto u_at = [&](int i, int* t, int* j) {
-    *t = i / (rp >> 2);
-    *j = 4 * (i - *t * (rp >> 2));
+    *t = i / uq;
+    *j = 4 * (i - *t * uq);
     return i < 4 * MT * rp && n0 + *t < p.n && *j < RR ? p.part + (n0 + *t) * p.dp + p.h.D + *j : nullptr;
   };
   auto u_put = [&](int t, int j, float4 a) {
