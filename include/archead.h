@@ -40,6 +40,12 @@
  *    raises ARCHEAD_ERR_RANGE_H.  Entries of the scaled rows below the FP16 normal range
  *    (2^-14; with one group code per 128 columns, g >= 128 and N <= 16, half of the
  *    columns are stored divided by 16) keep fewer bits, as rounding to FP16 does.
+ *  - Rows whose two parts differ very much in scale: with M = 128 max(|sAc[v]|, |sAw[v]|), the
+ *    calls with N > 16 tokens and the gradients hold a row's residual and its left factors in FP16
+ *    under one scale.  The residual loses bits where M >= 2^38 |S|, and all of them at 2^46 |S|; a left
+ *    factor entry is rounded to 11 bits (in the logits to 22), to fewer below 2^-17 |S|, and is lost below
+ *    2^-28 |S|.  Factors built together with their residual are far from either; factors scaled
+ *    otherwise are balanced before packing (sAc 2^-e, sBc 2^e).
  */
 #ifndef ARCHEAD_H_
 #define ARCHEAD_H_

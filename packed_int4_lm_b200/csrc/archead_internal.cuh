@@ -215,7 +215,7 @@ struct TcImage {
   const float* tok;  // per token: f - es - lse log2 e (NaN: its target is invalid)
   int nt;            // token tile of the image
   const float* sp;     // per row S'_v
-  const uint32_t* cs;  // per row the residual's 2^-k, FP16x2
+  const uint32_t* cs;  // per row the residual's 2^(8 - k), FP16x2
 };
 cudaError_t launch_residual_tc(const __half* Hb, const float* tsc, const archead_head* head,
                                const Shapes& s, const TcPlan& plan, float* Y,

@@ -10,9 +10,12 @@ namespace archead {
 // split into a scale S'_v, folded into dY, and entries that FP16 holds: the residual q c 2^-k,
 // exact for k <= 24, and the factor entries a / S', |a| / S' < 2^14.  With M = 128 max(|sAc|,
 // |sAw|) bounding the factor entries, S' = S 2^k with k = ilogb(M) - ilogb(S) - 13, at least -3
-// (the dequantisation's addend 24 c 2^-k must stay finite).  Where S is 0, or k would pass 40
-// (the residual is then under 2^-45 of the factors' bound), the residual is dropped and S' comes
-// from M alone; a row without either has S' = 0.
+// (the dequantisation's addend 24 c 2^-k must stay finite).  From k = 25 on (M >= 2^38 S) the scales
+// c 2^-k keep fewer bits, as in the logits' tcgen05 kernel, and none from 33 on.  Where S is 0, or k would
+// pass 40, the residual is dropped and S' comes from M alone; a row without either has S' = 0.  A factor
+// entry is one FP16 value (11 bits, as dY; the result keeps 8), of fewer bits below 2^-14 S'.  The rule
+// looks at the left factors alone, so it relies on right factors that are not tiny or huge; the header
+// states the limits.
 struct GradRow {
   float sp;  // S'
   float cs;  // 2^-k, 0 without a residual
@@ -39,7 +42,7 @@ __host__ __device__ __forceinline__ GradRow grad_row(float S, float sac, float s
 struct GradWarpParams {
   archead_head h;
   const char* img;  // image tiles of `it` tokens
-  const uint32_t* cs;
+  const uint32_t* cs;  // per row 2^(8 - k), FP16x2
   const char* fimg;  // factor image: per 32 rows, fcols x 64 bytes
   float* part;
   int64_t n, dp, nunits;
@@ -126,11 +129,11 @@ __device__ __forceinline__ uint32_t load_word(const uint32_t* c) {
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(c));
   return r;
 }
-// Code e of them times 2^-k, twice in FP16 (exact for k <= 24): 1024 + c is a half with the byte c
-// in its low mantissa bits.
+// Code e of them times 2^-k, twice in FP16 (exact for k <= 24): 4 + c 2^-8 is a half with the byte c in
+// its low mantissa bits, and cs = 2^(8 - k) is an FP16 number up to k = 32.
 __device__ __forceinline__ __half2 code_half2(uint32_t codes, int e, uint32_t cs) {
-  const uint32_t r = __byte_perm(codes, 0x64646464u, 0x4040u + 0x0101u * e);
-  return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(1024.f)),
+  const uint32_t r = __byte_perm(codes, 0x44444444u, 0x4040u + 0x0101u * e);
+  return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(4.f)),
                  *reinterpret_cast<const __half2*>(&cs));
 }
 

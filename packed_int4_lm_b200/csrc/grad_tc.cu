@@ -38,7 +38,7 @@ struct RowsParams {
   archead_head h;
   int64_t vpad;
   float* sp;         // S'_v, vpad (0 past V)
-  uint32_t* cs;      // 2^-k per row (grad_row) as FP16x2, vpad (0 past V)
+  uint32_t* cs;      // 2^(8 - k) per row (grad_row, code_half2) as FP16x2, vpad (0 past V)
   float2* row;       // TcImage's rows without -es, or nullptr
   float* spmax;      // kRowBlocks
   char* fimg;        // factor image, or nullptr without ranks
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) grad_rows_kernel(const RowsPar
       }
     }
     p.sp[v] = s;
-    p.cs[v] = h2_bits(__float2half2_rn(c));
+    p.cs[v] = h2_bits(__float2half2_rn(256.f * c));
     if (p.row) p.row[v] = make_float2(log2f(fabsf(s)), __uint_as_float(s < 0.f ? 0x80008000u : 0u));
     m = fmaxf(m, fabsf(s));
   }
