@@ -15,6 +15,48 @@ from workloads import bf16_bits, make_channel_scales, make_hidden, make_targets
 pytestmark = pytest.mark.gpu
 
 
+def wide_tiles():
+    """Tiles of 256 tokens x 256 rows from which on the logits run in them."""
+    api = os.path.join(os.path.dirname(ah.__file__), "csrc", "archead_api.cu")
+    return int(re.search(r"kWideTiles = (\d+);", open(api).read()).group(1))
+
+
+@pytest.mark.parametrize("name,N", [("g64", 19275), ("g32 odd", 15437), ("g128", 4700), ("g256 ranks 128", 19275),
+                                    ("wide scales", 19275)])
+def test_nll_grad_in_wide_tiles(cuda_ok, name, N):
+    """Batches that fill the SMs twice with tiles of 256 tokens x 256 rows: several blocks of columns,
+    ranks of every kind, a last tile of tokens without its second half.  240 of the tokens, the last
+    ones among them, against FP64."""
+    head, W, M = head_of(name)
+    V, D = head["V"], head["D"]
+    assert -(-V // 256) * -(-N // 256) >= wide_tiles() and -(-N // 128) % 2 == 1 and N % 128
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    rng = np.random.default_rng(N)
+    rows = np.unique(np.r_[rng.integers(0, N, size=160), N - 80:N])
+    H = make_hidden(N, make_channel_scales(D, 0.5, 4, 20.0, 1), 2)
+    tg = make_targets(N, V, 3).numpy()
+    dnll = rng.normal(size=N).astype(np.float32)
+    dnll[rows[::7]] = 0
+    t, Hd, dn = torch.from_numpy(tg).cuda(), H.cuda(), torch.from_numpy(dnll).cuda()
+    nl, ls = ah.nll_lse(Hd, dh, t)
+    got = ah.nll_grad(Hd, dh, t, nl, ls, dn)
+    ah.check()
+    assert torch.equal(got, ah.nll_grad(Hd, dh, t, nl, ls, dn))
+    Y = oracle.logits(head, bf16_bits(H[rows]))
+    m = Y.max(1)
+    lse = m + np.log(np.exp(Y - m[:, None]).sum(1))
+    P = np.exp(Y - lse[:, None])
+    at = (np.arange(len(rows)), tg[rows])
+    P[at] = np.expm1(Y[at] - lse)
+    want = dnll[rows].astype(np.float64)[:, None] * (P @ W)
+    # The NLL is the difference of a log-sum-exp and a logit, FP32 numbers off by up to 4 half steps of
+    # the largest logit each.  A target may lead by chance (logits reach 1000 under the wide scales: 1 - p =
+    # 1.2e-7 where lse = 386 has a half step of 1.5e-5), and then that error is its whole entry p - 1.
+    slip = 4 * 2.0 ** -24 * np.abs(Y).max(1)[:, None]
+    tol = nll_tol(head, P, Y, M, dnll[rows], want) + np.abs(dnll[rows])[:, None] * 2 * slip * M[tg[rows]]
+    close(got[torch.from_numpy(rows).cuda()], want, tol, name)
+
+
 def scaled_factors(head, e):
     """The same head with its left factors 2^e larger and its right ones as much smaller."""
     out = dict(head)
@@ -46,3 +88,35 @@ def test_factors_scaled_against_each_other(cuda_ok, N, e):
     fade = q * np.where(k > 24, 2.0 ** -25 * S * 2.0 ** k, 0)[:, None]
     want = dY.astype(np.float64) @ W
     close(got, want, BF16 * np.abs(want) + PROD * (size @ M) + smallest_step(head, M, dY) + size @ fade, e)
+
+
+@pytest.mark.parametrize("name", ["g64", "g128"])
+def test_nll_grad_with_nlls_of_smaller_batches(cuda_ok, name):
+    """NLLs and log-sum-exps taken eight tokens at a time (another kernel, other rounding), the
+    gradient of all tokens at once; confident tokens among them."""
+    head, W, M = head_of(name)
+    dh = ah.DeviceHead.from_canonical(head, "cuda")
+    N, D = 304, head["D"]
+    rng = np.random.default_rng(4)
+    tg = rng.integers(2, head["V"], size=N).astype(np.int32)
+    base = W[tg] / (W[tg] ** 2).sum(1, keepdims=True) * np.linspace(1, 40, N)[:, None]
+    H = torch.from_numpy(base + 0.3 * rng.normal(size=(N, D))).to(torch.bfloat16)
+    Y = oracle.logits(head, bf16_bits(H))
+    m = Y.max(1)
+    lse = m + np.log(np.exp(Y - m[:, None]).sum(1))
+    P = np.exp(Y - lse[:, None])
+    rest = P.copy()
+    rest[np.arange(N), tg] = 0
+    P[np.arange(N), tg] = -rest.sum(1)
+    Hd, t = H.cuda(), torch.from_numpy(tg).cuda()
+    parts = [ah.nll_lse(Hd[n:n + 8], dh, t[n:n + 8]) for n in range(0, N, 8)]
+    nl, ls = (torch.cat(x) for x in zip(*parts))
+    got = ah.nll_grad(Hd, dh, t, nl, ls, torch.ones(N, device="cuda"))
+    ah.check()
+    want = P @ W
+    # as for confident tokens of one batch; every probability besides moves by what the two kernels'
+    # logits differ by, at most 1e-4 max|Y| each
+    slip = 4 * 2.0 ** -24 * np.abs(Y).max(1)[:, None]
+    tol = nll_tol(head, P, Y, M, np.ones(N, np.float32), want) + 2 * slip * M[tg] + 1e-4 * np.abs(Y).max() * (np.abs(P) @ M)
+    close(got, want, tol)
+    assert nl.min() < 1e-3
