@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) dy_amax_kernel(const AmaxParams p) {
 struct ImageParams {
   const float* src;  // dY, or logits
   int64_t n, npad, V;
-  int nt, group;
+  int nt;
   const float* sp;
   const float* spmax;
   const unsigned* amax;  // dY: per-token maxima
@@ -258,9 +258,11 @@ __global__ void __launch_bounds__(256) grad_targets_kernel(const TokensParams p)
       __float2half_rn(expm1f(-p.t.nll[n]) * a * p.sp[t] * b);
 }
 
-// One warp per 128 vocabulary rows and group of up to 32 tokens (`group`; fewer for small batches,
-// which would leave most SMs idle): each lane four rows, two 128-byte image rows per token, four
-// tokens' loads in flight.  A group lies in one image tile.
+// One warp per 128 vocabulary rows and group of 8 tokens (a group lies in one image tile): each lane four
+// rows, two 128-byte image rows per token, four tokens' loads in flight.  Groups of 32 leave SMs idle
+// (a call at V = 32000, D = 2048: N = 64 45 against 42 us, N = 600 149 against 141), groups of 4 pay more
+// for a warp's start (N = 600 145 us); at N = 4096 and V = 128256 all are the same.
+constexpr int kGroup = 8;
 template <bool kSoftmax, bool kQuads>
 __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   allow_dependent_launch();
@@ -268,14 +270,14 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t nunits = (p.V + kUnit - 1) / kUnit;
   const int64_t u = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int64_t n0 = (int64_t)blockIdx.y * p.group;
+  const int64_t n0 = (int64_t)blockIdx.y * kGroup;
   const int es = spmax_exp(p.spmax);
   // this lane's token of the group: its factor 2^f and, for logits, lse, target and its entry
   const int64_t mine = n0 + lane;
   int f = 0;
   float lse = 0.f, at = 0.f;
   int32_t target = -1;
-  if (lane < p.group && mine < p.n) {
+  if (lane < kGroup && mine < p.n) {
     if (kSoftmax) {
       target = p.t.targets[mine];
       lse = p.t.lse[mine];
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   const int nn0 = (int)(n0 - tt * p.nt), r = 4 * (lane & 15);  // row in its half unit
   char* dst = p.img + ((tt * 2 * nunits + 2 * u + (lane >> 4)) * p.nt + nn0) * 128 + 2 * (r & 7);
   const float* src = p.src + n0 * p.V + v;
-  for (int k0 = 0; k0 < p.group && n0 + k0 < p.npad; k0 += 4) {
+  for (int k0 = 0; k0 < kGroup && n0 + k0 < p.npad; k0 += 4) {
     float y[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1115,10 +1117,9 @@ bool image_quads(const HeadGrad& a, const float* src) {
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  const int group = g.npad <= 64 ? 4 : (g.npad <= 512 ? 8 : 32);  // (divides the image tile)
-  const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, group, b.sp, b.spmax, b.amax,
+  const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, b.sp, b.spmax, b.amax,
                          t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
-  const dim3 grid((unsigned)((g.nunits + 7) / 8), (unsigned)((g.npad + group - 1) / group));
+  const dim3 grid((unsigned)((g.nunits + 7) / 8), (unsigned)((g.npad + kGroup - 1) / kGroup));
   const bool quads = image_quads(a, src);
   ++*a.launches;
   if (t)
