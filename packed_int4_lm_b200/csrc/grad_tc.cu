@@ -1199,10 +1199,14 @@ cudaError_t grad_product(const HeadGrad& a, const float* dnll, uint16_t* dH) {
   if (e != cudaSuccess) return e;
   const FinishParams fp = {h, b.part, a.n, g.dp, g.slabs, b.texp, dnll, reinterpret_cast<__nv_bfloat16*>(dH)};
   *a.launches += 2;
-  // 64 tokens per block share b where those blocks fill the SMs twice; otherwise 16, for more blocks
-  // (V = 27766, D = 512, N = 926: 73 us in 60 blocks of 64)
-  const int mt = (a.n + 63) / 64 * (h.D / 128) >= 2 * sm_count() ? 4 : 1;
-  const size_t smem = finish_smem(mt, h.r_c + h.r_r);
+  // 64 tokens per block share b, where such blocks are many: they hold u in shared memory and have few
+  // threads, so with 16 tokens more loads are in flight.  A call at V = 32000, D = 4096 in blocks of 16 and of
+  // 64: 128 ranks N = 1500 (768 blocks of 64) 495 and 543 us, N = 2048 (1024) 614 and 596, N = 4096 1241 and 1188; 256 ranks
+  // N = 600 219 and 324 (V = 20000), N = 4096 1336 and 1436; without ranks N = 600 192 and 190, N = 1024 297 and 285.
+  const int ranks = h.r_c + h.r_r;
+  const int64_t rounds = (a.n + 63) / 64 * (h.D / 128) / sm_count();
+  const int mt = ranks <= 128 && rounds >= (ranks ? 6 : 2) ? 4 : 1;
+  const size_t smem = finish_smem(mt, ranks);
   auto kern = mt == 4 ? grad_finish_kernel<4> : grad_finish_kernel<1>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)((a.n + 16 * mt - 1) / (16 * mt)), (unsigned)(h.D / 128)), finish_threads(mt), smem, a.st, fp);
