@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) dy_amax_kernel(const AmaxParams p) {
 struct ImageParams {
   const float* src;  // dY, or logits
   int64_t n, npad, V;
-  int nt;
+  int nt, group;
   const float* sp;
   const float* spmax;
   const unsigned* amax;  // dY: per-token maxima
@@ -258,11 +258,11 @@ __global__ void __launch_bounds__(256) grad_targets_kernel(const TokensParams p)
       __float2half_rn(expm1f(-p.t.nll[n]) * a * p.sp[t] * b);
 }
 
-// One warp per 128 vocabulary rows and group of 8 tokens (a group lies in one image tile): each lane four
-// rows, two 128-byte image rows per token, four tokens' loads in flight.  Groups of 32 leave SMs idle
-// (a call at V = 32000, D = 2048: N = 64 45 against 42 us, N = 600 149 against 141), groups of 4 pay more
-// for a warp's start (N = 600 145 us); at N = 4096 and V = 128256 all are the same.
-constexpr int kGroup = 8;
+// One warp per 128 vocabulary rows and group of 8 tokens, or of 4 where such warps are fewer than run
+// at once (a group lies in one image tile): each lane four rows, two 128-byte image rows per token, four
+// tokens' loads in flight.  Whole calls with groups of 4 and of 8: nll_grad of 16 tokens, V = 4096, D = 512 32.2 and
+// 34.1 us; logits_grad V = 32000, D = 2048 N = 128 (4000 warps of 8) 49.7 and 51.4, N = 600 (20000) 145 and 141; V =
+// 128256, D = 4096 N = 128 177 and 171.  Groups of 32 (N = 600 149 us) win nowhere.
 template <bool kSoftmax, bool kQuads>
 __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   allow_dependent_launch();
@@ -270,14 +270,14 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t nunits = (p.V + kUnit - 1) / kUnit;
   const int64_t u = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int64_t n0 = (int64_t)blockIdx.y * kGroup;
+  const int64_t n0 = (int64_t)blockIdx.y * p.group;
   const int es = spmax_exp(p.spmax);
   // this lane's token of the group: its factor 2^f and, for logits, lse, target and its entry
   const int64_t mine = n0 + lane;
   int f = 0;
   float lse = 0.f, at = 0.f;
   int32_t target = -1;
-  if (lane < kGroup && mine < p.n) {
+  if (lane < p.group && mine < p.n) {
     if (kSoftmax) {
       target = p.t.targets[mine];
       lse = p.t.lse[mine];
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(256) dy_image_kernel(const ImageParams p) {
   const int nn0 = (int)(n0 - tt * p.nt), r = 4 * (lane & 15);  // row in its half unit
   char* dst = p.img + ((tt * 2 * nunits + 2 * u + (lane >> 4)) * p.nt + nn0) * 128 + 2 * (r & 7);
   const float* src = p.src + n0 * p.V + v;
-  for (int k0 = 0; k0 < kGroup && n0 + k0 < p.npad; k0 += 4) {
+  for (int k0 = 0; k0 < p.group && n0 + k0 < p.npad; k0 += 4) {
     float y[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1117,9 +1117,10 @@ bool image_quads(const HeadGrad& a, const float* src) {
 cudaError_t grad_image(const HeadGrad& a, const float* src, const SoftmaxTokens* t) {
   const GradPlan g = grad_plan(*a.head, a.n);
   const GradParts b = grad_parts(a, g);
-  const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, b.sp, b.spmax, b.amax,
+  const int group = g.nunits * (g.npad / 8) < 40ll * sm_count() ? 4 : 8;
+  const ImageParams p = {src, a.n, g.npad, a.head->V, g.it, group, b.sp, b.spmax, b.amax,
                          t ? *t : SoftmaxTokens{}, b.img, b.texp, a.err};
-  const dim3 grid((unsigned)((g.nunits + 7) / 8), (unsigned)((g.npad + kGroup - 1) / kGroup));
+  const dim3 grid((unsigned)((g.nunits + 7) / 8), (unsigned)(g.npad / group));
   const bool quads = image_quads(a, src);
   ++*a.launches;
   if (t)
