@@ -164,13 +164,18 @@ int archead_nll_lse(const uint16_t* H, const archead_head* head, const int32_t* 
  *   states, through the packed head (which stays frozen):
  *     dH[n, :] = dnll[n] sum_v (exp(Y[n, v] - lse[n]) - [v = targets[n]]) W[v, :],
  *   W = W_d + A_w B_w and Y = H W^T, evaluated again from the packed head.
- *   nll, lse float N (device): what archead_nll_lse gave for the same H, head and targets.
+ *   nll, lse float N (device): what archead_nll_lse gave for the same H, head and targets, in
+ *   batches of any size.
  *   dnll float N (device): the loss's derivative by each token's NLL.  dH bf16 N x D (device,
  *   16-byte aligned, fully overwritten).
  *   A token with dnll[n] = 0 (a masked one) gets a row of zeros whatever its other inputs
  *   hold, and its target may be any value; H must be finite in every row
  *   (ARCHEAD_ERR_RANGE_H).  A target outside [0, V) of another token sets
  *   ARCHEAD_ERR_TARGET and makes its row NaN.
+ *   Precision: the softmax's entries (the target's as exp(-nll) - 1) are rounded once to FP16, times
+ *   their row's scale and a power of two per token: 11 bits, fewer below 2^-27 of the largest
+ *   entry that the token may have and none below 2^-37.  So are the left factors; sums are FP32,
+ *   dH is rounded to BF16.
  *   The tokens are taken in chunks that bound the scratch memory (about 2 GB).  Equal calls
  *   give equal bits.  Asynchronous on `stream`.
  */
@@ -182,7 +187,8 @@ int archead_nll_grad(const uint16_t* H, const archead_head* head, const int32_t*
  * archead_logits_grad -- dH = dY W: the gradient with respect to the hidden states of a loss
  *   whose gradient by the logits is dY (float N x V, device, 4-byte aligned), W as above.
  *   dH bf16 N x D (device, 16-byte aligned, fully overwritten).  A non-finite entry of dY
- *   makes its own token's row non-finite and no other.  Asynchronous on `stream`.
+ *   makes its own token's row non-finite and no other.  Precision and bits as above, with dY's
+ *   entries in place of the softmax's.  Asynchronous on `stream`.
  */
 int archead_logits_grad(const float* dY, const archead_head* head, uint16_t* dH, int64_t N,
                         int64_t V, int64_t D, int r_c, int r_r, int g, void* stream);
@@ -215,6 +221,11 @@ enum archead_reduction {
  *   Offsets that fall or leave [0, N] set ARCHEAD_ERR_SEGMENT.  Each is then clamped into
  *   [0, N]; where they still fall, dnll and stats are unspecified (nothing outside the arrays
  *   is read or written).  0 <= clip_low < 1, clip_high >= 0, kl_coef finite; B < 2^31 - 1.
+ *   A NaN log-probability or advantage makes its token's dnll NaN and the loss with it; nll_ref = +inf
+ *   has an infinite KL term, whose derivative is -1.  With kl_coef = 0 the KL term is reported
+ *   in stats[2] alone.
+ *   Differences and exponentials are FP32 (a ratio is off by |nll_old - nll| + 4 half steps), the
+ *   clip border is exact.
  *   Sums are held in FP64 and in a fixed order: equal calls give equal bits.  N = 0 writes
  *   stats alone.  Asynchronous on `stream`.
  */

@@ -5,15 +5,16 @@
 // into pieces of 256: a lane holds eight tokens of a piece, two 16-byte loads per array where the
 // arrays are aligned to it, and a warp walks the sequences that lie in its pieces (adjacent ones, so
 // that the first sequence is searched for once, 32 probes a step).  A sequence inside a piece is
-// summed by its warp, a short one among others by a lane; one that crosses pieces leaves one partial sum per piece (`tail` where it
-// starts, `head` in each later piece), which its readers add in order.  The steps are device
-// functions:
+// summed by its warp, a short one among others by a lane; one that crosses pieces leaves one partial
+// sum per piece (`tail` where it starts, `head` in each later piece), which its readers add in
+// order.  The steps are device functions:
 //  * small batches (at most 32 pieces) run them in one block, in one launch, with the sequences' sums in
 //    shared memory (7 sequences of 40 tokens: 13 us a call against 22 us for the chain, most of it
 //    the host's);
 //  * others in a chain of launches, each waiting for the one before (8192 sequences, 4.2 M tokens:
 //    policy 45 us, preference 36 us; their arrays alone take 18 and 10 us at the measured copy rate.
-//    What is left is about 90 instructions per token and the latency of the chain).
+//    Latency bounds them: one by one the launches take 14, 7, 29 and 6, and 17, 11 and 15 us, with issue
+//    slots used to 57 and 47 % at most and DRAM to 38 %).
 // Sums are FP64 in an order that the sizes alone fix, so equal calls give equal bits.  A
 // sequence's slope over the pairs that hold it arrives in any order: it is added in fixed
 // point (integer adds commute exactly).
@@ -96,7 +97,7 @@ __device__ __forceinline__ int warp_seq_of(const Seqs& q, int t) {
 // the whole warp for the tokens [lo, hi) of sequence s = [b0, b1), whose window data lane j holds.
 // Short sequences inside the piece are taken several at once, by many(s, lo, hi, b0, b1, mine): lane
 // j has sequence s + j = [b0, b1) if it is one of them (mine), and [lo, hi) are the tokens of all (6500
-// sequences of one token, preference: 144 -> 34 us; 8192 of 512 tokens 31 -> 32 us).
+// sequences of one token, preference: 144 -> 33 us; 8192 of 512 tokens 31 -> 32 us).
 template <typename W>
 struct Walker {
   const Seqs q;
