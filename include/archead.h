@@ -208,7 +208,8 @@ enum archead_reduction {
  *     r = exp(nll_old - nll),  z = nll - nll_ref,
  *     l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(z) - z - 1).
  *   nll, nll_old float N; nll_ref float N or NULL (no KL term); weights float N or NULL (all
- *   1), not negative; cu_seqlens int32 B + 1 or NULL: sequence i is the tokens
+ *   1), not negative, what they are divided by (a sum of them) between 2^-120 and 2^120 or 0;
+ *   cu_seqlens int32 B + 1 or NULL: sequence i is the tokens
  *   [cu_seqlens[i], cu_seqlens[i + 1]); advantages A float N, or float B with adv_per_seq
  *   (which needs cu_seqlens, as ARCHEAD_REDUCE_SEQUENCE does).  All on the device.
  *   dnll float N (device): the loss's derivative by each token's NLL; where the clipped side

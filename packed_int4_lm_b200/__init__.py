@@ -288,7 +288,8 @@ def _grad_out(out: Optional[torch.Tensor], N: int, dh: DeviceHead, dev, stream) 
 
 def nll_lse(H: torch.Tensor, dh: DeviceHead, targets: torch.Tensor, stream=None):
     """The per-token NLL, as nll gives it, and log-sum-exp of the logits (N float32 each):
-    what nll_grad takes."""
+    what nll_grad takes.  Every token needs a target in [0, V) here, also one that the loss masks
+    (another id makes its NLL NaN and check() reports it)."""
     _check_H(H, dh)
     N, dev = H.shape[0], H.device
     _head_on(dh, dev)
