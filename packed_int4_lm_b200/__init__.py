@@ -440,16 +440,11 @@ def dequant(dh: DeviceHead, row0: int = 0, nrows: Optional[int] = None, stream=N
     """FP32 dequantised components via the archead_dequant hook (for bit-exact checks)."""
     nrows = dh.V - row0 if nrows is None else nrows
     dev = dh.tensors["r_nib"].device
-    out = {
-        "R": torch.empty(nrows, dh.D, device=dev),
-        "Ac": torch.empty(nrows, dh.r_c, device=dev),
-        "Aw": torch.empty(nrows, dh.r_r, device=dev),
-        "Bc": torch.empty(dh.r_c, dh.D, device=dev),
-        "Bw": torch.empty(dh.r_r, dh.D, device=dev),
-    }
-    _lib.check(_lib.lib().archead_dequant(ctypes.byref(dh.struct), row0, nrows,
-                                          *[_ptr(out[k]) for k in ("R", "Ac", "Aw", "Bc", "Bw")],
-                                          _stream_handle(stream)), "archead_dequant")
+    shapes = {"R": (nrows, dh.D), "Ac": (nrows, dh.r_c), "Aw": (nrows, dh.r_r), "Bc": (dh.r_c, dh.D),
+              "Bw": (dh.r_r, dh.D)}
+    out = dict(zip(shapes, _outputs(dev, stream, lambda: [torch.empty(s, device=dev) for s in shapes.values()])))
+    _run("archead_dequant", dev, stream, (*out.values(), *dh.tensors.values()), ctypes.byref(dh.struct),
+         row0, nrows, *[_ptr(x) for x in out.values()])
     return out
 
 

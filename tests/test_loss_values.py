@@ -321,7 +321,7 @@ def test_policy_of_the_most_sequences(cuda_ok):
 
 
 @pytest.mark.parametrize("which", ["policy", "preference", "nll_lse", "nll_grad", "logits_grad", "logits", "nll",
-                                   "nll_partials", "nll_merge", "agreement"])
+                                   "nll_partials", "nll_merge", "agreement", "dequant"])
 def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, which):
     """A call on another stream while the current one still has work that writes a freed tensor of
     the outputs' size: the outputs do not lie there."""
@@ -357,7 +357,9 @@ def test_outputs_on_another_stream_are_not_the_current_streams_memory(cuda_ok, w
             return [ah.nll_partials(H, dh, t2[:, 0], 0, head["V"], stream=stream)]
         if which == "nll_merge":
             return [ah.nll_merge(part[None], stream=stream)]
-        return list(ah.agreement(H, dh, dY, stream=stream).values())
+        if which == "agreement":
+            return list(ah.agreement(H, dh, dY, stream=stream).values())
+        return list(ah.dequant(dh, 128, 500, stream=stream).values())
 
     want = [o.clone() for o in call()]
     call(side)
